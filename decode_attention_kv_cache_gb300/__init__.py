@@ -41,11 +41,17 @@ class kvc_cache(ctypes.Structure):
                 ("v_q", ctypes.c_void_p), ("v_s", ctypes.c_void_p)]
 
 
+class kvc_pages(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("n_seq", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libkvc.so is not built; run `python -m decode_attention_kv_cache_gb300.build`")
     L = ctypes.CDLL(LIB_PATH)
     P, I32, SZ, VP = ctypes.POINTER, ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
+    I64 = ctypes.c_int64
     sig = {
         "kvc_cache_bytes": (ctypes.c_int, [P(kvc_desc), P(SZ), P(SZ), P(SZ), P(SZ)]),
         "kvc_scratch_bytes": (ctypes.c_int, [P(kvc_desc), I32, P(SZ)]),
@@ -68,6 +74,13 @@ def _load():
         "kv_cache_append_batch": (ctypes.c_int, [P(kvc_cache), I32, I32, P(I32), VP, VP, I32, VP]),
         "kv_state_get_heads": (ctypes.c_int, [P(kvc_cache), I32, I32, I32, VP, SZ, VP]),
         "kv_state_set_heads": (ctypes.c_int, [P(kvc_cache), I32, VP, SZ, P(I32), VP]),
+        "kv_paged_append": (ctypes.c_int, [P(kvc_cache), P(kvc_pages), I32, VP, I32, VP, VP, I64, I64, I32, VP]),
+        "kv_paged_read": (ctypes.c_int, [P(kvc_cache), P(kvc_pages), I32, VP, I32, VP, VP, I32, VP]),
+        "kvc_paged_scratch_bytes": (ctypes.c_int, [P(kvc_desc), I32, I32, P(SZ)]),
+        "decode_attn_paged": (ctypes.c_int, [P(kvc_cache), P(kvc_pages), I32, VP, I64, I32, I32, VP, VP, VP, SZ, VP]),
+        "kvc_packed_scratch_bytes": (ctypes.c_int, [I32, I32, I32, I32, I32, P(SZ)]),
+        "attn_packed": (ctypes.c_int, [VP, VP, VP, I64, I64, I64, I32, VP, VP, I32, I32, I32, I32, I32, I32, VP, VP,
+                                       VP, SZ, VP]),
         "kvc_test_arm_wait_timeout": (ctypes.c_int, [I32, ctypes.c_uint64]),
     }
     for name, (res, args) in sig.items():
@@ -376,6 +389,150 @@ def kv_cache_truncate(cache, n_tokens, stream=None):
     """Rewind `cache` to its first n_tokens positions (later positions cleared to zero bytes)."""
     _check(_lib().kv_cache_truncate(ctypes.byref(cache.c), int(n_tokens), _stream(stream, cache.device)),
            "kv_cache_truncate")
+
+
+class PageTable:
+    """The pages of n_seq sequences in a pool (a KVCache whose positions are cut into pages).
+
+    table: int32 [n_seq][max_pages], lengths: int32 [n_seq], contiguous tensors on the pool's device.  They are
+    read when a kernel runs, so both may be updated in place between calls (and between replays of a graph).
+    An entry outside the pool, such as -1, is a hole.
+    """
+
+    def __init__(self, table, lengths, page_size):
+        _need(table, "table", torch.int32); _need(lengths, "lengths", torch.int32)
+        if table.dim() != 2 or lengths.shape != table.shape[:1] or lengths.device != table.device:
+            raise ValueError("table must be [n_seq][max_pages] and lengths [n_seq], on one device")
+        self.table, self.lengths, self.page_size = table, lengths, int(page_size)
+        self.n_seq, self.device = table.shape[0], table.device
+        self.c = kvc_pages(table.data_ptr(), lengths.data_ptr(), table.shape[0], table.shape[1], self.page_size)
+        self.ref = ctypes.byref(self.c)
+
+
+def _on(device):
+    """The raw current stream of `device`, which has to be the current device for the launches that follow."""
+    if torch.cuda.current_device() != device.index:
+        raise ValueError("the tensors are on %s, which is not the current device" % device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _packed_rows(t, what, heads, head_dim, dtype, device):
+    """Distance between tokens (elements) of a [rows][heads][head_dim] tensor with contiguous heads."""
+    if t.device != device or t.dtype != dtype or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError("%s must be a %s tensor [rows][%d][%d] on %s" % (what, dtype, heads, head_dim, device))
+    ld, hs, es = t.stride()
+    if es != 1 or (hs != head_dim and heads != 1):
+        raise ValueError("%s must have contiguous heads" % what)
+    return ld if t.shape[0] > 1 else heads * head_dim
+
+
+def _starts(t, what, n_seq, device):
+    if t.dtype != torch.int32 or t.device != device or t.shape != (n_seq + 1,) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor [n_seq + 1] on %s" % (what, device))
+    return t.data_ptr()
+
+
+def _output(t, what, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor %s on %s" % (what, dtype, list(shape), device))
+    return t
+
+
+def kv_paged_append(cache, layer, pages, row_start, k, v, stream=None):
+    """Store packed rows k, v [n_rows][H_kv][D]: rows [row_start[i], row_start[i + 1]) are the last positions of
+    sequence i (pages.lengths counts them), quantised or rounded as kv_cache_append does."""
+    dev, n = pages.device, k.shape[0]
+    ld_k = _packed_rows(k, "k", cache.n_head_kv, cache.head_dim, k.dtype, dev)
+    ld_v = _packed_rows(v, "v", cache.n_head_kv, cache.head_dim, k.dtype, dev)
+    if v.shape[0] != n or k.dtype not in DTYPES or cache.device.type != "cuda":
+        raise ValueError("k and v must have the same rows and be f32, bf16 or f16")
+    st = _lib().kv_paged_append(ctypes.byref(cache.c), pages.ref, layer, _starts(row_start, "row_start", pages.n_seq, dev),
+                                n, k.data_ptr(), v.data_ptr(), ld_k, ld_v, DTYPES[k.dtype],
+                                _on(dev) if stream is None else stream.cuda_stream)
+    _check(st, "kv_paged_append")
+
+
+def kv_paged_read(cache, layer, pages, row_start, n_rows, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """The values the pool holds for packed rows (as in kv_paged_append): k, v [n_rows][H_kv][D] in dtype."""
+    dev = pages.device
+    if dtype not in DTYPES:
+        raise ValueError("dtype must be f32, bf16 or f16")
+    shape = (n_rows, cache.n_head_kv, cache.head_dim)
+    k, v = _output(k, "k", shape, dtype, dev), _output(v, "v", shape, dtype, dev)
+    st = _lib().kv_paged_read(ctypes.byref(cache.c), pages.ref, layer, _starts(row_start, "row_start", pages.n_seq, dev),
+                              n_rows, k.data_ptr(), v.data_ptr(), DTYPES[dtype],
+                              _on(dev) if stream is None else stream.cuda_stream)
+    _check(st, "kv_paged_read")
+    return k, v
+
+
+def paged_scratch(cache, n_seq, n_head_q):
+    """A scratch buffer for decode_attn_paged (needs no initialisation)."""
+    n = ctypes.c_size_t()
+    _check(_lib().kvc_paged_scratch_bytes(ctypes.byref(cache.desc), n_seq, n_head_q, ctypes.byref(n)),
+           "kvc_paged_scratch_bytes")
+    return torch.empty(max(n.value, 16), dtype=torch.uint8, device=cache.device)
+
+
+def decode_attn_paged(cache, layer, pages, q, out=None, lse=None, scratch=None, stream=None):
+    """Attention of one token q[i] [H_q][D] of each sequence over its pages.lengths[i] keys; returns out
+    [n_seq][H_q][D] in q's type.  lse: None, or a float32 tensor [n_seq][H_q] to fill."""
+    dev, n = pages.device, pages.n_seq
+    if q.dim() != 3 or q.shape[0] != n or q.dtype not in DTYPES:
+        raise ValueError("q must be an f32, bf16 or f16 tensor [n_seq][H_q][D]")
+    hq = q.shape[1]
+    ld = _packed_rows(q, "q", hq, cache.head_dim, q.dtype, dev)
+    out = _output(out, "out", (n, hq, cache.head_dim), q.dtype, dev)
+    if lse is not None:
+        lse = _output(lse, "lse", (n, hq), torch.float32, dev)
+    if scratch is None:
+        scratch = paged_scratch(cache, n, hq)
+    _need(scratch, "scratch")
+    st = _lib().decode_attn_paged(ctypes.byref(cache.c), pages.ref, layer, q.data_ptr(), ld, DTYPES[q.dtype], hq,
+                                  out.data_ptr(), None if lse is None else lse.data_ptr(), scratch.data_ptr(),
+                                  scratch.numel() * scratch.element_size(),
+                                  _on(dev) if stream is None else stream.cuda_stream)
+    _check(st, "decode_attn_paged")
+    return out
+
+
+def packed_scratch(n_rows, n_seq, n_head_q, n_head_kv, head_dim, device="cuda"):
+    """A scratch buffer for attn_packed calls of up to n_rows query rows and n_seq sequences."""
+    n = ctypes.c_size_t()
+    _check(_lib().kvc_packed_scratch_bytes(n_rows, n_seq, n_head_q, n_head_kv, head_dim, ctypes.byref(n)),
+           "kvc_packed_scratch_bytes")
+    return torch.empty(max(n.value, 16), dtype=torch.uint8, device=device)
+
+
+def attn_packed(q, k, v, q_start, k_start=None, out=None, lse=None, scratch=None, stream=None):
+    """Causal attention of packed prompts: q [n_q][H_q][D], k and v [n_k][H_kv][D] (bf16 or f16); sequence s has
+    query rows [q_start[s], q_start[s + 1]) and keys [k_start[s], k_start[s + 1]) (q_start when None), its queries
+    being its last positions.  Returns out like q, contiguous.  lse: None, or a float32 [n_q][H_q] to fill."""
+    dev = q.device
+    if q.dim() != 3 or k.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q, k and v must be bf16 or f16 tensors [rows][heads][D]")
+    (n_q, hq, d), (n_k, hkv, _) = q.shape, k.shape
+    n_seq = q_start.shape[0] - 1
+    ld_q = _packed_rows(q, "q", hq, d, q.dtype, dev)
+    ld_k, ld_v = _packed_rows(k, "k", hkv, d, q.dtype, dev), _packed_rows(v, "v", hkv, d, q.dtype, dev)
+    if v.shape != k.shape or not q.is_cuda:
+        raise ValueError("k and v must have the same rows, on a CUDA device")
+    qs = _starts(q_start, "q_start", n_seq, dev)
+    ks = qs if k_start is None else _starts(k_start, "k_start", n_seq, dev)
+    out = _output(out, "out", (n_q, hq, d), q.dtype, dev)
+    if lse is not None:
+        lse = _output(lse, "lse", (n_q, hq), torch.float32, dev)
+    if scratch is None:
+        scratch = packed_scratch(n_q, n_seq, hq, hkv, d, dev)
+    _need(scratch, "scratch")
+    st = _lib().attn_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), ld_q, ld_k, ld_v, DTYPES[q.dtype], qs, ks, n_seq,
+                            n_q, n_k, hq, hkv, d, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                            scratch.data_ptr(), scratch.numel() * scratch.element_size(),
+                            _on(dev) if stream is None else stream.cuda_stream)
+    _check(st, "attn_packed")
+    return out
 
 
 def kvc_device_status():

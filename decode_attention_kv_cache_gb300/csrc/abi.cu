@@ -67,6 +67,16 @@ size_t record_bytes(const kvc_desc &d) {
                               : (size_t)d.n_head_kv * d.head_dim * 2;
 }
 
+bool pages_ok(const kvc_cache *c, const kvc_pages *p) {
+    return p && p->n_seq >= 0 && p->n_seq <= 65535 && p->max_pages > 0 && p->page_size > 0 && p->page_size % 16 == 0 &&
+           c->d.n_ctx % p->page_size == 0 && (int64_t)p->max_pages * p->page_size <= INT32_MAX;
+}
+
+// whether ld is a distance between tokens of `heads` heads of the type: no overlap, 16-byte rows
+bool ld_ok(int64_t ld, int64_t heads, int64_t head_dim, int dtype) {
+    return ld >= heads * head_dim && ld * dtype_bytes(dtype) % 16 == 0 && ld < ((int64_t)1 << 38);
+}
+
 bool dtype_ok(int dtype) { return dtype == KVC_IN_F32 || dtype == KVC_IN_BF16 || dtype == KVC_IN_F16; }
 
 }  // namespace
@@ -334,6 +344,81 @@ int kv_state_set_heads(kvc_cache *cache, int32_t head0, const void *src, size_t 
     const int rc = launch_state_unpack_heads(*cache, head0, (int)h[3], n, static_cast<const uint8_t *>(src), s);
     if (rc == KVC_OK) *n_tokens_out = n;
     return rc;
+}
+
+int kv_paged_append(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const int32_t *row_start,
+                    int32_t n_rows, const void *k, const void *v, int64_t ld_k, int64_t ld_v, int32_t dtype,
+                    kvc_stream_t stream) {
+    if (!cache_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype) || n_rows < 0) return KVC_EINVAL;
+    if (!ld_ok(ld_k, pool->d.n_head_kv, pool->d.head_dim, dtype) ||
+        !ld_ok(ld_v, pool->d.n_head_kv, pool->d.head_dim, dtype))
+        return KVC_EINVAL;
+    if (layer < 0 || layer >= pool->d.n_layer) return KVC_ERANGE;
+    if (n_rows == 0 || pages->n_seq == 0) return KVC_OK;
+    if (!pages->table || !pages->len || !row_start || !k || !v || !aligned16(k) || !aligned16(v)) return KVC_EINVAL;
+    return launch_paged_append(*pool, *pages, layer, row_start, n_rows, k, v, ld_k, ld_v, dtype, (cudaStream_t)stream);
+}
+
+int kv_paged_read(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const int32_t *row_start,
+                  int32_t n_rows, void *k, void *v, int32_t dtype, kvc_stream_t stream) {
+    if (!cache_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype) || n_rows < 0) return KVC_EINVAL;
+    if (layer < 0 || layer >= pool->d.n_layer) return KVC_ERANGE;
+    if (n_rows == 0 || pages->n_seq == 0) return KVC_OK;
+    if (!pages->table || !pages->len || !row_start || !k || !v || !aligned16(k) || !aligned16(v)) return KVC_EINVAL;
+    return launch_paged_read(*pool, *pages, layer, row_start, n_rows, k, v, dtype, (cudaStream_t)stream);
+}
+
+int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_q, size_t *bytes) {
+    if (!desc_ok(desc) || !bytes || n_seq < 0 || n_seq > 65535) return KVC_EINVAL;
+    if (desc->head_dim != 64 && desc->head_dim != 128) return KVC_EINVAL;
+    if (n_head_q <= 0 || n_head_q % desc->n_head_kv || n_head_q / desc->n_head_kv > 16) return KVC_EINVAL;
+    *bytes = paged_scratch_bytes(*desc, n_seq, n_head_q);
+    return KVC_OK;
+}
+
+int decode_attn_paged(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const void *q, int64_t ld_q,
+                      int32_t dtype, int32_t n_head_q, void *out, float *lse, void *scratch, size_t scratch_bytes,
+                      kvc_stream_t stream) {
+    if (!cache_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype)) return KVC_EINVAL;
+    size_t need = 0;
+    if (kvc_paged_scratch_bytes(&pool->d, pages->n_seq, n_head_q, &need) != KVC_OK) return KVC_EINVAL;
+    if (!ld_ok(ld_q, n_head_q, pool->d.head_dim, dtype)) return KVC_EINVAL;
+    if (layer < 0 || layer >= pool->d.n_layer) return KVC_ERANGE;
+    if (pages->n_seq == 0) return KVC_OK;
+    if (!pages->table || !pages->len || !q || !out || !scratch || !aligned16(q) || !aligned16(out) ||
+        !aligned16(scratch))
+        return KVC_EINVAL;
+    if (scratch_bytes < need) return KVC_ENOSPC;
+    return launch_decode_paged(*pool, *pages, layer, q, ld_q, dtype, n_head_q, out, lse, scratch, (cudaStream_t)stream);
+}
+
+int kvc_packed_scratch_bytes(int32_t n_rows, int32_t n_seq, int32_t n_head_q, int32_t n_head_kv, int32_t head_dim,
+                             size_t *bytes) {
+    if (!bytes || n_rows < 0 || n_seq < 0 || n_seq > 65535 || (head_dim != 64 && head_dim != 128)) return KVC_EINVAL;
+    if (n_head_q <= 0 || n_head_kv <= 0 || n_head_q > 65535 || n_head_q % n_head_kv || n_head_q / n_head_kv > 128)
+        return KVC_EINVAL;
+    *bytes = packed_scratch_bytes(n_rows, n_seq, n_head_q, n_head_kv, head_dim);
+    return KVC_OK;
+}
+
+int attn_packed(const void *q, const void *k, const void *v, int64_t ld_q, int64_t ld_k, int64_t ld_v, int32_t dtype,
+                const int32_t *q_start, const int32_t *k_start, int32_t n_seq, int32_t n_q, int32_t n_k,
+                int32_t n_head_q, int32_t n_head_kv, int32_t head_dim, void *out, float *lse, void *scratch,
+                size_t scratch_bytes, kvc_stream_t stream) {
+    size_t need = 0;
+    if (n_k < 0 || (dtype != KVC_IN_BF16 && dtype != KVC_IN_F16)) return KVC_EINVAL;
+    if (kvc_packed_scratch_bytes(n_q, n_seq, n_head_q, n_head_kv, head_dim, &need) != KVC_OK) return KVC_EINVAL;
+    if (!ld_ok(ld_q, n_head_q, head_dim, dtype) || !ld_ok(ld_k, n_head_kv, head_dim, dtype) ||
+        !ld_ok(ld_v, n_head_kv, head_dim, dtype))
+        return KVC_EINVAL;
+    if (n_q == 0 || n_seq == 0) return KVC_OK;
+    if (!q || !out || !scratch || !q_start || !k_start || !aligned16(q) || !aligned16(out) || !aligned16(scratch))
+        return KVC_EINVAL;
+    if (n_k > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return KVC_EINVAL;
+    if (scratch_bytes < need) return KVC_ENOSPC;
+    const PackedArgs a = {q, k, v, ld_q, ld_k, ld_v, q_start, k_start, n_seq, n_q, n_k, n_head_q, n_head_kv,
+                          head_dim, dtype, out, lse};
+    return launch_packed(a, scratch, (cudaStream_t)stream);
 }
 
 int kv_cache_truncate(const kvc_cache *cache, int32_t n_tokens, kvc_stream_t stream) {

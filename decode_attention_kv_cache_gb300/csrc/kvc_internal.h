@@ -76,6 +76,32 @@ int launch_state_pack_heads(const kvc_cache &c, int head0, int H_total, int n_to
 int launch_state_unpack_heads(const kvc_cache &c, int head0, int H_total, int n_tokens, const uint8_t *src,
                               cudaStream_t s);
 
+// Paged pools and packed prompts.  PagedView: what the kernels need of a pool's pages.
+struct PagedView {
+    const int32_t *table, *len;
+    int n_seq, max_pages, page_size, n_pages;
+};
+inline PagedView paged_view(const kvc_cache &c, const kvc_pages &p) {
+    return {p.table, p.len, p.n_seq, p.max_pages, p.page_size, c.d.n_ctx / p.page_size};
+}
+int launch_paged_append(const kvc_cache &c, const kvc_pages &p, int layer, const int32_t *row_start, int n_rows,
+                        const void *k, const void *v, int64_t ld_k, int64_t ld_v, int dtype, cudaStream_t s);
+int launch_paged_read(const kvc_cache &c, const kvc_pages &p, int layer, const int32_t *row_start, int n_rows, void *k,
+                      void *v, int dtype, cudaStream_t s);
+size_t paged_scratch_bytes(const kvc_desc &d, int n_seq, int n_head_q);
+int launch_decode_paged(const kvc_cache &c, const kvc_pages &p, int layer, const void *q, int64_t ld_q, int dtype,
+                        int n_head_q, void *out, float *lse, void *scratch, cudaStream_t s);
+struct PackedArgs {
+    const void *q, *k, *v;
+    int64_t ld_q, ld_k, ld_v;
+    const int32_t *q_start, *k_start;
+    int n_seq, n_q, n_k, H_q, H_kv, D, dtype;
+    void *out;
+    float *lse;
+};
+size_t packed_scratch_bytes(int n_rows, int n_seq, int n_head_q, int n_head_kv, int head_dim);
+int launch_packed(const PackedArgs &a, void *scratch, cudaStream_t s);
+
 // Test hook of the failure path: the wait limit (ns) of a stall armed for the next launch of a kernel
 // kind (KVC_TEST_PREFILL / KVC_TEST_DECODE), 0 when none; take_ consumes it.
 void arm_test_stall(int which, uint64_t limit_ns);

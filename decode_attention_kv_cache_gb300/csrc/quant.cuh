@@ -44,27 +44,21 @@ __device__ __forceinline__ void load_inputs8(const void *base, int64_t idx, floa
     }
 }
 
-// Quantise x[0..31]: the 32 codes packed four to a word (byte i of word w is code 4 w + i) and the
-// fp16 bits of the scale.
-__device__ __forceinline__ uint16_t q8_0_quantize32(const float (&x)[32], uint32_t (&packed)[8]) {
-    float m2[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        m2[0] = ptx::fmax3(m2[0], fabsf(x[i]), fabsf(x[i + 1]));
-        m2[1] = ptx::fmax3(m2[1], fabsf(x[i + 2]), fabsf(x[i + 3]));
-    }
-    const float amax = fmaxf(m2[0], m2[1]);
+// The codes of N values of a block whose largest magnitude is amax, packed four to a word (byte i of word w
+// is code 4 w + i); returns the fp16 bits of the block's scale.
+template <int N>
+__device__ __forceinline__ uint16_t q8_0_codes(const float (&x)[N], float amax, uint32_t (&packed)[N / 4]) {
     const float d = __fdiv_rn(amax, 127.0f);
 #pragma unroll
-    for (int w = 0; w < 8; ++w) packed[w] = 0u;
+    for (int w = 0; w < N / 4; ++w) packed[w] = 0u;
     // codes are zero when amax/127 is zero (x/d undefined); |x * r| <= 127 (to an ulp) otherwise
     if (d > 0.f && amax <= 3.402823466e38f) {
         const float r = __frcp_rn(d);
         const uint64_t r2 = ptx::f2_pack(r, r), mz = ptx::f2_pack(-0.f, -0.f), M2 = ptx::f2_pack(12582912.f, 12582912.f),
                        nM2 = ptx::f2_pack(-12582912.f, -12582912.f), n1 = ptx::f2_pack(-1.f, -1.f);
-        int q[32];
+        int q[N];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
+        for (int i = 0; i < N; i += 2) {
             const uint64_t y = ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), r2, mz);   // x * r, one rounding
             const uint64_t t = ptx::f2_add(y, M2);                                // y rounded to an integer (to even)
             const uint64_t f = ptx::f2_fma(ptx::f2_add(t, nM2), n1, y);              // y minus that integer
@@ -79,11 +73,34 @@ __device__ __forceinline__ uint16_t q8_0_quantize32(const float (&x)[32], uint32
             }
         }
 #pragma unroll
-        for (int w = 0; w < 8; ++w)
+        for (int w = 0; w < N / 4; ++w)
             packed[w] = __byte_perm(__byte_perm(q[4 * w], q[4 * w + 1], 0x0040),
                                     __byte_perm(q[4 * w + 2], q[4 * w + 3], 0x0040), 0x5410);
     }
     return __half_as_ushort(__float2half_rn(d));
+}
+
+// Quantise x[0..31]: the 32 codes packed four to a word and the fp16 bits of the scale.
+__device__ __forceinline__ uint16_t q8_0_quantize32(const float (&x)[32], uint32_t (&packed)[8]) {
+    float m2[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        m2[0] = ptx::fmax3(m2[0], fabsf(x[i]), fabsf(x[i + 1]));
+        m2[1] = ptx::fmax3(m2[1], fabsf(x[i + 2]), fabsf(x[i + 3]));
+    }
+    return q8_0_codes<32>(x, fmaxf(m2[0], m2[1]), packed);
+}
+
+// A block spread over four neighbouring lanes, eight values each: this lane's codes and the block's scale.
+// All four lanes take part.
+__device__ __forceinline__ uint16_t q8_0_quantize_quad(const float (&x)[8], uint32_t (&packed)[2]) {
+    float m = ptx::fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2]));
+    m = ptx::fmax3(m, fabsf(x[3]), fabsf(x[4]));
+    m = ptx::fmax3(m, fabsf(x[5]), fabsf(x[6]));
+    m = fmaxf(m, fabsf(x[7]));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return q8_0_codes<8>(x, m, packed);
 }
 
 }  // namespace kvc

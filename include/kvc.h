@@ -377,6 +377,112 @@ int kv_state_set_heads(kvc_cache *cache, int32_t head0, const void *src, size_t 
  * KVC_ECUDA. */
 int kv_cache_truncate(const kvc_cache *cache, int32_t n_tokens, kvc_stream_t stream);
 
+/* ---- paged caches and packed prompts --------------------------------------------
+ *
+ * Serving many sequences from one pool.  The pool is an ordinary kvc_cache (its
+ * type and layout as above); its n_ctx positions are cut into pages of
+ * page_size positions, page p covering pool positions [p * page_size, (p + 1) *
+ * page_size) of every layer.  A kvc_pages gives each sequence its pages, in
+ * order, and its length:
+ *   position j of sequence i is pool position
+ *       table[i * max_pages + j / page_size] * page_size + j % page_size.
+ * table and len are DEVICE arrays, read when the kernels run, so a captured
+ * CUDA graph may be replayed with new lengths and pages.  Because they cannot be
+ * checked on the host, every value is defined: a table entry outside [0, n_ctx /
+ * page_size) and a position at or past max_pages * page_size is a hole - nothing
+ * is stored there, it reads as zero and attention gives it no weight (so the
+ * pages a sequence has let go may be marked -1) - and a negative length is zero.
+ * Several sequences may share pages that are only read.  Rows that one call
+ * stores to the same pool position race: the position then holds either.
+ *
+ * Packed rows.  Rows of several sequences lie one after another in one tensor;
+ * row_start (device, [n_seq + 1], not decreasing) gives each sequence's rows,
+ * [row_start[i], row_start[i + 1]), which belong to the LAST row_start[i + 1] -
+ * row_start[i] of its len[i] positions: one row per sequence in a decode step,
+ * len[i] rows for a whole prompt, a chunk's rows otherwise.  A sequence may have
+ * none.  Rows that would fall before position 0 belong to no position.  Rows
+ * outside [row_start[0], row_start[n_seq]), such as padding behind the last
+ * sequence, are neither read nor written.  n_rows is the number of rows of the
+ * tensors; no row at or past it is touched, whatever row_start says.
+ * Packed tensors are token-major with contiguous heads; ld_* is the distance
+ * between tokens in elements (at least heads * head_dim, a multiple of 16 bytes),
+ * so parts of a fused projection are read in place.
+ *
+ * These calls are launched as programmatic dependents, as above, and may be
+ * captured.  n_seq == 0 or n_rows == 0 is a no-op. */
+typedef struct {
+    const int32_t *table; /* device [n_seq][max_pages] */
+    const int32_t *len;   /* device [n_seq] */
+    int32_t n_seq;        /* 0 .. 65535 */
+    int32_t max_pages;    /* entries of each sequence's table row; max_pages * page_size < 2^31 */
+    int32_t page_size;    /* a multiple of 16 that divides the pool's n_ctx */
+} kvc_pages;
+
+/* Store packed rows of k and v ([n_rows][n_head_kv][head_dim] in `dtype`) at
+ * their positions in `layer` of the pool, quantised or rounded exactly as
+ * kv_cache_append does (the same bytes).  Rows of holes are dropped.
+ * Errors: KVC_EINVAL (null or unaligned pointers, dtype, ld, page_size, n_seq or
+ * max_pages out of bounds), KVC_ERANGE (layer). */
+int kv_paged_append(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const int32_t *row_start,
+                    int32_t n_rows, const void *k, const void *v, int64_t ld_k, int64_t ld_v, int32_t dtype,
+                    kvc_stream_t stream);
+
+/* The reverse: write the values the pool holds for the packed rows' positions to
+ * k and v, [n_rows][n_head_kv][head_dim] contiguous in `dtype` (d * q, or the
+ * fp16 value, rounded once to nearest even).  Holes and rows before position 0
+ * read as zero.  With row_start from the lengths themselves this unpacks whole
+ * sequences, in the form attn_packed takes.  Errors as kv_paged_append. */
+int kv_paged_read(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const int32_t *row_start,
+                  int32_t n_rows, void *k, void *v, int32_t dtype, kvc_stream_t stream);
+
+/* Bytes of the scratch buffer decode_attn_paged needs on the current device (no
+ * initialisation; calls on one scratch must not overlap on the GPU). */
+int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_q, size_t *bytes);
+
+/* Single-token attention of each sequence over its pages:
+ *   out[i][h] = sum_{j < len[i]} softmax_j(q[i][h] . khat[j][h/G] / sqrt(head_dim)) vhat[j][h/G]
+ * with khat, vhat the values `layer` of the pool holds for sequence i; the new
+ * token's own K/V must have been stored.  q: [n_seq][n_head_q][head_dim] in
+ * `dtype`, ld_q elements between tokens; out: the same shape, contiguous, in
+ * `dtype`; lse: null, or [n_seq][n_head_q] float32 that receives the natural
+ * logarithm of the sum of exponentials (to join the result with attention over
+ * other keys).  A sequence without keys (len 0, or holes only) gives out 0 and
+ * lse -infinity.  Values the pool holds outside the sequences' positions are
+ * never used, whatever they are.  Any number of sequences and lengths share the
+ * GPU evenly: the keys of all of them are cut into equal shares.
+ * Computed as decode_attn (fp16 products of q and the values, float32
+ * accumulation and softmax), then rounded once to `dtype`.  head_dim 64 or 128, n_head_q /
+ * n_head_kv <= 16.  Errors as kv_paged_append, KVC_ENOSPC (scratch too small). */
+int decode_attn_paged(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const void *q, int64_t ld_q,
+                      int32_t dtype, int32_t n_head_q, void *out, float *lse, void *scratch, size_t scratch_bytes,
+                      kvc_stream_t stream);
+
+/* Bytes of the scratch buffer attn_packed needs on the current device (no
+ * initialisation; calls on one scratch must not overlap on the GPU). */
+int kvc_packed_scratch_bytes(int32_t n_rows, int32_t n_seq, int32_t n_head_q, int32_t n_head_kv, int32_t head_dim,
+                             size_t *bytes);
+
+/* Causal attention of packed prompts over packed keys and values.  Sequence s
+ * has query rows [q_start[s], q_start[s + 1]) of q and keys [k_start[s],
+ * k_start[s + 1]) of k and v (device arrays, [n_seq + 1]; they may be the same
+ * array); the queries are its last positions, so with nq rows and nk keys row i
+ * sees the keys j <= i + nk - nq:
+ *   out[i][h] = sum_j softmax_j(q[i][h] . k[j][h/G] / sqrt(head_dim)) v[j][h/G].
+ * A row that sees no key (nk < nq) gives out 0 and lse -infinity.  q: [n_q]
+ * [n_head_q][head_dim], k and v: [n_k][n_head_kv][head_dim], all bf16 or all f16
+ * (`dtype`), ld_* elements between tokens; out: [n_q][n_head_q][head_dim]
+ * contiguous in `dtype`; lse: null or [n_q][n_head_q] float32, the natural
+ * logarithm of the sum of exponentials.  Values must be finite within a
+ * sequence; what lies outside its rows is never used.  Tensor-core products in
+ * the inputs' type, float32 accumulation and softmax; the softmax numerators
+ * enter the second product rounded to `dtype`.  head_dim 64 or 128, n_head_q /
+ * n_head_kv <= 128.  Errors: KVC_EINVAL (null or unaligned pointers, dtype f32,
+ * shapes, ld), KVC_ENOSPC (scratch too small). */
+int attn_packed(const void *q, const void *k, const void *v, int64_t ld_q, int64_t ld_k, int64_t ld_v, int32_t dtype,
+                const int32_t *q_start, const int32_t *k_start, int32_t n_seq, int32_t n_q, int32_t n_k,
+                int32_t n_head_q, int32_t n_head_kv, int32_t head_dim, void *out, float *lse, void *scratch,
+                size_t scratch_bytes, kvc_stream_t stream);
+
 /* ---- diagnostics ------------------------------------------------------------- */
 
 /* A short static description of a status code. */
