@@ -1,10 +1,31 @@
-// Attention of one new token for each sequence over a paged pool: the plain form of the kernel.
+// Attention of one new token for each sequence over a paged pool.
 //
 //   out[i][h] = sum_{j < len[i]} softmax_j(q[i][h] . khat[j][h/G] / sqrt(D)) vhat[j][h/G]
 //
-// One CTA per (sequence, query head).  Its four warps take every fourth key; a lane holds D/32 dimensions.
-// Each warp keeps a running maximum and sum of its keys in float32 (one pass over the data), and the four are
-// joined in shared memory.
+// What bounds it: every key and value is read once and used for the G query heads of its group, so the floor
+// is the pool's bytes over the HBM rate (a few operations per byte; q8_0 also has to turn each code into fp16).
+//
+// Work split.  The keys of all (sequence, kv head) pairs, in tiles of 64, form one list that is cut into
+// equal runs, one for each CTA (two per SM), wherever the boundaries fall: ragged lengths, one long sequence
+// and many short ones all fill the GPU.  The lengths are read on the device.  A pair inside one run is written
+// straight to out; a pair cut by run boundaries leaves one partial (O, maximum, sum) per run in scratch - at
+// most two per CTA - and a second kernel joins them in run order.
+//
+// One CTA: a producer warp looks up the pages and keeps a ring of tiles in flight by TMA (one box per page piece,
+// swizzled so that both products read them without bank conflicts, scales by 8-byte asynchronous copies); four
+// consumer warps take 16 keys of each tile, one subtile each, which always lies within one page.  A warp keeps its own
+// running maximum (raised only when a score passes it by 2^8, so that the accumulators are seldom rescaled) and
+// sum, and the four are joined when a pair ends.  Both products run on warp-level matrix instructions with
+// the keys (S^T = K Q^T) and the value dimensions (O^T = V^T P^T) as the 16-row side, so that a group of up
+// to 8 query heads wastes nothing but padding columns:
+//   - the order of dimensions in the first product and of keys in both is free as long as the operands agree,
+//     so each lane loads 8 or 16 consecutive bytes of a row, and codes need no shuffles between lanes;
+//   - q8_0 codes enter the first product as the integers they are; each block's products are scaled by d in
+//     float32.  In the second product the values are fp16(d * q) and the numerators p are rounded to fp16;
+//   - S^T leaves the first product with a lane per key and enters the second with a lane per head: one 8x8
+//     transposition for each half of the subtile.
+// Keys past the length and pages outside the pool are never loaded, or are given zero weight and zeroed values.
+// Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -13,136 +34,757 @@
 #include "ptx.cuh"
 
 namespace kvc {
+
+// set by a kernel of this file that gave up a bounded wait (read and cleared with the other kernels' status)
+__device__ int g_paged_status;
+
 namespace {
 
-struct Args {
-    const void *kq, *vq;
-    const uint16_t *ks, *vs;
-    Geom g;
-    int layer, H_q, G;
-    const void *q;
-    int64_t ld_q;
-    void *out;
-    float *lse;
-    float scale;
+using namespace ptx;
+
+constexpr int KT = 64;              // keys per tile
+constexpr int CW = 4;               // consumer warps, 16 keys of a tile each
+constexpr int THREADS = 32 * (CW + 1);
+constexpr int CTAS_PER_SM = 2;
+constexpr int SMEM_BUDGET = 115712;  // 113 KB: two CTAs per SM
+constexpr int COMBINE_THREADS = 256;
+constexpr float RESCALE_LOG2 = 8.0f;
+constexpr float LN2 = 0.69314718055994531f;
+
+template <int D, bool Q8, int DT, int NT>
+struct Cfg {
+    static constexpr int NB = D / 32;                       // q8_0 blocks per row
+    static constexpr int ROW = D * (Q8 ? 1 : 2);            // bytes of a row
+    static constexpr int TILE = KT * ROW;                   // a K or V tile
+    static constexpr int SC = Q8 ? KT * NB * 2 : 0;         // a tile's scales
+    static constexpr int STAGE = 2 * TILE + ((2 * SC + 1023) & ~1023);
+    static constexpr int MT = D / 16;                       // 16-row tiles of O^T
+    static constexpr int OWN = MT / CW;                     // of which each warp writes
+    static constexpr int RED = MT * NT * (CW - 1) * 512;    // the other warps' accumulators
+    static constexpr int ESZ = DT == KVC_IN_F32 ? 4 : 2;
+    static constexpr int QB = 8 * NT * D * ESZ;
+    static constexpr int MISC = 1024;
+    static constexpr int FIT = (SMEM_BUDGET - 1024 - RED - QB - MISC) / STAGE;
+    static constexpr int NS = FIT < 12 ? FIT : 12;
+    static constexpr int OFF_RED = NS * STAGE, OFF_Q = OFF_RED + RED, OFF_MISC = OFF_Q + QB;
+    static constexpr int ALLOC = OFF_MISC + MISC + 1024;
+    static_assert(NS >= 2 && ALLOC <= SMEM_BUDGET, "shared memory plan");
 };
 
-template <int DT>
-__device__ __forceinline__ float load1(const void *p, int64_t i) {
-    if constexpr (DT == KVC_IN_F32) return static_cast<const float *>(p)[i];
-    else if constexpr (DT == KVC_IN_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-    else return __half2float(static_cast<const __half *>(p)[i]);
+// what the small area behind the ring holds
+struct Misc {
+    uint64_t full[12], empty[12], q_full, q_empty;
+    int count[12][CW];                   // keys of each subtile that exist
+    float2 ml[CW][16];                   // running maximum and sum of each warp and head
+    unsigned long long warp_units[CW + 1], total, rest;
+    int first_seq, abort;
+};
+static_assert(sizeof(Misc) <= 1024, "small area");
+
+struct Args {
+    const uint16_t *ks, *vs;             // scales of the layer
+    int64_t s_tok, s_head;
+    const uint8_t *q;
+    int64_t ld_q;                        // bytes
+    void *out;
+    float *lse;
+    float *part_o;                       // [CTA][2][G][D]
+    float2 *part_ml;                     // [CTA][2][G]
+    int4 *desc;                          // [CTA]: sequence, kv head, partials (0: none) of the pair this CTA begins
+    int H_q, H_kv, G, box, n_slots;
+    float scale_log2;
+};
+
+// A pair's keys, or the part of them that falls into one CTA's run.
+struct Piece {
+    int seq, h, t0, t1, nt;
+};
+
+struct Walk {
+    int seq, h, t, nt;
+    unsigned long long left;
+    __device__ __forceinline__ bool next(const PagedView &pg, int H_kv, Piece &p) {
+        if (left == 0) return false;
+        p = {seq, h, t, (int)min((unsigned long long)nt, t + left), nt};
+        left -= p.t1 - p.t0;
+        t = 0;
+        if (++h == H_kv && left) {
+            h = 0;
+            nt = 0;
+            while (nt == 0 && seq + 1 < pg.n_seq) nt = tiles(pg, ++seq);
+            if (nt == 0) left = 0;   // cannot happen while the lengths stay as they are
+        }
+        return true;
+    }
+    static __device__ __forceinline__ int keys(const PagedView &pg, int i) {
+        return min(max(__ldcg(pg.len + i), 0), pg.max_pages * pg.page_size);
+    }
+    static __device__ __forceinline__ int tiles(const PagedView &pg, int i) {
+        return (keys(pg, i) + KT - 1) / KT;
+    }
+};
+
+// The list of W units is cut into P runs, [W c / P, W (c + 1) / P), none of them empty: one for each CTA, or W.
+__device__ __forceinline__ unsigned long long runs_of(unsigned long long W) {
+    return min((unsigned long long)gridDim.x, W);
 }
-template <int DT>
-__device__ __forceinline__ void store1(void *p, int64_t i, float x) {
-    if constexpr (DT == KVC_IN_F32) static_cast<float *>(p)[i] = x;
-    else if constexpr (DT == KVC_IN_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
-    else static_cast<__half *>(p)[i] = __float2half_rn(x);
+__device__ __forceinline__ unsigned long long run_start(unsigned long long W, unsigned c) {
+    const unsigned long long P = runs_of(W);
+    return c >= P ? W : W * c / P;
 }
 
-template <int D, bool Q8, int DT>
-__global__ void __launch_bounds__(128) decode_paged_kernel(const PagedView pg, const Args a) {
-    asm volatile("griddepcontrol.launch_dependents;");
+// A wait of a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
+template <int DT>
+__device__ __forceinline__ void store_out(void *out, int64_t i, float x) {
+    if constexpr (DT == KVC_IN_F32) static_cast<float *>(out)[i] = x;
+    else if constexpr (DT == KVC_IN_BF16) static_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(x);
+    else static_cast<__half *>(out)[i] = __float2half_rn(x);
+}
+
+// the order of the eight keys of half a subtile: rows 2i and 2i+1 differ in bit 2, even rows (and odd rows) in bits
+// 1 and 2, which is what makes every swizzled read below free of bank conflicts (a row of 128 bytes)
+__device__ __forceinline__ int key_of(int r) { return r ^ ((r & 1) << 2); }
+
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+// bytes c ^ 0x80 under the high byte 0x64 are the fp16 numbers 1152 + c
+__device__ __forceinline__ uint32_t unbias(uint32_t u) { return as_u32(__hsub2(as_half2(u), as_half2(0x64806480u))); }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+
+template <int D, bool Q8, int DT, int NT>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
+    decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const PagedView pg, const Args a) {
+    using C = Cfg<D, Q8, DT, NT>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+    Misc *ms = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
+    volatile int *s_abort = &ms->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        ms->abort = 0;
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(&ms->full[s], Q8 ? 33 : 1);
+            mbar_init(&ms->empty[s], CW);
+        }
+        mbar_init(&ms->q_full, 1);
+        mbar_init(&ms->q_empty, CW);
+        fence_mbar_init();
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int E = D / 32;
-    const int seq = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int len = max(pg.len[seq], 0), kvh = h / a.G;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    // ---- this CTA's run of the list
+    {
+        const int per = (pg.n_seq + THREADS - 1) / THREADS;
+        const int i0 = min((int)threadIdx.x * per, pg.n_seq), i1 = min(i0 + per, pg.n_seq);
+        unsigned long long mine = 0;
+        for (int i = i0; i < i1; ++i) mine += (unsigned long long)Walk::tiles(pg, i) * a.H_kv;
+        unsigned long long sum = mine;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = load1<DT>(a.q, seq * a.ld_q + (int64_t)h * D + e * 32 + lane) * a.scale;
-        o[e] = 0.f;
-    }
-    auto value = [&](bool is_v, int slot, int e) -> float {
-        const int64_t at = a.layer * a.g.c_layer + slot * a.g.c_tok + kvh * a.g.c_head + e * 32 + lane;
-        if constexpr (Q8) {
-            const uint16_t d = (is_v ? a.vs : a.ks)[a.layer * a.g.s_layer + slot * a.g.s_tok + kvh * a.g.s_head + e];
-            return (float)static_cast<const int8_t *>(is_v ? a.vq : a.kq)[at] * __half2float(__ushort_as_half(d));
-        } else {
-            return __half2float(static_cast<const __half *>(is_v ? a.vq : a.kq)[at]);
+        for (int x = 1; x < 32; x <<= 1) {
+            const unsigned long long up = __shfl_up_sync(0xffffffffu, sum, x);
+            if (lane >= x) sum += up;
         }
-    };
-    for (int j = warp; j < len; j += 4) {
-        const int slot = page_slot(pg, seq, j);
-        if (slot < 0) continue;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], value(false, slot, e), s);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        const float m_new = fmaxf(m, s), c = __expf(m - m_new), p = __expf(s - m_new);
-        l = l * c + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * value(true, slot, e);
-        m = m_new;
+        if (lane == 31) ms->warp_units[warp] = sum;
+        __syncthreads();
+        unsigned long long before = sum - mine, total = 0;
+        for (int w = 0; w <= CW; ++w) {
+            if (w < warp) before += ms->warp_units[w];
+            total += ms->warp_units[w];
+        }
+        const unsigned long long u0 = run_start(total, blockIdx.x);
+        if (threadIdx.x == 0) ms->total = total;
+        if (u0 >= before && u0 < before + mine) {
+            unsigned long long r = u0 - before;
+            int i = i0;
+            for (; i + 1 < i1; ++i) {
+                const unsigned long long n = (unsigned long long)Walk::tiles(pg, i) * a.H_kv;
+                if (r < n) break;
+                r -= n;
+            }
+            ms->first_seq = i;
+            ms->rest = r;
+        }
+        __syncthreads();
     }
-    __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
+    const unsigned long long W = ms->total, u0 = run_start(W, blockIdx.x), u1 = run_start(W, blockIdx.x + 1);
+    Walk walk = {0, 0, 0, 1, u1 - u0};
+    if (u1 > u0) {
+        walk.seq = ms->first_seq;
+        walk.nt = max(Walk::tiles(pg, walk.seq), 1);
+        walk.h = (int)(ms->rest / walk.nt);
+        walk.t = (int)(ms->rest % walk.nt);
+    }
+
+    if (warp == CW) {
+        // ------------------------------------------------------------------ producer
+        uint32_t n = 0, nq = 0;
+        bool ok = true;
+        Piece p;
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+        }
+        while (ok && walk.next(pg, a.H_kv, p)) {
+            if (nq > 0 && !warp_wait(&ms->q_empty, (nq - 1) & 1, s_abort)) break;
+            if (lane == 0) {
+                const uint32_t bytes = a.G * D * C::ESZ;
+                mbar_arrive_expect_tx(&ms->q_full, bytes);
+                bulk_load(sm + C::OFF_Q, a.q + p.seq * a.ld_q + (int64_t)p.h * bytes, bytes, &ms->q_full);
+            }
+            ++nq;
+            const int len = Walk::keys(pg, p.seq);
+            int slots = -1;
+            for (int t = p.t0; t < p.t1; ++t) {
+                if (((t - p.t0) & 7) == 0) {   // the pages of the next eight tiles, a subtile per lane
+                    const int key = t * KT + lane * 16;
+                    slots = key < len ? page_slot(pg, p.seq, key) : -1;
+                }
+                const int st = n % C::NS;
+                if (n >= (uint32_t)C::NS && !warp_wait(&ms->empty[st], ((n / C::NS) - 1) & 1, s_abort)) { ok = false; break; }
+                const int l0 = ((t - p.t0) & 7) * 4, left = len - t * KT;
+                uint8_t *kt = sm + st * C::STAGE, *vt = kt + C::TILE;
+                // subtile j: its first pool position and how many of its keys exist
+                const int my_slot = __shfl_sync(0xffffffffu, slots, l0 + (lane & 3));
+                if (lane < CW) ms->count[st][lane] = my_slot < 0 ? 0 : min(16, left - lane * 16);
+                const int per_box = a.box >> 4, boxes = KT / a.box;
+                const int box_slot = __shfl_sync(0xffffffffu, slots, l0 + ((lane * per_box) & 3));
+                const bool load = lane < boxes && box_slot >= 0;
+                const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&ms->full[st], loads * 2 * a.box * C::ROW);
+                __syncwarp();
+                if (load) {
+                    const int off = lane * a.box * (Q8 ? C::ROW : 128);
 #pragma unroll
-    for (int e = 0; e < E; ++e) sm_o[warp][e * 32 + lane] = o[e];
-    if (lane == 0) { sm_m[warp] = m; sm_l[warp] = l; }
+                    for (int hh = 0; hh < (Q8 ? 1 : D / 64); ++hh) {
+                        tma_load_3d(kt + hh * KT * 128 + off, &tm_k, &ms->full[st], hh * 64, box_slot, p.h);
+                        tma_load_3d(vt + hh * KT * 128 + off, &tm_v, &ms->full[st], hh * 64, box_slot, p.h);
+                    }
+                }
+                if constexpr (Q8) {
+                    uint8_t *sc = vt + C::TILE;
+#pragma unroll
+                    for (int i = 0; i < 2 * KT / 32; ++i) {
+                        const int key = (i * 32 + lane) & (KT - 1), is_v = i / (KT / 32);
+                        const int s = __shfl_sync(0xffffffffu, slots, l0 + (key >> 4));
+                        const bool valid = s >= 0 && key < left;
+                        const uint16_t *src = (is_v ? a.vs : a.ks) + (valid ? (int64_t)(s + (key & 15)) * a.s_tok + p.h * a.s_head : 0);
+                        cp_async_zfill<C::NB * 2>(sc + is_v * C::SC + key * C::NB * 2, src, valid);
+                    }
+                    cp_async_arrive(&ms->full[st]);
+                }
+                ++n;
+            }
+        }
+        if (*s_abort) {   // a wait gave up: let the copies in flight land before the CTA exits
+            volatile int never = 0;
+            for (uint32_t st = 0; st < (uint32_t)C::NS && st < n; ++st) {
+                const uint32_t last = st + ((n - 1 - st) / C::NS) * C::NS;
+                mbar_wait(&ms->full[st], (last / C::NS) & 1, &never, 200000000ull);
+            }
+            if (nq > 0) mbar_wait(&ms->q_full, (nq - 1) & 1, &never, 200000000ull);
+        }
+    } else {
+        // ------------------------------------------------------------------ consumers
+        const int g = lane >> 2, t4 = lane & 3;
+        const int kp = key_of(g);                               // my key (and kp + 8) in the first product
+        const int v0 = key_of(2 * t4), v1 = key_of(2 * t4 + 1);   // my keys (and + 8) in the second
+        uint32_t n = 0, nq = 0;
+        bool owner = false, ok = true;   // !ok: a wait gave up; the warp only keeps up with the others' barriers
+        Piece p;
+        // sequences without keys have no unit in the list
+        for (int i = blockIdx.x; i < pg.n_seq; i += gridDim.x) {
+            if (Walk::keys(pg, i) > 0) continue;
+            for (int e = threadIdx.x; e < a.H_q * D; e += 32 * CW) store_out<DT>(a.out, (int64_t)i * a.H_q * D + e, 0.f);
+            if (a.lse)
+                for (int e = threadIdx.x; e < a.H_q; e += 32 * CW) a.lse[(int64_t)i * a.H_q + e] = -INFINITY;
+        }
+        while (walk.next(pg, a.H_kv, p)) {
+            // the group's queries as the second operand of S^T: lane (g, t4) holds head g's eight values from
+            // dimension 32 i + 8 t4 (q8_0, i a block) or 64 (i / 2) + 8 (t4 + 4 (i % 2)) (f16), for two steps each
+            ok = ok && warp_wait(&ms->q_full, nq & 1, s_abort);
+            uint32_t qf[D / 16][NT][2];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int dim = Q8 ? 32 * i + 8 * t4 : 64 * (i >> 1) + 8 * (t4 + 4 * (i & 1));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int head = nt * 8 + g;
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};
+                    if (head < a.G) {
+                        const uint32_t at = smem_u32(sm + C::OFF_Q) + (head * D + dim) * C::ESZ;
+                        const uint4 x = lds128(at);
+                        const uint32_t xi[4] = {x.x, x.y, x.z, x.w};
+                        if constexpr (DT == KVC_IN_F16) {
+                            for (int e = 0; e < 4; ++e) w[e] = xi[e];
+                        } else if constexpr (DT == KVC_IN_BF16) {
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack_half2(__uint_as_float(xi[e] << 16), __uint_as_float(xi[e] & 0xFFFF0000u));
+                        } else {
+                            const uint4 y = lds128(at + 16);
+                            w[0] = pack_half2(__uint_as_float(x.x), __uint_as_float(x.y));
+                            w[1] = pack_half2(__uint_as_float(x.z), __uint_as_float(x.w));
+                            w[2] = pack_half2(__uint_as_float(y.x), __uint_as_float(y.y));
+                            w[3] = pack_half2(__uint_as_float(y.z), __uint_as_float(y.w));
+                        }
+                    }
+                    qf[2 * i][nt][0] = w[0]; qf[2 * i][nt][1] = w[1];
+                    qf[2 * i + 1][nt][0] = w[2]; qf[2 * i + 1][nt][1] = w[3];
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms->q_empty);
+            ++nq;
+
+            float o[C::MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                m[nt][0] = m[nt][1] = -INFINITY;
+                l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+                for (int i = 0; i < C::MT; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+            }
+            for (int t = p.t0; t < p.t1; ++t, ++n) {
+                const int st = n % C::NS;
+                ok = ok && warp_wait(&ms->full[st], (n / C::NS) & 1, s_abort);
+                if (!ok) break;
+                const int count = ms->count[st][warp];
+                if (count > 0) {
+                    const uint32_t kt = smem_u32(sm + st * C::STAGE), vt = kt + C::TILE, sc = vt + C::TILE;
+                    const int ra = warp * 16 + kp, rb = ra + 8;   // my rows of the tile
+                    float s[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+                    if constexpr (Q8) {
+                        uint32_t da[C::NB / 2], db[C::NB / 2];   // scales of my two keys
+                        if constexpr (D == 128) {
+                            const uint2 x = lds64(sc + ra * 8), y = lds64(sc + rb * 8);
+                            da[0] = x.x; da[1] = x.y; db[0] = y.x; db[1] = y.y;
+                        } else {
+                            da[0] = lds32(sc + ra * 4); db[0] = lds32(sc + rb * 4);
+                        }
+#pragma unroll
+                        for (int b = 0; b < C::NB; ++b) {
+                            const int c = 2 * b + (t4 >> 1);
+                            const int sw = D == 128 ? c ^ (kp & 7) : c ^ ((kp >> 1) & 3);
+                            const uint2 x = lds64(kt + ra * C::ROW + (sw << 4) + 8 * (t4 & 1));
+                            const uint2 y = lds64(kt + rb * C::ROW + (sw << 4) + 8 * (t4 & 1));
+                            float acc[NT][4];
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t u = (j ? x.y : x.x) ^ 0x80808080u, w = (j ? y.y : y.x) ^ 0x80808080u;
+                                const uint32_t A[4] = {unbias(__byte_perm(u, 0x64646464u, 0x4140)),
+                                                       unbias(__byte_perm(w, 0x64646464u, 0x4140)),
+                                                       unbias(__byte_perm(u, 0x64646464u, 0x4342)),
+                                                       unbias(__byte_perm(w, 0x64646464u, 0x4342))};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma_16816(acc[nt], A, qf[2 * b + j][nt][0], qf[2 * b + j][nt][1]);
+                            }
+                            const float2 fa = __half22float2(as_half2(da[b >> 1])), fb = __half22float2(as_half2(db[b >> 1]));
+                            const float ca = b & 1 ? fa.y : fa.x, cb = b & 1 ? fb.y : fb.x;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                s[nt][0] = fmaf(acc[nt][0], ca, s[nt][0]);
+                                s[nt][1] = fmaf(acc[nt][1], ca, s[nt][1]);
+                                s[nt][2] = fmaf(acc[nt][2], cb, s[nt][2]);
+                                s[nt][3] = fmaf(acc[nt][3], cb, s[nt][3]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            const uint32_t base = kt + (i >> 1) * KT * 128 + (((t4 + 4 * (i & 1)) ^ (kp & 7)) << 4);
+                            const uint4 x = lds128(base + ra * 128), y = lds128(base + rb * 128);
+                            const uint32_t A[4] = {x.x, y.x, x.y, y.y}, B[4] = {x.z, y.z, x.w, y.w};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_16816(s[nt], A, qf[2 * i][nt][0], qf[2 * i][nt][1]);
+                                mma_16816(s[nt], B, qf[2 * i + 1][nt][0], qf[2 * i + 1][nt][1]);
+                            }
+                        }
+                    }
+                    if (count < 16) {   // the last subtile of a sequence
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (kp >= count) s[nt][0] = s[nt][1] = -INFINITY;
+                            if (kp + 8 >= count) s[nt][2] = s[nt][3] = -INFINITY;
+                        }
+                    }
+                    bool above = false;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            above |= fmaxf(s[nt][e], s[nt][e + 2]) * a.scale_log2 > m[nt][e] + RESCALE_LOG2;
+                    if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float f[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float x = fmaxf(s[nt][e], s[nt][e + 2]);
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                                const float m_new = fmaxf(m[nt][e], x * a.scale_log2);
+                                f[e] = m[nt][e] == m_new ? 1.f : ex2(m[nt][e] - m_new);
+                                m[nt][e] = m_new;
+                                l[nt][e] *= f[e];
+                            }
+#pragma unroll
+                            for (int i = 0; i < C::MT; ++i) {
+                                o[i][nt][0] *= f[0]; o[i][nt][1] *= f[1]; o[i][nt][2] *= f[0]; o[i][nt][3] *= f[1];
+                            }
+                        }
+                    }
+                    uint32_t pb[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float e[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) e[i] = ex2(fmaf(s[nt][i], a.scale_log2, -m[nt][i & 1]));
+                        l[nt][0] += e[0] + e[2];
+                        l[nt][1] += e[1] + e[3];
+                        pb[nt][0] = movmatrix_trans(pack_half2(e[0], e[1]));
+                        pb[nt][1] = movmatrix_trans(pack_half2(e[2], e[3]));
+                    }
+                    if constexpr (Q8) {
+                        constexpr int NW = D / 32;   // words of one key's part: 16 (8) dimensions from D / 8 * g
+                        uint32_t w[4][NW], d[4];
+                        const int keys[4] = {v0, v1, v0 + 8, v1 + 8};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = warp * 16 + keys[i];
+                            if constexpr (D == 128) {
+                                const uint4 x = lds128(vt + key * 128 + ((g ^ (keys[i] & 7)) << 4));
+                                w[i][0] = x.x; w[i][1] = x.y; w[i][2] = x.z; w[i][3] = x.w;
+                            } else {
+                                const uint2 x = lds64(vt + key * 64 + (((g >> 1) ^ ((keys[i] >> 1) & 3)) << 4) + 8 * (g & 1));
+                                w[i][0] = x.x; w[i][1] = x.y;
+                            }
+                            d[i] = lds16(sc + C::SC + (key * C::NB + (g * (D / 8)) / 32) * 2);
+                        }
+                        const __half2 d01 = as_half2(d[0] | d[1] << 16), d23 = as_half2(d[2] | d[3] << 16);
+#pragma unroll
+                        for (int i = 0; i < C::MT; ++i) {
+                            uint32_t A[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {   // row half e & 1 (the odd byte), keys 2 (e / 2) and + 1
+                                const int b = 2 * (i & 1) + (e & 1);
+                                uint32_t u = __byte_perm(w[e & 2][i >> 1], w[(e & 2) + 1][i >> 1], 0x11u * b | 0x1100u * (4 + b));
+                                u = (u & 0x00FF00FFu) ^ 0x64806480u;
+                                A[e] = as_u32(__hmul2(as_half2(unbias(u)), e & 2 ? d23 : d01));
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_16816(o[i][nt], A, pb[nt][0], pb[nt][1]);
+                        }
+                    } else {
+                        const int key = warp * 16 + key_of(lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+                        for (int i = 0; i < C::MT; ++i) {
+                            const int c = 2 * i + ((lane >> 3) & 1);
+                            uint32_t A[4];
+                            ldmatrix_x4_trans(A, vt + (c >> 3) * KT * 128 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+                            if (count < 16) {   // values behind the sequence may be anything: their weight is zero
+                                const uint32_t lo = (v0 < count ? 0xFFFFu : 0u) | (v1 < count ? 0xFFFF0000u : 0u);
+                                const uint32_t hi = (v0 + 8 < count ? 0xFFFFu : 0u) | (v1 + 8 < count ? 0xFFFF0000u : 0u);
+                                A[0] &= lo; A[1] &= lo; A[2] &= hi; A[3] &= hi;
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_16816(o[i][nt], A, pb[nt][0], pb[nt][1]);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms->empty[st]);
+            }
+
+            // ---- the piece is done: join the four warps.  Warp w ends up with tiles [w OWN, (w + 1) OWN) of O^T.
+            float f[NT][2], M[NT][2], L[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[nt][e];
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    l[nt][e] = x;
+                    if (g == 0) ms->ml[warp][nt * 8 + 2 * t4 + e] = make_float2(m[nt][e], x);
+                }
+            named_barrier(1, 32 * CW);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int head = nt * 8 + 2 * t4 + e;
+                    float2 x[CW];
+                    float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < CW; ++w) {
+                        x[w] = ms->ml[w][head];
+                        mx = fmaxf(mx, x[w].x);
+                    }
+#pragma unroll
+                    for (int w = 0; w < CW; ++w) sum += x[w].x == -INFINITY ? 0.f : x[w].y * ex2(x[w].x - mx);
+                    M[nt][e] = mx;
+                    L[nt][e] = sum;
+                    f[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mx);
+                }
+            float4 *red = reinterpret_cast<float4 *>(sm + C::OFF_RED);
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    o[i][nt][0] *= f[nt][0]; o[i][nt][1] *= f[nt][1]; o[i][nt][2] *= f[nt][0]; o[i][nt][3] *= f[nt][1];
+                    const int to = i / C::OWN;
+                    if (to != warp)
+                        red[((i * NT + nt) * (CW - 1) + ((warp - to - 1) & 3)) * 32 + lane] =
+                            make_float4(o[i][nt][0], o[i][nt][1], o[i][nt][2], o[i][nt][3]);
+                }
+            named_barrier(1, 32 * CW);
+            const bool whole = p.t0 == 0 && p.t1 == p.nt;
+            const int slot = (blockIdx.x * 2 + (p.t0 == 0)) * a.G;
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i) {
+                if (i / C::OWN != warp) continue;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int x = 0; x < CW - 1; ++x) {
+                        const float4 y = red[((i * NT + nt) * (CW - 1) + x) * 32 + lane];
+                        o[i][nt][0] += y.x; o[i][nt][1] += y.y; o[i][nt][2] += y.z; o[i][nt][3] += y.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int head = nt * 8 + 2 * t4 + (e & 1);
+                        const int dim = Q8 ? g * (D / 8) + 2 * i + (e >> 1) : 16 * i + g + 8 * (e >> 1);
+                        if (head >= a.G) continue;
+                        if (whole)
+                            store_out<DT>(a.out, ((int64_t)p.seq * a.H_q + p.h * a.G + head) * D + dim,
+                                          L[nt][e & 1] > 0.f || L[nt][e & 1] != L[nt][e & 1] ? o[i][nt][e] / L[nt][e & 1] : 0.f);
+                        else
+                            a.part_o[(int64_t)(slot + head) * D + dim] = o[i][nt][e];
+                    }
+                }
+            }
+            if (warp == 0 && g == 0) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int head = nt * 8 + 2 * t4 + e;
+                        if (head >= a.G) continue;
+                        if (!whole) a.part_ml[slot + head] = make_float2(M[nt][e], L[nt][e]);
+                        else if (a.lse)
+                            a.lse[(int64_t)p.seq * a.H_q + p.h * a.G + head] =
+                                L[nt][e] == 0.f ? -INFINITY : (M[nt][e] + log2f(L[nt][e])) * LN2;
+                    }
+            }
+            if (p.t0 == 0 && p.t1 < p.nt) {
+                owner = true;
+                if (threadIdx.x == 0) {
+                    const unsigned long long end = u1 + (p.nt - p.t1);   // the pair's last unit, plus one
+                    const int last = (int)((end * runs_of(W) - 1) / W);    // the CTA whose run holds it
+                    a.desc[blockIdx.x] = make_int4(p.seq, p.h, last - (int)blockIdx.x + 1, 0);
+                }
+            }
+        }
+        if (!owner && threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
     __syncthreads();
-    const float M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-    float L = 0.f, acc = 0.f;
-    if (M > -INFINITY) {
-        for (int w = 0; w < 4; ++w) {
-            const float c = __expf(sm_m[w] - M);
-            L += c * sm_l[w];
-            if (threadIdx.x < D) acc += c * sm_o[w][threadIdx.x];
-        }
-    }
-    if (threadIdx.x < D) store1<DT>(a.out, ((int64_t)seq * a.H_q + h) * D + threadIdx.x, L > 0.f ? acc / L : 0.f);
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)seq * a.H_q + h] = M > -INFINITY ? M + __logf(L) : -INFINITY;
+    if (threadIdx.x == 0 && *s_abort) atomicExch(&g_paged_status, 1);
 }
 
-template <int D, bool Q8, int DT>
-cudaError_t launch_t(const PagedView &pg, const Args &a, cudaStream_t s) {
+// Joins the partials of the pair that CTA blockIdx.x of the first kernel began, for one query head:
+// out = sum_p w_p O_p / sum_p w_p l_p, w_p = 2^(m_p - max m), the runs in a fixed order.
+template <int D, int DT>
+__global__ void __launch_bounds__(COMBINE_THREADS) combine_paged_kernel(const Args a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int4 d = __ldcg(a.desc + blockIdx.x);
+    if (d.z == 0) return;
+    constexpr int LANES = D / 4, GROUPS = COMBINE_THREADS / LANES;
+    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, head = blockIdx.y;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // partial j lies with CTA blockIdx.x + j: its second slot for the first (the pair begins there), else the first
+    constexpr int B = 4;
+    for (int j0 = grp; j0 < d.z; j0 += B * GROUPS) {
+        float2 ml[B];
+        float4 o[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int j = j0 + b * GROUPS;
+            ml[b] = make_float2(-INFINITY, 0.f);
+            o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < d.z) {
+                const int slot = ((blockIdx.x + j) * 2 + (j == 0)) * a.G + head;
+                ml[b] = __ldcg(a.part_ml + slot);
+                o[b] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (int64_t)slot * D) + lane);
+            }
+        }
+        float mx = m;
+#pragma unroll
+        for (int b = 0; b < B; ++b) mx = fmaxf(mx, ml[b].x);
+        if (mx == -INFINITY) continue;
+        const float f = m == -INFINITY ? 0.f : ex2(m - mx);
+        m = mx;
+        l *= f; acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const float w = ml[b].x == -INFINITY ? 0.f : ex2(ml[b].x - m);
+            l = fmaf(w, ml[b].y, l);
+            acc.x = fmaf(w, o[b].x, acc.x); acc.y = fmaf(w, o[b].y, acc.y);
+            acc.z = fmaf(w, o[b].z, acc.z); acc.w = fmaf(w, o[b].w, acc.w);
+        }
+    }
+    __shared__ float sm_m[GROUPS], sm_l[GROUPS];
+    __shared__ float4 sm_o[GROUPS][LANES];
+    if (lane == 0) { sm_m[grp] = m; sm_l[grp] = l; }
+    sm_o[grp][lane] = acc;
+    __syncthreads();
+    if (grp != 0) return;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) M = fmaxf(M, sm_m[i]);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+        const float w = sm_m[i] == -INFINITY ? 0.f : ex2(sm_m[i] - M);
+        const float4 o = sm_o[i][lane];
+        L = fmaf(w, sm_l[i], L);
+        acc.x = fmaf(w, o.x, acc.x); acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z); acc.w = fmaf(w, o.w, acc.w);
+    }
+    const int64_t row = (int64_t)d.x * a.H_q + d.y * a.G + head;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    store_out<DT>(a.out, row * D + 4 * lane, acc.x * inv);
+    store_out<DT>(a.out, row * D + 4 * lane + 1, acc.y * inv);
+    store_out<DT>(a.out, row * D + 4 * lane + 2, acc.z * inv);
+    store_out<DT>(a.out, row * D + 4 * lane + 3, acc.w * inv);
+    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+}
+
+template <int D, bool Q8, int DT, int NT>
+int launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const PagedView &pg, const Args &a, cudaStream_t s) {
+    using C = Cfg<D, Q8, DT, NT>;
+    if (allow_dynamic_smem((const void *)decode_paged_kernel<D, Q8, DT, NT>, C::ALLOC) != KVC_OK) return KVC_ECUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(pg.n_seq, a.H_q);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(a.n_slots);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = C::ALLOC;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_paged_kernel<D, Q8, DT>, pg, a);
+    if (cudaLaunchKernelEx(&cfg, decode_paged_kernel<D, Q8, DT, NT>, tk, tv, pg, a) != cudaSuccess) return KVC_ECUDA;
+    cfg.gridDim = dim3(a.n_slots, a.G);
+    cfg.blockDim = dim3(COMBINE_THREADS);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, combine_paged_kernel<D, DT>, a) != cudaSuccess) return KVC_ECUDA;
+    return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ECUDA;
 }
 
 template <int D, bool Q8>
-cudaError_t launch_dt(int dtype, const PagedView &pg, const Args &a, cudaStream_t s) {
+int launch_d(int dtype, const CUtensorMap &tk, const CUtensorMap &tv, const PagedView &pg, const Args &a, cudaStream_t s) {
     switch (dtype) {
-        case KVC_IN_F32: return launch_t<D, Q8, KVC_IN_F32>(pg, a, s);
-        case KVC_IN_BF16: return launch_t<D, Q8, KVC_IN_BF16>(pg, a, s);
-        default: return launch_t<D, Q8, KVC_IN_F16>(pg, a, s);
+#define KVC_CASE(DT)                                                                             \
+    case DT:                                                                                     \
+        return a.G <= 8 ? launch_t<D, Q8, DT, 1>(tk, tv, pg, a, s) : launch_t<D, Q8, DT, 2>(tk, tv, pg, a, s);
+        KVC_CASE(KVC_IN_F32)
+        KVC_CASE(KVC_IN_BF16)
+        KVC_CASE(KVC_IN_F16)
+#undef KVC_CASE
+        default: return KVC_EINVAL;
     }
 }
 
+int slots_of() { return CTAS_PER_SM * sm_count(); }
+
 }  // namespace
 
-size_t paged_scratch_bytes(const kvc_desc &, int, int) { return 16; }
+size_t paged_scratch_bytes(const kvc_desc &d, int, int n_head_q) {
+    const size_t G = n_head_q / d.n_head_kv;
+    return (size_t)slots_of() * (2 * G * (d.head_dim + 2) * sizeof(float) + sizeof(int4));
+}
 
 int launch_decode_paged(const kvc_cache &c, const kvc_pages &p, int layer, const void *q, int64_t ld_q, int dtype,
-                        int n_head_q, void *out, float *lse, void *, cudaStream_t s) {
+                        int n_head_q, void *out, float *lse, void *scratch, cudaStream_t s) {
+    const kvc_desc &d = c.d;
+    const Geom g = geom_of(d);
+    const bool q8 = d.type == KVC_Q8_0;
+    const int esz = q8 ? 1 : 2, D = d.head_dim;
     Args a;
-    a.kq = c.k_q;
-    a.vq = c.v_q;
-    a.ks = static_cast<const uint16_t *>(c.k_s);
-    a.vs = static_cast<const uint16_t *>(c.v_s);
-    a.g = geom_of(c.d);
-    a.layer = layer;
-    a.H_q = n_head_q;
-    a.G = n_head_q / c.d.n_head_kv;
-    a.q = q;
-    a.ld_q = ld_q;
+    a.ks = q8 ? static_cast<const uint16_t *>(c.k_s) + layer * g.s_layer : nullptr;
+    a.vs = q8 ? static_cast<const uint16_t *>(c.v_s) + layer * g.s_layer : nullptr;
+    a.s_tok = g.s_tok;
+    a.s_head = g.s_head;
+    a.q = static_cast<const uint8_t *>(q);
+    a.ld_q = ld_q * dtype_bytes(dtype);
     a.out = out;
     a.lse = lse;
-    a.scale = 1.f / sqrtf((float)c.d.head_dim);
+    a.H_q = n_head_q;
+    a.H_kv = d.n_head_kv;
+    a.G = n_head_q / d.n_head_kv;
+    a.n_slots = slots_of();
+    a.desc = static_cast<int4 *>(scratch);
+    a.part_o = reinterpret_cast<float *>(a.desc + a.n_slots);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)a.n_slots * 2 * a.G * D);
+    a.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+    // a TMA box covers the part of a tile that lies in one page
+    a.box = p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
+    const CUtensorMapDataType dt = q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapSwizzle sw = q8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    CUtensorMap tk, tv;
+    const uint32_t inner = q8 ? D : 64;
+    auto map = [&](CUtensorMap *m, const void *base) {
+        return make_map_3d(m, dt, static_cast<const uint8_t *>(base) + layer * g.c_layer * esz, D, d.n_ctx, d.n_head_kv,
+                           g.c_tok * esz, g.c_head * esz, inner, a.box, 1, sw);
+    };
+    if (!map(&tk, c.k_q) || !map(&tv, c.v_q)) return KVC_ECUDA;
     const PagedView pg = paged_view(c, p);
-    const bool q8 = c.d.type == KVC_Q8_0;
-    cudaError_t e;
-    if (c.d.head_dim == 128) e = q8 ? launch_dt<128, true>(dtype, pg, a, s) : launch_dt<128, false>(dtype, pg, a, s);
-    else e = q8 ? launch_dt<64, true>(dtype, pg, a, s) : launch_dt<64, false>(dtype, pg, a, s);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? KVC_OK : KVC_ECUDA;
+    if (D == 128) return q8 ? launch_d<128, true>(dtype, tk, tv, pg, a, s) : launch_d<128, false>(dtype, tk, tv, pg, a, s);
+    return q8 ? launch_d<64, true>(dtype, tk, tv, pg, a, s) : launch_d<64, false>(dtype, tk, tv, pg, a, s);
+}
+
+int read_and_clear_paged_status(int32_t *status) {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_paged_status, sizeof(int)) != cudaSuccess) return KVC_ECUDA;
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_paged_status, &zero, sizeof(int)) != cudaSuccess) return KVC_ECUDA;
+    *status = v;
+    return KVC_OK;
 }
 
 }  // namespace kvc

@@ -110,5 +110,6 @@ uint64_t take_test_stall(int which);
 // Device status word set by kernels that give up a bounded wait (all kernels' words, read and cleared).
 int read_and_clear_device_status(int32_t *status);
 int read_and_clear_decode_status(int32_t *status);
+int read_and_clear_paged_status(int32_t *status);
 
 }  // namespace kvc

@@ -214,6 +214,47 @@ __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// ---- warp-level matrix instructions, for products of a few rows -------------------------
+// D[16x8] += A[16x16] B[16x8], fp16 in, float32 accumulation.  Lane (g = lane / 4, t = lane % 4) holds
+// a: rows g, g+8 x columns 2t, 2t+1 | 2t+8, 2t+9 (order: row g, row g+8, row g high, row g+8 high);
+// b: rows 2t, 2t+1 | 2t+8, 2t+9 of column g; d: (g, 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1).
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four 8x8 matrices of 16-bit values, transposed: lane i gives the address of row i % 8 of matrix i / 8.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// An 8x8 matrix of 16-bit values held two to a lane, transposed across the warp.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// ---- small asynchronous copies ------------------------------------------------------------
+// N bytes (4 or 8) to shared memory, zeros when !valid (the source is then not read).
+template <int N>
+__device__ __forceinline__ void cp_async_zfill(void *dst, const void *src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N),
+                 "r"(valid ? N : 0)
+                 : "memory");
+}
+// One arrival on `bar` once this thread's cp_async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// A barrier among `n` threads of the CTA.
+__device__ __forceinline__ void named_barrier(int id, int n) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
 // ---- register reallocation between warpgroups (all warps of a warpgroup execute it) ----
 template <uint32_t N>
 __device__ __forceinline__ void setmaxnreg_inc() {
