@@ -5,9 +5,11 @@
 // What bounds it: every key and value is read once and used for the G query heads of its group, so the floor
 // is the pool's bytes over the HBM rate (a few operations per byte; q8_0 also has to turn each code into fp16).
 //
-// Work split.  The keys of all (sequence, kv head) pairs, in tiles of 64, form one list that is cut into
-// equal runs, one for each CTA (two per SM), wherever the boundaries fall: ragged lengths, one long sequence
-// and many short ones all fill the GPU.  The lengths are read on the device.  A pair inside one run is written
+// Work split.  The keys of all (kv head, sequence) pairs, in tiles of 64 and with a charge for each pair, form
+// one list that is cut into equal runs, one for each CTA (two per SM), wherever the boundaries fall: ragged
+// lengths, one long sequence and many short ones all fill the GPU.  Heads are outermost, so where their number
+// divides the CTAs' the CTAs of all heads pass the same tokens at the same time, which is what a layer-major
+// pool (a token's heads side by side) wants of DRAM and L2.  The lengths are read on the device.  A pair inside one run is written
 // straight to out; a pair cut by run boundaries leaves one partial (O, maximum, sum) per run in scratch - at
 // most two per CTA - and a second kernel joins them in run order.
 //
@@ -48,6 +50,7 @@ constexpr int THREADS = 32 * (CW + 1);
 constexpr int CTAS_PER_SM = 2;
 constexpr int SMEM_BUDGET = 115712;  // 113 KB: two CTAs per SM
 constexpr int COMBINE_THREADS = 256;
+constexpr int PIECE_COST = 2;       // what starting and ending a pair costs, in tiles
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -62,22 +65,23 @@ struct Cfg {
     static constexpr int OWN = MT / CW;                     // of which each warp writes
     static constexpr int RED = MT * NT * (CW - 1) * 512;    // the other warps' accumulators
     static constexpr int ESZ = DT == KVC_IN_F32 ? 4 : 2;
-    static constexpr int QB = 8 * NT * D * ESZ;
+    static constexpr int QB = 8 * NT * D * ESZ;             // the most that a group's queries take
     static constexpr int MISC = 1024;
     static constexpr int FIT = (SMEM_BUDGET - 1024 - RED - QB - MISC) / STAGE;
     static constexpr int NS = FIT < 12 ? FIT : 12;
-    static constexpr int OFF_RED = NS * STAGE, OFF_Q = OFF_RED + RED, OFF_MISC = OFF_Q + QB;
-    static constexpr int ALLOC = OFF_MISC + MISC + 1024;
-    static_assert(NS >= 2 && ALLOC <= SMEM_BUDGET, "shared memory plan");
+    static constexpr int OFF_RED = NS * STAGE, OFF_MISC = OFF_RED + RED, OFF_Q = OFF_MISC + MISC;
+    static constexpr int Q_ROOM = SMEM_BUDGET - 1024 - OFF_Q;
+    static_assert(NS >= 2 && Q_ROOM >= QB, "shared memory plan");
 };
+constexpr int MAX_NQ = 4;           // slots for the queries of pieces to come: as many as fit
 
 // what the small area behind the ring holds
 struct Misc {
-    uint64_t full[12], empty[12], q_full, q_empty;
+    uint64_t full[12], empty[12], q_full[MAX_NQ], q_empty[MAX_NQ];
     int count[12][CW];                   // keys of each subtile that exist
     float2 ml[CW][16];                   // running maximum and sum of each warp and head
-    unsigned long long warp_units[CW + 1], total, rest;
-    int first_seq, abort;
+    unsigned long long warp_units[CW + 1], total;
+    int first_seq, rest, abort;
 };
 static_assert(sizeof(Misc) <= 1024, "small area");
 
@@ -91,36 +95,45 @@ struct Args {
     float *part_o;                       // [CTA][2][G][D]
     float2 *part_ml;                     // [CTA][2][G]
     int4 *desc;                          // [CTA]: sequence, kv head, partials (0: none) of the pair this CTA begins
-    int H_q, H_kv, G, box, n_slots;
+    int H_q, H_kv, G, box, n_slots, n_q;
     float scale_log2;
 };
 
 // A pair's keys, or the part of them that falls into one CTA's run.
 struct Piece {
-    int seq, h, t0, t1, nt;
+    int seq, h, t0, t1, nt, keys;
 };
 
+__device__ __forceinline__ int keys_of(const PagedView &pg, int i) {
+    return min(max(__ldcg(pg.len + i), 0), pg.max_pages * pg.page_size);
+}
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + KT - 1) / KT; }
+__device__ __forceinline__ int units_of(int keys) { return keys > 0 ? tiles_of(keys) + PIECE_COST : 0; }
+
+// A warp's way through its CTA's run of the list: kv heads, in each the sequences, in each its units.  The
+// lengths of 32 sequences are held a lane each, so that most steps load nothing.
 struct Walk {
-    int seq, h, t, nt;
+    int seq, h, x, base, held;   // x: units of the current pair that lie before this run
     unsigned long long left;
+    __device__ __forceinline__ Walk(const PagedView &pg, int seq_, int h_, int x_, unsigned long long left_)
+        : seq(seq_), h(h_), x(x_), left(left_) { load(pg); }
+    __device__ __forceinline__ void load(const PagedView &pg) {
+        base = seq;
+        const int i = base + (threadIdx.x & 31);
+        held = i < pg.n_seq ? keys_of(pg, i) : 0;
+    }
     __device__ __forceinline__ bool next(const PagedView &pg, int H_kv, Piece &p) {
-        if (left == 0) return false;
-        p = {seq, h, t, (int)min((unsigned long long)nt, t + left), nt};
-        left -= p.t1 - p.t0;
-        t = 0;
-        if (++h == H_kv && left) {
-            h = 0;
-            nt = 0;
-            while (nt == 0 && seq + 1 < pg.n_seq) nt = tiles(pg, ++seq);
-            if (nt == 0) left = 0;   // cannot happen while the lengths stay as they are
+        while (left > 0 && h < H_kv) {
+            if (seq - base >= 32 || seq < base) load(pg);
+            const int keys = __shfl_sync(0xffffffffu, held, seq - base), all = units_of(keys);
+            const int x1 = (int)min((unsigned long long)all, x + left);
+            p = {seq, h, max(x - PIECE_COST, 0), max(x1 - PIECE_COST, 0), tiles_of(keys), keys};
+            left -= x1 - x;
+            x = 0;
+            if (++seq == pg.n_seq) { seq = 0; ++h; }
+            if (p.t1 > p.t0) return true;
         }
-        return true;
-    }
-    static __device__ __forceinline__ int keys(const PagedView &pg, int i) {
-        return min(max(__ldcg(pg.len + i), 0), pg.max_pages * pg.page_size);
-    }
-    static __device__ __forceinline__ int tiles(const PagedView &pg, int i) {
-        return (keys(pg, i) + KT - 1) / KT;
+        return false;
     }
 };
 
@@ -191,19 +204,21 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
             mbar_init(&ms->full[s], Q8 ? 33 : 1);
             mbar_init(&ms->empty[s], CW);
         }
-        mbar_init(&ms->q_full, 1);
-        mbar_init(&ms->q_empty, CW);
+        for (int s = 0; s < MAX_NQ; ++s) {
+            mbar_init(&ms->q_full[s], 1);
+            mbar_init(&ms->q_empty[s], CW);
+        }
         fence_mbar_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
-    // ---- this CTA's run of the list
+    // ---- this CTA's run of the list: where it starts
     {
         const int per = (pg.n_seq + THREADS - 1) / THREADS;
         const int i0 = min((int)threadIdx.x * per, pg.n_seq), i1 = min(i0 + per, pg.n_seq);
         unsigned long long mine = 0;
-        for (int i = i0; i < i1; ++i) mine += (unsigned long long)Walk::tiles(pg, i) * a.H_kv;
+        for (int i = i0; i < i1; ++i) mine += units_of(keys_of(pg, i));
         unsigned long long sum = mine;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
@@ -217,84 +232,105 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
             if (w < warp) before += ms->warp_units[w];
             total += ms->warp_units[w];
         }
-        const unsigned long long u0 = run_start(total, blockIdx.x);
+        unsigned long long r = total ? run_start(total * a.H_kv, blockIdx.x) % total : 0;
         if (threadIdx.x == 0) ms->total = total;
-        if (u0 >= before && u0 < before + mine) {
-            unsigned long long r = u0 - before;
+        if (r >= before && r < before + mine) {
+            r -= before;
             int i = i0;
             for (; i + 1 < i1; ++i) {
-                const unsigned long long n = (unsigned long long)Walk::tiles(pg, i) * a.H_kv;
+                const unsigned long long n = units_of(keys_of(pg, i));
                 if (r < n) break;
                 r -= n;
             }
             ms->first_seq = i;
-            ms->rest = r;
+            ms->rest = (int)r;
         }
         __syncthreads();
     }
-    const unsigned long long W = ms->total, u0 = run_start(W, blockIdx.x), u1 = run_start(W, blockIdx.x + 1);
-    Walk walk = {0, 0, 0, 1, u1 - u0};
-    if (u1 > u0) {
-        walk.seq = ms->first_seq;
-        walk.nt = max(Walk::tiles(pg, walk.seq), 1);
-        walk.h = (int)(ms->rest / walk.nt);
-        walk.t = (int)(ms->rest % walk.nt);
-    }
+    const unsigned long long W = ms->total * a.H_kv, u0 = run_start(W, blockIdx.x), u1 = run_start(W, blockIdx.x + 1);
+    Walk walk(pg, u1 > u0 ? ms->first_seq : 0, u1 > u0 ? (int)(u0 / ms->total) : 0, u1 > u0 ? ms->rest : 0, u1 - u0);
 
     if (warp == CW) {
         // ------------------------------------------------------------------ producer
+        // Tiles are taken eight at a time, across pieces: lane 4 i + j knows subtile j of the i-th.  The pages of the
+        // next eight are being looked up while these are copied.
+        struct Batch {
+            int n, seq, h, t, keys, page;
+            bool first;
+        };
         uint32_t n = 0, nq = 0;
-        bool ok = true;
-        Piece p;
+        bool more = true;
+        Piece p = {0, 0, 0, 0, 0, 0};
+        int t = 0;
+        auto take = [&](Batch &b) {
+            b.n = 0;
+            b.keys = 0;
+            b.t = 0;
+            while (b.n < 8 && more) {
+                const bool first = t >= p.t1;
+                if (first) {
+                    more = walk.next(pg, a.H_kv, p);
+                    if (!more) break;
+                    t = p.t0;
+                }
+                if ((lane >> 2) == b.n) {
+                    b.seq = p.seq; b.h = p.h; b.t = t; b.keys = p.keys; b.first = first;
+                }
+                ++t;
+                ++b.n;
+            }
+            const int key = b.t * KT + (lane & 3) * 16;
+            b.page = key < b.keys ? __ldcg(pg.table + (int64_t)b.seq * pg.max_pages + key / pg.page_size) : -1;
+        };
         if (lane == 0) {
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
         }
-        while (ok && walk.next(pg, a.H_kv, p)) {
-            if (nq > 0 && !warp_wait(&ms->q_empty, (nq - 1) & 1, s_abort)) break;
-            if (lane == 0) {
-                const uint32_t bytes = a.G * D * C::ESZ;
-                mbar_arrive_expect_tx(&ms->q_full, bytes);
-                bulk_load(sm + C::OFF_Q, a.q + p.seq * a.ld_q + (int64_t)p.h * bytes, bytes, &ms->q_full);
-            }
-            ++nq;
-            const int len = Walk::keys(pg, p.seq);
-            int slots = -1;
-            for (int t = p.t0; t < p.t1; ++t) {
-                if (((t - p.t0) & 7) == 0) {   // the pages of the next eight tiles, a subtile per lane
-                    const int key = t * KT + lane * 16;
-                    slots = key < len ? page_slot(pg, p.seq, key) : -1;
+        const int q_bytes = a.G * D * C::ESZ, per_box = a.box >> 4, boxes = KT / a.box;
+        Batch cur, nxt;
+        take(cur);
+        for (bool ok = true; ok && cur.n > 0; cur = nxt) {
+            take(nxt);
+            const int key0 = cur.t * KT + (lane & 3) * 16;
+            // my subtile's first pool position (-1: none of its keys exist) and how many of its keys exist
+            const int slot = (unsigned)cur.page < (unsigned)pg.n_pages ? cur.page * pg.page_size + key0 % pg.page_size : -1;
+            const int count = slot < 0 ? 0 : min(16, cur.keys - key0);
+            for (int i = 0; i < cur.n; ++i) {
+                const int h = __shfl_sync(0xffffffffu, cur.h, 4 * i);
+                if (__shfl_sync(0xffffffffu, (int)cur.first, 4 * i)) {
+                    const int qs = nq % a.n_q, seq = __shfl_sync(0xffffffffu, cur.seq, 4 * i);
+                    if (nq >= (uint32_t)a.n_q && !warp_wait(&ms->q_empty[qs], ((nq / a.n_q) - 1) & 1, s_abort)) { ok = false; break; }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&ms->q_full[qs], q_bytes);
+                        bulk_load(sm + C::OFF_Q + qs * q_bytes, a.q + seq * a.ld_q + (int64_t)h * q_bytes, q_bytes, &ms->q_full[qs]);
+                    }
+                    ++nq;
                 }
                 const int st = n % C::NS;
                 if (n >= (uint32_t)C::NS && !warp_wait(&ms->empty[st], ((n / C::NS) - 1) & 1, s_abort)) { ok = false; break; }
-                const int l0 = ((t - p.t0) & 7) * 4, left = len - t * KT;
                 uint8_t *kt = sm + st * C::STAGE, *vt = kt + C::TILE;
-                // subtile j: its first pool position and how many of its keys exist
-                const int my_slot = __shfl_sync(0xffffffffu, slots, l0 + (lane & 3));
-                if (lane < CW) ms->count[st][lane] = my_slot < 0 ? 0 : min(16, left - lane * 16);
-                const int per_box = a.box >> 4, boxes = KT / a.box;
-                const int box_slot = __shfl_sync(0xffffffffu, slots, l0 + ((lane * per_box) & 3));
+                if ((lane >> 2) == i) ms->count[st][lane & 3] = count;
+                const int box_slot = __shfl_sync(0xffffffffu, slot, 4 * i + ((lane * per_box) & 3));
                 const bool load = lane < boxes && box_slot >= 0;
                 const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
-                __syncwarp();
                 if (lane == 0) mbar_arrive_expect_tx(&ms->full[st], loads * 2 * a.box * C::ROW);
                 __syncwarp();
                 if (load) {
                     const int off = lane * a.box * (Q8 ? C::ROW : 128);
 #pragma unroll
                     for (int hh = 0; hh < (Q8 ? 1 : D / 64); ++hh) {
-                        tma_load_3d(kt + hh * KT * 128 + off, &tm_k, &ms->full[st], hh * 64, box_slot, p.h);
-                        tma_load_3d(vt + hh * KT * 128 + off, &tm_v, &ms->full[st], hh * 64, box_slot, p.h);
+                        tma_load_3d(kt + hh * KT * 128 + off, &tm_k, &ms->full[st], hh * 64, box_slot, h);
+                        tma_load_3d(vt + hh * KT * 128 + off, &tm_v, &ms->full[st], hh * 64, box_slot, h);
                     }
                 }
                 if constexpr (Q8) {
                     uint8_t *sc = vt + C::TILE;
 #pragma unroll
-                    for (int i = 0; i < 2 * KT / 32; ++i) {
-                        const int key = (i * 32 + lane) & (KT - 1), is_v = i / (KT / 32);
-                        const int s = __shfl_sync(0xffffffffu, slots, l0 + (key >> 4));
-                        const bool valid = s >= 0 && key < left;
-                        const uint16_t *src = (is_v ? a.vs : a.ks) + (valid ? (int64_t)(s + (key & 15)) * a.s_tok + p.h * a.s_head : 0);
+                    for (int x = 0; x < 2 * KT / 32; ++x) {
+                        const int key = (x * 32 + lane) & (KT - 1), is_v = x / (KT / 32);
+                        const int sl = __shfl_sync(0xffffffffu, slot, 4 * i + (key >> 4));
+                        const bool valid = (key & 15) < __shfl_sync(0xffffffffu, count, 4 * i + (key >> 4));
+                        const uint16_t *src = (is_v ? a.vs : a.ks) + (valid ? (int64_t)(sl + (key & 15)) * a.s_tok + h * a.s_head : 0);
                         cp_async_zfill<C::NB * 2>(sc + is_v * C::SC + key * C::NB * 2, src, valid);
                     }
                     cp_async_arrive(&ms->full[st]);
@@ -308,7 +344,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                 const uint32_t last = st + ((n - 1 - st) / C::NS) * C::NS;
                 mbar_wait(&ms->full[st], (last / C::NS) & 1, &never, 200000000ull);
             }
-            if (nq > 0) mbar_wait(&ms->q_full, (nq - 1) & 1, &never, 200000000ull);
+            for (uint32_t qs = 0; qs < (uint32_t)a.n_q && qs < nq; ++qs) {
+                const uint32_t last = qs + ((nq - 1 - qs) / a.n_q) * a.n_q;
+                mbar_wait(&ms->q_full[qs], (last / a.n_q) & 1, &never, 200000000ull);
+            }
         }
     } else {
         // ------------------------------------------------------------------ consumers
@@ -320,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         Piece p;
         // sequences without keys have no unit in the list
         for (int i = blockIdx.x; i < pg.n_seq; i += gridDim.x) {
-            if (Walk::keys(pg, i) > 0) continue;
+            if (keys_of(pg, i) > 0) continue;
             for (int e = threadIdx.x; e < a.H_q * D; e += 32 * CW) store_out<DT>(a.out, (int64_t)i * a.H_q * D + e, 0.f);
             if (a.lse)
                 for (int e = threadIdx.x; e < a.H_q; e += 32 * CW) a.lse[(int64_t)i * a.H_q + e] = -INFINITY;
@@ -328,7 +367,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         while (walk.next(pg, a.H_kv, p)) {
             // the group's queries as the second operand of S^T: lane (g, t4) holds head g's eight values from
             // dimension 32 i + 8 t4 (q8_0, i a block) or 64 (i / 2) + 8 (t4 + 4 (i % 2)) (f16), for two steps each
-            ok = ok && warp_wait(&ms->q_full, nq & 1, s_abort);
+            const int qs = nq % a.n_q;
+            const uint32_t q_at = smem_u32(sm + C::OFF_Q) + qs * a.G * D * C::ESZ;
+            ok = ok && warp_wait(&ms->q_full[qs], (nq / a.n_q) & 1, s_abort);
             uint32_t qf[D / 16][NT][2];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
@@ -338,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                     const int head = nt * 8 + g;
                     uint32_t w[4] = {0u, 0u, 0u, 0u};
                     if (head < a.G) {
-                        const uint32_t at = smem_u32(sm + C::OFF_Q) + (head * D + dim) * C::ESZ;
+                        const uint32_t at = q_at + (head * D + dim) * C::ESZ;
                         const uint4 x = lds128(at);
                         const uint32_t xi[4] = {x.x, x.y, x.z, x.w};
                         if constexpr (DT == KVC_IN_F16) {
@@ -359,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ms->q_empty);
+            if (lane == 0) mbar_arrive(&ms->q_empty[qs]);
             ++nq;
 
             float o[C::MT][NT][4], m[NT][2], l[NT][2];
@@ -695,16 +736,17 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_paged_kernel(const Ar
 }
 
 template <int D, bool Q8, int DT, int NT>
-int launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const PagedView &pg, const Args &a, cudaStream_t s) {
+int launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const PagedView &pg, Args a, cudaStream_t s) {
     using C = Cfg<D, Q8, DT, NT>;
-    if (allow_dynamic_smem((const void *)decode_paged_kernel<D, Q8, DT, NT>, C::ALLOC) != KVC_OK) return KVC_ECUDA;
+    a.n_q = min(MAX_NQ, C::Q_ROOM / (a.G * D * C::ESZ));
+    if (allow_dynamic_smem((const void *)decode_paged_kernel<D, Q8, DT, NT>, SMEM_BUDGET) != KVC_OK) return KVC_ECUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.n_slots);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = C::ALLOC;
+    cfg.dynamicSmemBytes = SMEM_BUDGET;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
