@@ -74,10 +74,10 @@ def _load():
         "kv_cache_append_batch": (ctypes.c_int, [P(kvc_cache), I32, I32, P(I32), VP, VP, I32, VP]),
         "kv_state_get_heads": (ctypes.c_int, [P(kvc_cache), I32, I32, I32, VP, SZ, VP]),
         "kv_state_set_heads": (ctypes.c_int, [P(kvc_cache), I32, VP, SZ, P(I32), VP]),
-        "kv_paged_append": (ctypes.c_int, [P(kvc_cache), P(kvc_pages), I32, VP, I32, VP, VP, I64, I64, I32, VP]),
-        "kv_paged_read": (ctypes.c_int, [P(kvc_cache), P(kvc_pages), I32, VP, I32, VP, VP, I32, VP]),
+        "kv_paged_append": (ctypes.c_int, [VP, VP, I32, VP, I32, VP, VP, I64, I64, I32, VP]),
+        "kv_paged_read": (ctypes.c_int, [VP, VP, I32, VP, I32, VP, VP, I32, VP]),
         "kvc_paged_scratch_bytes": (ctypes.c_int, [P(kvc_desc), I32, I32, P(SZ)]),
-        "decode_attn_paged": (ctypes.c_int, [P(kvc_cache), P(kvc_pages), I32, VP, I64, I32, I32, VP, VP, VP, SZ, VP]),
+        "decode_attn_paged": (ctypes.c_int, [VP, VP, I32, VP, I64, I32, I32, VP, VP, VP, SZ, VP]),
         "kvc_packed_scratch_bytes": (ctypes.c_int, [I32, I32, I32, I32, I32, P(SZ)]),
         "attn_packed": (ctypes.c_int, [VP, VP, VP, I64, I64, I64, I32, VP, VP, I32, I32, I32, I32, I32, I32, VP, VP,
                                        VP, SZ, VP]),
@@ -158,6 +158,7 @@ class KVCache:
         _check(_lib().kvc_cache_init(ctypes.byref(self.c), ctypes.byref(self.desc), _ptr(self._bufs[0]),
                                   _ptr(self._bufs[1]) if scales else ctypes.c_void_p(0), _ptr(self._bufs[2]),
                                   _ptr(self._bufs[3]) if scales else ctypes.c_void_p(0)), "kvc_cache_init")
+        self.addr, self.cuda = ctypes.addressof(self.c), self._bufs[0].device
 
     def _shape(self, last):
         if self.layout == "head_major":
@@ -406,65 +407,86 @@ class PageTable:
         self.table, self.lengths, self.page_size = table, lengths, int(page_size)
         self.n_seq, self.device = table.shape[0], table.device
         self.c = kvc_pages(table.data_ptr(), lengths.data_ptr(), table.shape[0], table.shape[1], self.page_size)
-        self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self.c)
 
 
-def _on(device):
-    """The raw current stream of `device`, which has to be the current device for the launches that follow."""
-    if torch.cuda.current_device() != device.index:
+# The calls below are made once a layer and step with a few rows, where the host's time counts: they look at each
+# attribute once and pass plain integers.
+
+def _on(device, stream):
+    """The raw stream to launch on: `stream`, or the current one of `device`, which has to be the current device."""
+    index = device.index
+    if torch._C._cuda_getDevice() != index:
         raise ValueError("the tensors are on %s, which is not the current device" % device)
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _packed_rows(t, what, heads, head_dim, dtype, device):
     """Distance between tokens (elements) of a [rows][heads][head_dim] tensor with contiguous heads."""
-    if t.device != device or t.dtype != dtype or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or t.dtype != dtype or t.device != device:
         raise ValueError("%s must be a %s tensor [rows][%d][%d] on %s" % (what, dtype, heads, head_dim, device))
     ld, hs, es = t.stride()
     if es != 1 or (hs != head_dim and heads != 1):
         raise ValueError("%s must have contiguous heads" % what)
-    return ld if t.shape[0] > 1 else heads * head_dim
+    return ld if shape[0] > 1 else heads * head_dim
 
 
 def _starts(t, what, n_seq, device):
-    if t.dtype != torch.int32 or t.device != device or t.shape != (n_seq + 1,) or not t.is_contiguous():
+    if t.shape != (n_seq + 1,) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor [n_seq + 1] on %s" % (what, device))
     return t.data_ptr()
 
 
-def _output(t, what, shape, dtype, device):
+def _output(t, what, shape, dtype, device, like=None):
     if t is None:
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor %s on %s" % (what, dtype, list(shape), device))
     return t
+
+
+def _bytes(scratch, device):
+    if scratch.device != device or not scratch.is_contiguous():
+        raise ValueError("scratch must be a contiguous tensor on %s" % device)
+    return scratch.nbytes
+
+
+def _pool(cache, pages):
+    if cache.cuda != pages.device:
+        raise ValueError("the pool is on %s, its pages on %s" % (cache.cuda, pages.device))
+    return pages.device
 
 
 def kv_paged_append(cache, layer, pages, row_start, k, v, stream=None):
     """Store packed rows k, v [n_rows][H_kv][D]: rows [row_start[i], row_start[i + 1]) are the last positions of
     sequence i (pages.lengths counts them), quantised or rounded as kv_cache_append does."""
-    dev, n = pages.device, k.shape[0]
-    ld_k = _packed_rows(k, "k", cache.n_head_kv, cache.head_dim, k.dtype, dev)
-    ld_v = _packed_rows(v, "v", cache.n_head_kv, cache.head_dim, k.dtype, dev)
-    if v.shape[0] != n or k.dtype not in DTYPES or cache.device.type != "cuda":
+    dev, dtype, code = _pool(cache, pages), k.dtype, DTYPES.get(k.dtype)
+    ld_k = _packed_rows(k, "k", cache.n_head_kv, cache.head_dim, dtype, dev)
+    ld_v = _packed_rows(v, "v", cache.n_head_kv, cache.head_dim, dtype, dev)
+    n = k.shape[0]
+    if v.shape[0] != n or code is None:
         raise ValueError("k and v must have the same rows and be f32, bf16 or f16")
-    st = _lib().kv_paged_append(ctypes.byref(cache.c), pages.ref, layer, _starts(row_start, "row_start", pages.n_seq, dev),
-                                n, k.data_ptr(), v.data_ptr(), ld_k, ld_v, DTYPES[k.dtype],
-                                _on(dev) if stream is None else stream.cuda_stream)
-    _check(st, "kv_paged_append")
+    st = _lib().kv_paged_append(cache.addr, pages.addr, layer, _starts(row_start, "row_start", pages.n_seq, dev), n,
+                                k.data_ptr(), v.data_ptr(), ld_k, ld_v, code, _on(dev, stream))
+    if st:
+        raise KvcError(st, "kv_paged_append")
 
 
 def kv_paged_read(cache, layer, pages, row_start, n_rows, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """The values the pool holds for packed rows (as in kv_paged_append): k, v [n_rows][H_kv][D] in dtype."""
-    dev = pages.device
-    if dtype not in DTYPES:
+    dev, code = _pool(cache, pages), DTYPES.get(dtype)
+    if code is None:
         raise ValueError("dtype must be f32, bf16 or f16")
     shape = (n_rows, cache.n_head_kv, cache.head_dim)
-    k, v = _output(k, "k", shape, dtype, dev), _output(v, "v", shape, dtype, dev)
-    st = _lib().kv_paged_read(ctypes.byref(cache.c), pages.ref, layer, _starts(row_start, "row_start", pages.n_seq, dev),
-                              n_rows, k.data_ptr(), v.data_ptr(), DTYPES[dtype],
-                              _on(dev) if stream is None else stream.cuda_stream)
-    _check(st, "kv_paged_read")
+    k = _output(k, "k", shape, dtype, dev)
+    v = _output(v, "v", shape, dtype, dev, k)
+    st = _lib().kv_paged_read(cache.addr, pages.addr, layer, _starts(row_start, "row_start", pages.n_seq, dev), n_rows,
+                              k.data_ptr(), v.data_ptr(), code, _on(dev, stream))
+    if st:
+        raise KvcError(st, "kv_paged_read")
     return k, v
 
 
@@ -479,22 +501,21 @@ def paged_scratch(cache, n_seq, n_head_q):
 def decode_attn_paged(cache, layer, pages, q, out=None, lse=None, scratch=None, stream=None):
     """Attention of one token q[i] [H_q][D] of each sequence over its pages.lengths[i] keys; returns out
     [n_seq][H_q][D] in q's type.  lse: None, or a float32 tensor [n_seq][H_q] to fill."""
-    dev, n = pages.device, pages.n_seq
-    if q.dim() != 3 or q.shape[0] != n or q.dtype not in DTYPES:
+    dev, n, dtype, shape = _pool(cache, pages), pages.n_seq, q.dtype, q.shape
+    code = DTYPES.get(dtype)
+    if len(shape) != 3 or shape[0] != n or code is None:
         raise ValueError("q must be an f32, bf16 or f16 tensor [n_seq][H_q][D]")
-    hq = q.shape[1]
-    ld = _packed_rows(q, "q", hq, cache.head_dim, q.dtype, dev)
-    out = _output(out, "out", (n, hq, cache.head_dim), q.dtype, dev)
+    hq = shape[1]
+    ld = _packed_rows(q, "q", hq, cache.head_dim, dtype, dev)
+    out = _output(out, "out", shape, dtype, dev, q)
     if lse is not None:
-        lse = _output(lse, "lse", (n, hq), torch.float32, dev)
+        lse = _output(lse, "lse", (n, hq), torch.float32, dev).data_ptr()
     if scratch is None:
         scratch = paged_scratch(cache, n, hq)
-    _need(scratch, "scratch")
-    st = _lib().decode_attn_paged(ctypes.byref(cache.c), pages.ref, layer, q.data_ptr(), ld, DTYPES[q.dtype], hq,
-                                  out.data_ptr(), None if lse is None else lse.data_ptr(), scratch.data_ptr(),
-                                  scratch.numel() * scratch.element_size(),
-                                  _on(dev) if stream is None else stream.cuda_stream)
-    _check(st, "decode_attn_paged")
+    st = _lib().decode_attn_paged(cache.addr, pages.addr, layer, q.data_ptr(), ld, code, hq, out.data_ptr(), lse,
+                                  scratch.data_ptr(), _bytes(scratch, dev), _on(dev, stream))
+    if st:
+        raise KvcError(st, "decode_attn_paged")
     return out
 
 
@@ -510,28 +531,28 @@ def attn_packed(q, k, v, q_start, k_start=None, out=None, lse=None, scratch=None
     """Causal attention of packed prompts: q [n_q][H_q][D], k and v [n_k][H_kv][D] (bf16 or f16); sequence s has
     query rows [q_start[s], q_start[s + 1]) and keys [k_start[s], k_start[s + 1]) (q_start when None), its queries
     being its last positions.  Returns out like q, contiguous.  lse: None, or a float32 [n_q][H_q] to fill."""
-    dev = q.device
-    if q.dim() != 3 or k.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16):
+    dev, dtype, qshape, kshape = q.device, q.dtype, q.shape, k.shape
+    if len(qshape) != 3 or len(kshape) != 3 or dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("q, k and v must be bf16 or f16 tensors [rows][heads][D]")
-    (n_q, hq, d), (n_k, hkv, _) = q.shape, k.shape
-    n_seq = q_start.shape[0] - 1
-    ld_q = _packed_rows(q, "q", hq, d, q.dtype, dev)
-    ld_k, ld_v = _packed_rows(k, "k", hkv, d, q.dtype, dev), _packed_rows(v, "v", hkv, d, q.dtype, dev)
-    if v.shape != k.shape or not q.is_cuda:
+    if v.shape != kshape or dev.type != "cuda":
         raise ValueError("k and v must have the same rows, on a CUDA device")
+    n_q, hq, d = qshape
+    n_k, hkv = kshape[0], kshape[1]
+    n_seq = q_start.shape[0] - 1
+    ld_q = _packed_rows(q, "q", hq, d, dtype, dev)
+    ld_k, ld_v = _packed_rows(k, "k", hkv, d, dtype, dev), _packed_rows(v, "v", hkv, d, dtype, dev)
     qs = _starts(q_start, "q_start", n_seq, dev)
     ks = qs if k_start is None else _starts(k_start, "k_start", n_seq, dev)
-    out = _output(out, "out", (n_q, hq, d), q.dtype, dev)
+    out = _output(out, "out", qshape, dtype, dev, q)
     if lse is not None:
-        lse = _output(lse, "lse", (n_q, hq), torch.float32, dev)
+        lse = _output(lse, "lse", (n_q, hq), torch.float32, dev).data_ptr()
     if scratch is None:
         scratch = packed_scratch(n_q, n_seq, hq, hkv, d, dev)
-    _need(scratch, "scratch")
-    st = _lib().attn_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), ld_q, ld_k, ld_v, DTYPES[q.dtype], qs, ks, n_seq,
-                            n_q, n_k, hq, hkv, d, out.data_ptr(), None if lse is None else lse.data_ptr(),
-                            scratch.data_ptr(), scratch.numel() * scratch.element_size(),
-                            _on(dev) if stream is None else stream.cuda_stream)
-    _check(st, "attn_packed")
+    st = _lib().attn_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), ld_q, ld_k, ld_v, DTYPES[dtype], qs, ks, n_seq,
+                            n_q, n_k, hq, hkv, d, out.data_ptr(), lse, scratch.data_ptr(), _bytes(scratch, dev),
+                            _on(dev, stream))
+    if st:
+        raise KvcError(st, "attn_packed")
     return out
 
 
