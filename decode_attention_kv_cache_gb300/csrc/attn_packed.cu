@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(128) packed_kernel(const PackedArgs a, float s
     const int row = (int)(w / a.H_q), h = (int)(w - (int64_t)row * a.H_q), kvh = h / (a.H_q / a.H_kv);
     if (row >= a.n_q) return;
     const int seq = find_seq(a.q_start, a.n_seq, row);
-    if (seq < 0) return;
+    if (row < __ldcg(a.q_start + seq) || row >= __ldcg(a.q_start + seq + 1)) return;
     const int k0 = max(__ldcg(a.k_start + seq), 0), k1 = min(__ldcg(a.k_start + seq + 1), a.n_k);
     const int last = k1 - (__ldcg(a.q_start + seq + 1) - row);   // the last key row this row sees
     const T *q = static_cast<const T *>(a.q) + row * a.ld_q + (int64_t)h * D;

@@ -17,6 +17,7 @@ namespace kvc {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int APPEND_PASSES = 2, READ_PASSES = 4;
 
 struct Pool {
     void *kq, *vq;
@@ -30,120 +31,186 @@ Pool pool_of(const kvc_cache &c, int layer) {
             c.d.n_head_kv, c.d.head_dim};
 }
 
-// One thread takes eight consecutive values of a row, of K and of V: their loads are in flight together and
-// share the search for the page.  The four lanes of a q8_0 block find its amax by two shuffles, so input,
-// codes and scales are all read and written in consecutive lanes' order.
-template <int DT, bool Q8>
+// A CTA takes THREADS * PASSES consecutive units of the packed rows (a unit: the values of one load, of K and
+// of V).  The pool positions of its rows are found once, one row per thread, into shared memory.
+struct Span {
+    int row0;      // the CTA's first row
+    int rem;       // its first unit, counted from that row's first
+    int rows;      // rows that it touches
+};
+
+__device__ __forceinline__ Span span_of(int64_t n_units, int units_per_row, int units_per_cta) {
+    const int64_t u0 = (int64_t)blockIdx.x * units_per_cta;
+    Span s;
+    s.row0 = (int)(u0 / units_per_row);
+    s.rem = (int)(u0 - (int64_t)s.row0 * units_per_row);
+    const int n = (int)min((int64_t)units_per_cta, n_units - u0);
+    s.rows = (s.rem + n - 1) / units_per_row + 1;
+    return s;
+}
+
+// One thread takes eight consecutive values of a row, of K and of V, PASSES times; all of its loads are in flight
+// before the first value is used, and the look-ups overlap them.  The four lanes of a q8_0 block find its amax by
+// two shuffles, so input, codes and scales are all read and written in consecutive lanes' order.
+template <int DT, bool Q8, int PASSES>
 __global__ void __launch_bounds__(THREADS)
     paged_append_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t ld_k, int64_t ld_v,
                         int64_t n_units, int units_per_row, const int32_t *row_start, const PagedView pg,
                         const Pool p) {
     asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ int slots[THREADS * PASSES / 4 + 1];   // a row has four units or more
+    const Span sp = span_of(n_units, units_per_row, THREADS * PASSES);
+    const int64_t left = n_units - (int64_t)blockIdx.x * (THREADS * PASSES);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t u = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-    const bool live = u < n_units;   // a multiple of four: whole blocks
-    const int row = live ? (int)(u / units_per_row) : 0;
-    const int e = live ? (int)(u - (int64_t)row * units_per_row) * 8 : 0;   // first value within the row
-    float x[2][8] = {};
-    if (live) {
-        load_inputs8<DT>(k, row * ld_k + e, x[0]);
-        load_inputs8<DT>(v, row * ld_v + e, x[1]);
+    Raw8<DT> raw[PASSES][2];
+    int r[PASSES], e[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int u = i * THREADS + threadIdx.x;
+        r[i] = (sp.rem + u) / units_per_row;
+        e[i] = (sp.rem + u - r[i] * units_per_row) * 8;
+        if (u >= left) r[i] = -1;   // a multiple of four units: whole blocks
+        if (r[i] >= 0) {
+            raw[i][0] = load_raw8<DT>(k, (sp.row0 + r[i]) * ld_k + e[i]);
+            raw[i][1] = load_raw8<DT>(v, (sp.row0 + r[i]) * ld_v + e[i]);
+        } else {
+            raw[i][0] = raw[i][1] = Raw8<DT>{};
+        }
     }
-    const int slot = live ? row_slot(pg, row_start, row) : -1;
-    const int head = e / p.D, c = e - head * p.D;
-    const int64_t at = p.layer * p.g.c_layer + slot * p.g.c_tok + head * p.g.c_head + c;
+    row_slots(pg, row_start, sp.row0, sp.rows, slots);
+    __syncthreads();
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        if constexpr (Q8) {
-            uint32_t w[2];
-            const uint16_t scale = q8_0_quantize_quad(x[kv], w);
-            if (slot >= 0) {
-                *reinterpret_cast<uint2 *>(static_cast<int8_t *>(kv ? p.vq : p.kq) + at) = make_uint2(w[0], w[1]);
-                if ((c & 31) == 0)
-                    (kv ? p.vs : p.ks)[p.layer * p.g.s_layer + slot * p.g.s_tok + head * p.g.s_head + (c >> 5)] = scale;
+    for (int i = 0; i < PASSES; ++i) {
+        const int slot = r[i] >= 0 ? slots[r[i]] : -1;
+        const int head = e[i] / p.D, c = e[i] - head * p.D;
+        const int64_t at = p.layer * p.g.c_layer + slot * p.g.c_tok + head * p.g.c_head + c;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            float x[8];
+            widen8<DT>(raw[i][kv], x);
+            if constexpr (Q8) {
+                uint32_t w[2];
+                const uint16_t scale = q8_0_quantize_quad(x, w);
+                if (slot >= 0) {
+                    *reinterpret_cast<uint2 *>(static_cast<int8_t *>(kv ? p.vq : p.kq) + at) = make_uint2(w[0], w[1]);
+                    if ((c & 31) == 0)
+                        (kv ? p.vs : p.ks)[p.layer * p.g.s_layer + slot * p.g.s_tok + head * p.g.s_head + (c >> 5)] = scale;
+                }
+            } else if (slot >= 0) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = ptx::pack_half2(x[2 * j], x[2 * j + 1]);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(kv ? p.vq : p.kq) + at) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
             }
-        } else if (slot >= 0) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = ptx::pack_half2(x[kv][2 * i], x[kv][2 * i + 1]);
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(kv ? p.vq : p.kq) + at) =
-                make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
 
-__device__ __forceinline__ uint32_t pack2(int dtype_bf16, float lo, float hi) {
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
-    if (dtype_bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    if (DT == KVC_IN_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
+// eight 32-bit words to global memory: in one access where the address is a multiple of 32 (WIDE)
+template <bool WIDE>
+__device__ __forceinline__ void store8(void *dst, const uint32_t (&w)[8]) {
+    if (WIDE) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // One thread takes the values of one 16-byte load of the pool (16 codes of one block, or 8 fp16 values), of K
-// and of V.
-template <int DT, bool Q8>
+// and of V, PASSES times, all loads in flight together.  32-byte stores where the outputs allow them.
+template <int DT, bool Q8, int PASSES, bool WIDE>
 __global__ void __launch_bounds__(THREADS)
     paged_read_kernel(void *__restrict__ k, void *__restrict__ v, int64_t n_units, int units_per_row,
                       const int32_t *row_start, const PagedView pg, const Pool p) {
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int N = Q8 ? 16 : 8;
-    const int64_t u = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-    if (u >= n_units) return;
-    const int row = (int)(u / units_per_row);
-    const int e = (int)(u - (int64_t)row * units_per_row) * N;
-    const int slot = row_slot(pg, row_start, row);
-    if (slot == -2) return;
-    const int head = e / p.D, c = e - head * p.D;
-    const int64_t at = p.layer * p.g.c_layer + slot * p.g.c_tok + head * p.g.c_head + c;
-    uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    float d[2] = {0.f, 0.f};
-    if (slot >= 0) {
+    __shared__ int slots[THREADS * PASSES / 2 + 1];   // a row has two units or more
+    const Span sp = span_of(n_units, units_per_row, THREADS * PASSES);
+    const int64_t u0 = (int64_t)blockIdx.x * (THREADS * PASSES), left = n_units - u0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    row_slots(pg, row_start, sp.row0, sp.rows, slots);
+    __syncthreads();
+    uint4 raw[PASSES][2];
+    uint16_t d[PASSES][2];
+    int slot[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int u = i * THREADS + threadIdx.x, r = (sp.rem + u) / units_per_row;
+        const int e = (sp.rem + u - r * units_per_row) * N, head = e / p.D, c = e - head * p.D;
+        slot[i] = u < left ? slots[r] : -2;
+        raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        d[i][0] = d[i][1] = 0;
+        if (slot[i] < 0) continue;
+        const int64_t at = p.layer * p.g.c_layer + slot[i] * p.g.c_tok + head * p.g.c_head + c;
+        const int64_t sat = p.layer * p.g.s_layer + slot[i] * p.g.s_tok + head * p.g.s_head + (c >> 5);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-            raw[kv] = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(kv ? p.vq : p.kq) +
-                                                             at * (Q8 ? 1 : 2)));
-            if (Q8)
-                d[kv] = __half2float(__ushort_as_half(__ldcg(
-                    (kv ? p.vs : p.ks) + p.layer * p.g.s_layer + slot * p.g.s_tok + head * p.g.s_head + (c >> 5))));
+            raw[i][kv] = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(kv ? p.vq : p.kq) +
+                                                                at * (Q8 ? 1 : 2)));
+            if (Q8) d[i][kv] = __ldcg((kv ? p.vs : p.ks) + sat);
         }
     }
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        float x[N];
-        const uint32_t w[4] = {raw[kv].x, raw[kv].y, raw[kv].z, raw[kv].w};
+    for (int i = 0; i < PASSES; ++i) {
+        if (slot[i] == -2) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (Q8) {
+        for (int kv = 0; kv < 2; ++kv) {
+            float x[N];
+            const uint32_t w[4] = {raw[i][kv].x, raw[i][kv].y, raw[i][kv].z, raw[i][kv].w};
+            const float s = Q8 ? __half2float(__ushort_as_half(d[i][kv])) : 0.f;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) x[4 * i + b] = (float)(int8_t)(w[i] >> (8 * b)) * d[kv];
-            } else {
-                x[2 * i] = __half2float(__ushort_as_half((unsigned short)(w[i] & 0xFFFF)));
-                x[2 * i + 1] = __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (Q8) {
+                    // a code plus 128 in the low bits of 2^23 is the float 2^23 + 128 + code, exactly
+                    const uint32_t u = w[j] ^ 0x80808080u;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        x[4 * j + b] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540 + b)) - 8388736.f) * s;
+                } else {
+                    x[2 * j] = __half2float(__ushort_as_half((unsigned short)(w[j] & 0xFFFF)));
+                    x[2 * j + 1] = __half2float(__ushort_as_half((unsigned short)(w[j] >> 16)));
+                }
             }
-        }
-        uint8_t *dst = static_cast<uint8_t *>(kv ? v : k) + u * N * (DT == KVC_IN_F32 ? 4 : 2);
-        if constexpr (DT == KVC_IN_F32) {
+            const int64_t u = u0 + i * THREADS + threadIdx.x;
+            uint8_t *dst = static_cast<uint8_t *>(kv ? v : k) + u * N * (DT == KVC_IN_F32 ? 4 : 2);
+            if constexpr (DT == KVC_IN_F32) {
 #pragma unroll
-            for (int i = 0; i < N; i += 4)
-                *reinterpret_cast<float4 *>(dst + 4 * i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        } else {
+                for (int j = 0; j < N; j += 8) {
+                    uint32_t o[8];
 #pragma unroll
-            for (int i = 0; i < N; i += 8) {
-                uint32_t o[4];
+                    for (int b = 0; b < 8; ++b) o[b] = __float_as_uint(x[j + b]);
+                    store8<WIDE>(dst + 4 * j, o);
+                }
+            } else if constexpr (Q8) {
+                uint32_t o[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = pack2(DT == KVC_IN_BF16, x[i + 2 * j], x[i + 2 * j + 1]);
-                *reinterpret_cast<uint4 *>(dst + 2 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int b = 0; b < 8; ++b) o[b] = pack2<DT>(x[2 * b], x[2 * b + 1]);
+                store8<WIDE>(dst, o);
+            } else {
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
+                                                             pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
             }
         }
     }
 }
 
-cudaLaunchConfig_t config(int64_t n_units, cudaLaunchAttribute *attr, cudaStream_t s) {
+cudaLaunchConfig_t config(int64_t n_units, int units_per_cta, cudaLaunchAttribute *attr, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((n_units + THREADS - 1) / THREADS));
+    cfg.gridDim = dim3((unsigned)((n_units + units_per_cta - 1) / units_per_cta));
     cfg.blockDim = dim3(THREADS);
     cfg.stream = s;
     cfg.attrs = attr;
@@ -151,26 +218,44 @@ cudaLaunchConfig_t config(int64_t n_units, cudaLaunchAttribute *attr, cudaStream
     return cfg;
 }
 
+// Several passes only where there are enough units to keep every SM busy with several CTAs of that many.
+bool many(int64_t n_units, int passes) { return n_units >= (int64_t)THREADS * passes * 4 * sm_count(); }
+
+template <int DT, bool Q8, int PASSES>
+cudaError_t append_p(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int64_t n, int per_row,
+                     const void *k, const void *v, int64_t ld_k, int64_t ld_v, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config(n, THREADS * PASSES, attr, s);
+    return cudaLaunchKernelEx(&cfg, paged_append_kernel<DT, Q8, PASSES>, k, v, ld_k, ld_v, n, per_row, row_start,
+                              paged_view(c, pg), pool_of(c, layer));
+}
 template <int DT, bool Q8>
 cudaError_t append_t(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int n_rows,
                      const void *k, const void *v, int64_t ld_k, int64_t ld_v, cudaStream_t s) {
-    cudaLaunchAttribute attr[1];
     const int per_row = c.d.n_head_kv * (c.d.head_dim / 8);
     const int64_t n = (int64_t)n_rows * per_row;
-    const cudaLaunchConfig_t cfg = config(n, attr, s);
-    return cudaLaunchKernelEx(&cfg, paged_append_kernel<DT, Q8>, k, v, ld_k, ld_v, n, per_row, row_start,
-                              paged_view(c, pg), pool_of(c, layer));
+    return many(n, APPEND_PASSES)
+               ? append_p<DT, Q8, APPEND_PASSES>(c, pg, layer, row_start, n, per_row, k, v, ld_k, ld_v, s)
+               : append_p<DT, Q8, 1>(c, pg, layer, row_start, n, per_row, k, v, ld_k, ld_v, s);
 }
 
+template <int DT, bool Q8, int PASSES, bool WIDE>
+cudaError_t read_p(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int64_t n, int per_row,
+                   void *k, void *v, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config(n, THREADS * PASSES, attr, s);
+    return cudaLaunchKernelEx(&cfg, paged_read_kernel<DT, Q8, PASSES, WIDE>, k, v, n, per_row, row_start,
+                              paged_view(c, pg), pool_of(c, layer));
+}
 template <int DT, bool Q8>
 cudaError_t read_t(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int n_rows, void *k,
                    void *v, cudaStream_t s) {
-    cudaLaunchAttribute attr[1];
     const int per_row = c.d.n_head_kv * (c.d.head_dim / (Q8 ? 16 : 8));
     const int64_t n = (int64_t)n_rows * per_row;
-    const cudaLaunchConfig_t cfg = config(n, attr, s);
-    return cudaLaunchKernelEx(&cfg, paged_read_kernel<DT, Q8>, k, v, n, per_row, row_start, paged_view(c, pg),
-                              pool_of(c, layer));
+    const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31) == 0;
+    if (!wide) return read_p<DT, Q8, 1, false>(c, pg, layer, row_start, n, per_row, k, v, s);
+    return many(n, READ_PASSES) ? read_p<DT, Q8, READ_PASSES, true>(c, pg, layer, row_start, n, per_row, k, v, s)
+                                : read_p<DT, Q8, 1, true>(c, pg, layer, row_start, n, per_row, k, v, s);
 }
 
 int done(cudaError_t e) { return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? KVC_OK : KVC_ECUDA; }

@@ -19,18 +19,35 @@
 
 namespace kvc {
 
-// 8 consecutive input values (f32, bf16 or f16: DT is a kvc_dtype) from element index idx, read through L2
-// (a kernel just before the reader may have written them), as floats: bf16 and f16 widen exactly.
+// 8 consecutive input values (f32, bf16 or f16: DT is a kvc_dtype) as they lie in memory.
 template <int DT>
-__device__ __forceinline__ void load_inputs8(const void *base, int64_t idx, float (&x)[8]) {
+struct Raw8 {
+    uint4 u[DT == KVC_IN_F32 ? 2 : 1];
+};
+
+// Those from element index idx, read through L2 (a kernel just before the reader may have written them).
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_raw8(const void *base, int64_t idx) {
+    Raw8<DT> r;
     if constexpr (DT == KVC_IN_F32) {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + idx);
-        const float4 a = __ldcg(p), b = __ldcg(p + 1);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + idx);
+        r.u[0] = __ldcg(p);
+        r.u[1] = __ldcg(p + 1);
     } else {
-        const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + idx));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        r.u[0] = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + idx));
+    }
+    return r;
+}
+
+// As floats: bf16 and f16 widen exactly.
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw8<DT> &r, float (&x)[8]) {
+    if constexpr (DT == KVC_IN_F32) {
+        const uint4 a = r.u[0], b = r.u[1];
+        x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
+        x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y); x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
+    } else {
+        const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (DT == KVC_IN_BF16) {
@@ -42,6 +59,11 @@ __device__ __forceinline__ void load_inputs8(const void *base, int64_t idx, floa
             }
         }
     }
+}
+
+template <int DT>
+__device__ __forceinline__ void load_inputs8(const void *base, int64_t idx, float (&x)[8]) {
+    widen8<DT>(load_raw8<DT>(base, idx), x);
 }
 
 // The codes of N values of a block whose largest magnitude is amax, packed four to a word (byte i of word w
