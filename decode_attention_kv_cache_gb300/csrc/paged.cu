@@ -19,16 +19,29 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int APPEND_PASSES = 2, READ_PASSES = 4;
 
+// n / d for 32-bit n by a multiplication: floor(n (2^64 / d + 1) / 2^64), where the part that is too much,
+// n / 2^64, is below the 1/d that would be needed to reach the next integer.
+struct Div {
+    unsigned long long m;
+    __device__ __forceinline__ int operator()(int n) const { return (int)__umul64hi((unsigned long long)(unsigned)n, m); }
+};
+Div div_of(int d) { return {~0ull / d + 1}; }   // a row has two units or more, and so has a head
+
 struct Pool {
-    void *kq, *vq;
+    void *kq, *vq;             // of the layer
     uint16_t *ks, *vs;
-    Geom g;
-    int layer, H, D;
+    int64_t c_tok, c_head, s_tok, s_head;
+    Div per_row, per_head;     // units
+    int units_per_row, units_per_head;
 };
 
-Pool pool_of(const kvc_cache &c, int layer) {
-    return {c.k_q, c.v_q, static_cast<uint16_t *>(c.k_s), static_cast<uint16_t *>(c.v_s), geom_of(c.d), layer,
-            c.d.n_head_kv, c.d.head_dim};
+Pool pool_of(const kvc_cache &c, int layer, int values_per_unit) {
+    const Geom g = geom_of(c.d);
+    const int esz = c.d.type == KVC_Q8_0 ? 1 : 2, per_head = c.d.head_dim / values_per_unit, per_row = c.d.n_head_kv * per_head;
+    const int64_t at = layer * g.c_layer * esz, sat = c.d.type == KVC_Q8_0 ? layer * g.s_layer : 0;
+    return {static_cast<uint8_t *>(c.k_q) + at, static_cast<uint8_t *>(c.v_q) + at, static_cast<uint16_t *>(c.k_s) + sat,
+            static_cast<uint16_t *>(c.v_s) + sat, g.c_tok, g.c_head, g.s_tok, g.s_head, div_of(per_row),
+            div_of(per_head), per_row, per_head};
 }
 
 // A CTA takes THREADS * PASSES consecutive units of the packed rows (a unit: the values of one load, of K and
@@ -47,64 +60,6 @@ __device__ __forceinline__ Span span_of(int64_t n_units, int units_per_row, int 
     const int n = (int)min((int64_t)units_per_cta, n_units - u0);
     s.rows = (s.rem + n - 1) / units_per_row + 1;
     return s;
-}
-
-// One thread takes eight consecutive values of a row, of K and of V, PASSES times; all of its loads are in flight
-// before the first value is used, and the look-ups overlap them.  The four lanes of a q8_0 block find its amax by
-// two shuffles, so input, codes and scales are all read and written in consecutive lanes' order.
-template <int DT, bool Q8, int PASSES>
-__global__ void __launch_bounds__(THREADS)
-    paged_append_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t ld_k, int64_t ld_v,
-                        int64_t n_units, int units_per_row, const int32_t *row_start, const PagedView pg,
-                        const Pool p) {
-    asm volatile("griddepcontrol.launch_dependents;");
-    __shared__ int slots[THREADS * PASSES / 4 + 1];   // a row has four units or more
-    const Span sp = span_of(n_units, units_per_row, THREADS * PASSES);
-    const int64_t left = n_units - (int64_t)blockIdx.x * (THREADS * PASSES);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    Raw8<DT> raw[PASSES][2];
-    int r[PASSES], e[PASSES];
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int u = i * THREADS + threadIdx.x;
-        r[i] = (sp.rem + u) / units_per_row;
-        e[i] = (sp.rem + u - r[i] * units_per_row) * 8;
-        if (u >= left) r[i] = -1;   // a multiple of four units: whole blocks
-        if (r[i] >= 0) {
-            raw[i][0] = load_raw8<DT>(k, (sp.row0 + r[i]) * ld_k + e[i]);
-            raw[i][1] = load_raw8<DT>(v, (sp.row0 + r[i]) * ld_v + e[i]);
-        } else {
-            raw[i][0] = raw[i][1] = Raw8<DT>{};
-        }
-    }
-    row_slots(pg, row_start, sp.row0, sp.rows, slots);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int slot = r[i] >= 0 ? slots[r[i]] : -1;
-        const int head = e[i] / p.D, c = e[i] - head * p.D;
-        const int64_t at = p.layer * p.g.c_layer + slot * p.g.c_tok + head * p.g.c_head + c;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            float x[8];
-            widen8<DT>(raw[i][kv], x);
-            if constexpr (Q8) {
-                uint32_t w[2];
-                const uint16_t scale = q8_0_quantize_quad(x, w);
-                if (slot >= 0) {
-                    *reinterpret_cast<uint2 *>(static_cast<int8_t *>(kv ? p.vq : p.kq) + at) = make_uint2(w[0], w[1]);
-                    if ((c & 31) == 0)
-                        (kv ? p.vs : p.ks)[p.layer * p.g.s_layer + slot * p.g.s_tok + head * p.g.s_head + (c >> 5)] = scale;
-                }
-            } else if (slot >= 0) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = ptx::pack_half2(x[2 * j], x[2 * j + 1]);
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(kv ? p.vq : p.kq) + at) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-    }
 }
 
 template <int DT>
@@ -128,16 +83,73 @@ __device__ __forceinline__ void store8(void *dst, const uint32_t (&w)[8]) {
     }
 }
 
+// One thread takes eight consecutive values of a row, of K and of V, PASSES times; all of its loads are in flight
+// before the first value is used, and the look-ups overlap them.  The four lanes of a q8_0 block find its amax by
+// two shuffles, so input, codes and scales are all read and written in consecutive lanes' order.
+template <int DT, bool Q8, int PASSES>
+__global__ void __launch_bounds__(THREADS)
+    paged_append_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t ld_k, int64_t ld_v,
+                        int64_t n_units, const int32_t *row_start, const PagedView pg, const Pool p) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ int slots[THREADS * PASSES / 4 + 1];   // a row has four units or more
+    const Span sp = span_of(n_units, p.units_per_row, THREADS * PASSES);
+    const int64_t left = n_units - (int64_t)blockIdx.x * (THREADS * PASSES);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Raw8<DT> raw[PASSES][2];
+    int r[PASSES], e[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int u = i * THREADS + threadIdx.x;
+        r[i] = p.per_row(sp.rem + u);
+        e[i] = sp.rem + u - r[i] * p.units_per_row;
+        if (u >= left) r[i] = -1;   // a multiple of four units: whole blocks
+        if (r[i] >= 0) {
+            raw[i][0] = load_raw8<DT>(k, (sp.row0 + r[i]) * ld_k + e[i] * 8);
+            raw[i][1] = load_raw8<DT>(v, (sp.row0 + r[i]) * ld_v + e[i] * 8);
+        } else {
+            raw[i][0] = raw[i][1] = Raw8<DT>{};
+        }
+    }
+    row_slots(pg, row_start, sp.row0, sp.rows, slots);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int slot = r[i] >= 0 ? slots[r[i]] : -1;
+        const int head = p.per_head(e[i]), c = (e[i] - head * p.units_per_head) * 8;
+        const int64_t at = slot * p.c_tok + head * p.c_head + c;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            float x[8];
+            widen8<DT>(raw[i][kv], x);
+            if constexpr (Q8) {
+                uint32_t w[2];
+                const uint16_t scale = q8_0_quantize_quad(x, w);
+                if (slot >= 0) {
+                    *reinterpret_cast<uint2 *>(static_cast<int8_t *>(kv ? p.vq : p.kq) + at) = make_uint2(w[0], w[1]);
+                    if ((c & 31) == 0)
+                        (kv ? p.vs : p.ks)[slot * p.s_tok + head * p.s_head + (c >> 5)] = scale;
+                }
+            } else if (slot >= 0) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = ptx::pack_half2(x[2 * j], x[2 * j + 1]);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(kv ? p.vq : p.kq) + at) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+}
+
 // One thread takes the values of one 16-byte load of the pool (16 codes of one block, or 8 fp16 values), of K
 // and of V, PASSES times, all loads in flight together.  32-byte stores where the outputs allow them.
 template <int DT, bool Q8, int PASSES, bool WIDE>
 __global__ void __launch_bounds__(THREADS)
-    paged_read_kernel(void *__restrict__ k, void *__restrict__ v, int64_t n_units, int units_per_row,
-                      const int32_t *row_start, const PagedView pg, const Pool p) {
+    paged_read_kernel(void *__restrict__ k, void *__restrict__ v, int64_t n_units, const int32_t *row_start,
+                      const PagedView pg, const Pool p) {
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int N = Q8 ? 16 : 8;
     __shared__ int slots[THREADS * PASSES / 2 + 1];   // a row has two units or more
-    const Span sp = span_of(n_units, units_per_row, THREADS * PASSES);
+    const Span sp = span_of(n_units, p.units_per_row, THREADS * PASSES);
     const int64_t u0 = (int64_t)blockIdx.x * (THREADS * PASSES), left = n_units - u0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     row_slots(pg, row_start, sp.row0, sp.rows, slots);
@@ -147,14 +159,14 @@ __global__ void __launch_bounds__(THREADS)
     int slot[PASSES];
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-        const int u = i * THREADS + threadIdx.x, r = (sp.rem + u) / units_per_row;
-        const int e = (sp.rem + u - r * units_per_row) * N, head = e / p.D, c = e - head * p.D;
+        const int u = i * THREADS + threadIdx.x, r = p.per_row(sp.rem + u), e = sp.rem + u - r * p.units_per_row;
+        const int head = p.per_head(e), c = (e - head * p.units_per_head) * N;
         slot[i] = u < left ? slots[r] : -2;
         raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
         d[i][0] = d[i][1] = 0;
         if (slot[i] < 0) continue;
-        const int64_t at = p.layer * p.g.c_layer + slot[i] * p.g.c_tok + head * p.g.c_head + c;
-        const int64_t sat = p.layer * p.g.s_layer + slot[i] * p.g.s_tok + head * p.g.s_head + (c >> 5);
+        const int64_t at = slot[i] * p.c_tok + head * p.c_head + c;
+        const int64_t sat = slot[i] * p.s_tok + head * p.s_head + (c >> 5);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
             raw[i][kv] = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(kv ? p.vq : p.kq) +
@@ -222,12 +234,12 @@ cudaLaunchConfig_t config(int64_t n_units, int units_per_cta, cudaLaunchAttribut
 bool many(int64_t n_units, int passes) { return n_units >= (int64_t)THREADS * passes * 4 * sm_count(); }
 
 template <int DT, bool Q8, int PASSES>
-cudaError_t append_p(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int64_t n, int per_row,
+cudaError_t append_p(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int64_t n,
                      const void *k, const void *v, int64_t ld_k, int64_t ld_v, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = config(n, THREADS * PASSES, attr, s);
-    return cudaLaunchKernelEx(&cfg, paged_append_kernel<DT, Q8, PASSES>, k, v, ld_k, ld_v, n, per_row, row_start,
-                              paged_view(c, pg), pool_of(c, layer));
+    return cudaLaunchKernelEx(&cfg, paged_append_kernel<DT, Q8, PASSES>, k, v, ld_k, ld_v, n, row_start,
+                              paged_view(c, pg), pool_of(c, layer, 8));
 }
 template <int DT, bool Q8>
 cudaError_t append_t(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int n_rows,
@@ -235,17 +247,17 @@ cudaError_t append_t(const kvc_cache &c, const kvc_pages &pg, int layer, const i
     const int per_row = c.d.n_head_kv * (c.d.head_dim / 8);
     const int64_t n = (int64_t)n_rows * per_row;
     return many(n, APPEND_PASSES)
-               ? append_p<DT, Q8, APPEND_PASSES>(c, pg, layer, row_start, n, per_row, k, v, ld_k, ld_v, s)
-               : append_p<DT, Q8, 1>(c, pg, layer, row_start, n, per_row, k, v, ld_k, ld_v, s);
+               ? append_p<DT, Q8, APPEND_PASSES>(c, pg, layer, row_start, n, k, v, ld_k, ld_v, s)
+               : append_p<DT, Q8, 1>(c, pg, layer, row_start, n, k, v, ld_k, ld_v, s);
 }
 
 template <int DT, bool Q8, int PASSES, bool WIDE>
-cudaError_t read_p(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int64_t n, int per_row,
+cudaError_t read_p(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int64_t n,
                    void *k, void *v, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = config(n, THREADS * PASSES, attr, s);
-    return cudaLaunchKernelEx(&cfg, paged_read_kernel<DT, Q8, PASSES, WIDE>, k, v, n, per_row, row_start,
-                              paged_view(c, pg), pool_of(c, layer));
+    return cudaLaunchKernelEx(&cfg, paged_read_kernel<DT, Q8, PASSES, WIDE>, k, v, n, row_start,
+                              paged_view(c, pg), pool_of(c, layer, Q8 ? 16 : 8));
 }
 template <int DT, bool Q8>
 cudaError_t read_t(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int n_rows, void *k,
@@ -253,9 +265,9 @@ cudaError_t read_t(const kvc_cache &c, const kvc_pages &pg, int layer, const int
     const int per_row = c.d.n_head_kv * (c.d.head_dim / (Q8 ? 16 : 8));
     const int64_t n = (int64_t)n_rows * per_row;
     const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31) == 0;
-    if (!wide) return read_p<DT, Q8, 1, false>(c, pg, layer, row_start, n, per_row, k, v, s);
-    return many(n, READ_PASSES) ? read_p<DT, Q8, READ_PASSES, true>(c, pg, layer, row_start, n, per_row, k, v, s)
-                                : read_p<DT, Q8, 1, true>(c, pg, layer, row_start, n, per_row, k, v, s);
+    if (!wide) return read_p<DT, Q8, 1, false>(c, pg, layer, row_start, n, k, v, s);
+    return many(n, READ_PASSES) ? read_p<DT, Q8, READ_PASSES, true>(c, pg, layer, row_start, n, k, v, s)
+                                : read_p<DT, Q8, 1, true>(c, pg, layer, row_start, n, k, v, s);
 }
 
 int done(cudaError_t e) { return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? KVC_OK : KVC_ECUDA; }

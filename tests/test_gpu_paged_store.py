@@ -201,3 +201,33 @@ def test_pool_past_32_bit_offsets(kvc):
         assert np.array_equal(cache.codes(kv)[0, at:at + 50].cpu().numpy().reshape(-1, 32), q)
         ref = (q.astype(np.float32) * d.astype(np.float32).reshape(-1, 1)).reshape(50, 32, 128)
         assert np.array_equal(got.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_ties_near_ties_and_extreme_scales(kvc, dtype):
+    """Quotients at and around every half-integer, for scales over the whole range, against IEEE division."""
+    rng = np.random.default_rng(3)
+    rows, hkv, d = 256, 4, 128
+    lo, hi = (-14, 15) if dtype == "f16" else (-120, 120)
+    amax = np.ldexp(rng.uniform(1, 2, (rows, hkv, 4)), rng.integers(lo, hi, (rows, hkv, 4))).astype(np.float32)
+    amax = torch.from_numpy(amax).to(TYPES[dtype]).float().numpy()
+    step = amax / np.float32(127)
+    h = rng.integers(0, 127, (rows, hkv, 4, 32)) + 0.5
+    x = (step[..., None] * h.astype(np.float32)).astype(np.float32)
+    for _ in range(3):   # up to three floats to either side
+        side = rng.integers(-1, 2, x.shape)
+        x = np.where(side == 0, x, np.nextafter(x, np.where(side < 0, np.float32(0), np.float32(np.inf)))).astype(np.float32)
+    x = np.minimum(x, amax[..., None])
+    x[..., 5] = amax
+    x *= rng.choice([-1, 1], x.shape)
+    if dtype == "f32":
+        x[:8] *= np.float32(2.0 ** -30)       # down into the subnormal numbers
+        x[0, 0, :, :] = np.float32(1e-40)
+    t = torch.from_numpy(x.reshape(rows, hkv, d)).to(TYPES[dtype]).cuda()
+    cache, pages, slots = make_pool(kvc, [rows], 64, hkv, d, "q8_0", "head_major")
+    before = snapshot(cache)
+    kvc.kv_paged_append(cache, 0, pages, starts([rows]), t, t.flip(0).contiguous())
+    f = lambda u: u.float().cpu().numpy()
+    want = expected_bufs(cache, before, 0, slots[0], f(t), f(t.flip(0)))
+    for a, b in zip(cache._bufs, want):
+        assert torch.equal(a, b)
