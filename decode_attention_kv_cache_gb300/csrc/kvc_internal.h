@@ -111,5 +111,6 @@ uint64_t take_test_stall(int which);
 int read_and_clear_device_status(int32_t *status);
 int read_and_clear_decode_status(int32_t *status);
 int read_and_clear_paged_status(int32_t *status);
+int read_and_clear_packed_status(int32_t *status);
 
 }  // namespace kvc

@@ -1273,13 +1273,14 @@ int launch_prefill_step(const kvc_cache &c, int layer, int pos0, int n_tokens, c
 
 int read_and_clear_device_status(int32_t *status) {
     if (cudaDeviceSynchronize() != cudaSuccess) return KVC_ECUDA;
-    int v = 0, dv = 0, pv = 0;
+    int v = 0, dv = 0, pv = 0, kv = 0;
     if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int)) != cudaSuccess) return KVC_ECUDA;
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) != cudaSuccess) return KVC_ECUDA;
     if (read_and_clear_decode_status(&dv) != KVC_OK) return KVC_ECUDA;
     if (read_and_clear_paged_status(&pv) != KVC_OK) return KVC_ECUDA;
-    *status = v ? v : dv ? dv : pv;
+    if (read_and_clear_packed_status(&kv) != KVC_OK) return KVC_ECUDA;
+    *status = v ? v : dv ? dv : pv ? pv : kv;
     return KVC_OK;
 }
 
