@@ -23,10 +23,11 @@
 // One CTA (12 warps):
 //   warp 0     producer: walks the CTA's run of the list, passes each block on through a ring of items and
 //              loads Q tiles and a ring of K and V tiles (in the order K(0) V(0) K(1) V(1) ...) by TMA;
-//   warp 1     allocates tensor memory; one lane issues the MMAs.  Where a sequence ends inside a V tile the warp
-//              sets the rows behind it to zero, while the softmax of that tile runs;
+//   warp 1     allocates tensor memory; one lane issues the MMAs;
 //   warps 4-7, 8-11   softmax of the first and the second tile, a thread for each row: the row's maximum needs no
-//              exchange between threads.  O is rescaled only when the running maximum has grown by more than 2^8.
+//              exchange between threads.  A tile's QK - softmax - PV is a chain, so PV starts on the first 64 keys
+//              while the numerators of the others are computed.  O is rescaled only when the running maximum has grown by
+//              more than 2^8.  Where a sequence ends inside a V tile they also set the rows behind it to zero.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,7 +46,7 @@ using namespace ptx;
 
 constexpr int BM = 128;             // rows of a tile
 constexpr int BN = 128;             // keys of a tile
-constexpr int THREADS = 384;
+constexpr int THREADS = 384;        // a warpgroup with the producer and the MMA warp, two of softmax
 constexpr int NI = 4;               // items on their way from the producer
 constexpr int BLOCK_COST = 128;     // what a block costs besides its keys, in keys
 constexpr int SNAP = 2;             // a cut fewer tiles than this from an end of a block moves there
@@ -59,8 +60,9 @@ struct Cfg {
     static constexpr int TILE = 128 * D * 2;               // a Q, K or V tile
     static constexpr int NS = D == 128 ? 5 : 11;            // ring of K and V tiles
     static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE, OFF_MISC = OFF_RING + NS * TILE;
-    static constexpr int ALLOC = MAX_DYN_SMEM;
-    static_assert(OFF_MISC + 1024 + 1024 <= ALLOC, "shared memory plan");
+    static constexpr int USED = OFF_MISC + 1024;
+    static constexpr int ALLOC = USED + 1024 <= MAX_DYN_SMEM ? USED + 1024 : MAX_DYN_SMEM;
+    static_assert(USED <= MAX_DYN_SMEM, "shared memory plan");
     static constexpr uint32_t COL_S = 0, COL_O = 256;       // tile x: S at 128 x, O at 256 + D x
 };
 
@@ -75,7 +77,7 @@ struct Item {
 };
 
 struct Misc {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_done[2], full[12], empty[12], item_full[NI], item_empty[NI],
+    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[4], o_done[2], full[12], empty[12], item_full[NI], item_empty[NI],
         drain;
     Item items[NI];
     unsigned long long warp_units[THREADS / 32], total, rest;
@@ -173,6 +175,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
         : "memory");
 }
 
+// MMAs with the descriptors' two words apart.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi),
+        "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(idesc),
+        "r"((uint32_t)acc)
+        : "memory");
+}
+
 // key tiles [t0, t1) of one of an item's two tiles: the first tile's tokens see fewer keys than the second's
 __device__ __forceinline__ int tile_end(const Args &a, const Item &it, int x) {
     if (x == 1) return it.tokens > a.tok ? it.t1 : it.t0;   // no second tile
@@ -189,6 +209,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
+    if (sm + C::USED > smem_raw + C::ALLOC) {  // the tiles need 1024-byte alignment
+        if (threadIdx.x == 0) atomicExch(&g_packed_status, 2);
+        return;
+    }
     Misc *ms = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
     volatile int *s_abort = &ms->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -198,7 +222,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&ms->q_full[x], 1);
             mbar_init(&ms->q_empty[x], 1);
             mbar_init(&ms->s_full[x], 1);
-            mbar_init(&ms->p_ready[x], 128);
+            mbar_init(&ms->p_ready[2 * x], 128);
+            mbar_init(&ms->p_ready[2 * x + 1], 128);
             mbar_init(&ms->o_done[x], 1);
         }
         for (int s = 0; s < C::NS; ++s) {
@@ -256,16 +281,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncthreads();
     }
     const uint32_t tmem = ms->tmem;
-    auto take_item = [&](uint32_t &seq, Item &it) -> bool {   // by a whole warp
-        const int slot = seq % NI;
-        if (!warp_wait(&ms->item_full[slot], (seq / NI) & 1, s_abort)) return false;
-        it = ms->items[slot];
-        ++seq;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->item_empty[slot]);
-        return it.h >= 0;
-    };
 
+    // registers: 128 * 88 + 256 * 208 = 384 * 168, what the CTA is launched with
     if (warp < 4) setmaxnreg_dec<88>();
     if (warp == 0) {
         // ------------------------------------------------------------------ producer
@@ -402,98 +419,105 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
-        constexpr uint32_t FMT = BF16 ? (1u << 7) | (1u << 10) : 0u;
-        constexpr uint32_t IDESC_S = idesc_f16(BM, BN, 0, 0) | FMT, IDESC_O = idesc_f16(BM, D, 0, 1) | FMT;
-        const uint32_t sQ = smem_u32(sm + C::OFF_Q), sRing = smem_u32(sm + C::OFF_RING);
-        uint32_t n_item = 0, ring = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-        bool ok = true;
-        Item it;
-        // S of tile x = Q_x K^T, K in ring entry r
-        auto issue_s = [&](int x, uint32_t r) {
-            if (lane == 0) {
-                const uint32_t kb = sRing + (r % C::NS) * C::TILE, qb = sQ + x * C::TILE;
+        if (lane == 0) {
+            constexpr uint32_t FMT = BF16 ? (1u << 7) | (1u << 10) : 0u;
+            constexpr uint32_t IDESC_S = idesc_f16(BM, BN, 0, 0) | FMT, IDESC_O = idesc_f16(BM, D, 0, 1) | FMT;
+            // descriptors: the high word is fixed, the low word is the address (in 16 bytes) under the leading offset;
+            // between the steps of a product only the address moves
+            constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+            const uint32_t lo_q = (smem_u32(sm + C::OFF_Q) >> 4) | (1u << 16), lo_ring = smem_u32(sm + C::OFF_RING) >> 4;
+            uint32_t n_item = 0, ring = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
+            bool ok = true;
+            Item it;
+            // S of tile x = Q_x K^T, K in ring entry r
+            auto issue_s = [&](int x, uint32_t r) {
+                const uint32_t kb = (lo_ring + (r % C::NS) * (C::TILE >> 4)) | (1u << 16), qb = lo_q + x * (C::TILE >> 4);
+                const uint32_t d = tmem + C::COL_S + 128 * x;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t kk = (ks & 3) * 32;
-                    umma_f16_ss(tmem + C::COL_S + 128 * x, sdesc_sw128(qb + (ks >> 2) * (BM * 128) + kk, 16, 1024),
-                                sdesc_sw128(kb + (ks >> 2) * (BN * 128) + kk, 16, 1024), IDESC_S, ks > 0);
+                    const uint32_t off = (ks >> 2) * (128 * 128 >> 4) + (ks & 3) * 2;
+                    umma_ss(d, qb + off, kb + off, DESC_HI, IDESC_S, ks > 0);
                 }
                 umma_commit(&ms->s_full[x]);
-            }
-        };
-        // O of tile x (+)= P_x V, V in ring entry r
-        auto issue_pv = [&](int x, uint32_t r, bool acc) {
-            if (lane == 0) {
-                const uint32_t vb = sRing + (r % C::NS) * C::TILE;
+            };
+            // half of O of tile x (+)= P_x V (keys 64 hf .. + 63 of the tile), V in ring entry r
+            auto issue_pv = [&](int x, int hf, uint32_t r, bool acc) {
+                const uint32_t vb = (lo_ring + (r % C::NS) * (C::TILE >> 4)) | ((BN * 128 >> 4) << 16);
+                const uint32_t d = tmem + C::COL_O + D * x, pa = tmem + C::COL_S + 128 * x;
 #pragma unroll
-                for (int ks = 0; ks < BN / 16; ++ks)
-                    umma_f16_ts(tmem + C::COL_O + D * x, tmem + C::COL_S + 128 * x + ks * 8,
-                                sdesc_sw128(vb + ks * 16 * 128, BN * 128, 1024), IDESC_O, (acc || ks > 0) ? 1u : 0u);
-            }
-        };
-        auto ring_wait = [&](uint32_t r) -> bool {
-            const bool k = warp_wait(&ms->full[r % C::NS], (r / C::NS) & 1, s_abort);
-            tc_fence_after();
-            return k;
-        };
-        auto commit = [&](uint64_t *bar) {
-            if (lane == 0) umma_commit(bar);
-        };
-        while (ok && take_item(n_item, it)) {
-            const int end[2] = {tile_end(a, it, 0), tile_end(a, it, 1)};
-            const bool two = it.tokens > a.tok;
-            if (!(ok = ring_wait(ring))) break;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (x == 1 && !two) continue;
-                if (!(ok = warp_wait(&ms->q_full[x], nq[x] & 1, s_abort))) break;
-                ++nq[x];
+                for (int i = 0; i < BN / 32; ++i) {
+                    const int ks = BN / 32 * hf + i;
+                    umma_ts(d, pa + ks * 8, vb + ks * (16 * 128 >> 4), DESC_HI, IDESC_O, i > 0 || acc);
+                }
+            };
+            auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+                const bool k = mbar_wait(bar, parity, s_abort);
                 tc_fence_after();
-                if (it.t0 < end[x]) issue_s(x, ring);
-                if (it.t0 + 1 >= end[x]) commit(&ms->q_empty[x]);   // its only product with K: Q may be replaced
-            }
-            if (!ok) break;
-            commit(&ms->empty[ring % C::NS]);
-            for (int t = it.t0; ok && t < it.t1; ++t) {
-                const uint32_t rv = ring + 1 + 2 * (t - it.t0), rk = rv + 1;
-                const bool more = t + 1 < it.t1;
-                if (!(ok = ring_wait(rv))) break;
-                if ((t + 1) * BN > it.keys) {
-                    // rows behind the sequence are another's or nobody's, and a NaN times a zero weight would be a NaN
-                    uint8_t *vt = sm + C::OFF_RING + (rv % C::NS) * C::TILE;
-                    for (int i = max(it.keys - t * BN, 0) * 8 + lane; i < BN * 8; i += 32)
-#pragma unroll
-                        for (int dh = 0; dh < D / 64; ++dh)
-                            *reinterpret_cast<uint4 *>(vt + dh * BN * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                return k;
+            };
+            auto ring_wait = [&](uint32_t r) -> bool { return wait(&ms->full[r % C::NS], (r / C::NS) & 1); };
+            while (ok) {
+                const int slot = n_item % NI;
+                if (!mbar_wait(&ms->item_full[slot], (n_item / NI) & 1, s_abort)) break;
+                it = ms->items[slot];
+                ++n_item;
+                mbar_arrive(&ms->item_empty[slot]);
+                if (it.h < 0) break;
+                const int end0 = tile_end(a, it, 0), end1 = tile_end(a, it, 1);
+                const bool two = it.tokens > a.tok;
+                if (!(ok = ring_wait(ring))) break;
+                if (!(ok = wait(&ms->q_full[0], nq0 & 1))) break;
+                ++nq0;
+                if (it.t0 < end0) issue_s(0, ring);
+                if (it.t0 + 1 >= end0) umma_commit(&ms->q_empty[0]);   // its only product with K: Q may be replaced
+                if (two) {
+                    if (!(ok = wait(&ms->q_full[1], nq1 & 1))) break;
+                    ++nq1;
+                    issue_s(1, ring);
+                    if (it.t0 + 1 >= end1) umma_commit(&ms->q_empty[1]);
                 }
-                bool have_k = false;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (t >= end[x]) continue;
-                    if (!(ok = warp_wait(&ms->p_ready[x], np[x] & 1, s_abort))) break;
-                    ++np[x];
-                    tc_fence_after();
-                    issue_pv(x, rv, t > it.t0);
-                    if (t + 1 >= end[x]) commit(&ms->o_done[x]);
-                    else {
-                        if (!have_k && !(ok = ring_wait(rk))) break;
-                        have_k = true;
-                        issue_s(x, rk);
-                        if (t + 2 >= end[x]) commit(&ms->q_empty[x]);
+                umma_commit(&ms->empty[ring % C::NS]);
+                for (int t = it.t0; ok && t < it.t1; ++t) {
+                    const uint32_t rv = ring + 1 + 2 * (t - it.t0), rk = rv + 1;
+                    const bool more = t + 1 < it.t1;
+                    if (!(ok = ring_wait(rv))) break;
+                    if (more && !(ok = ring_wait(rk))) break;
+                    if (t < end0) {
+                        if (!(ok = wait(&ms->p_ready[0], np0 & 1))) break;
+                        issue_pv(0, 0, rv, t > it.t0);
+                        if (!(ok = wait(&ms->p_ready[1], np0 & 1))) break;
+                        issue_pv(0, 1, rv, true);
+                        ++np0;
+                        if (t + 1 < end0) {
+                            issue_s(0, rk);
+                            if (t + 2 >= end0) umma_commit(&ms->q_empty[0]);
+                        } else {
+                            umma_commit(&ms->o_done[0]);
+                        }
                     }
+                    if (t < end1) {
+                        if (!(ok = wait(&ms->p_ready[2], np1 & 1))) break;
+                        issue_pv(1, 0, rv, t > it.t0);
+                        if (!(ok = wait(&ms->p_ready[3], np1 & 1))) break;
+                        issue_pv(1, 1, rv, true);
+                        ++np1;
+                        if (t + 1 < end1) {
+                            issue_s(1, rk);
+                            if (t + 2 >= end1) umma_commit(&ms->q_empty[1]);
+                        } else {
+                            umma_commit(&ms->o_done[1]);
+                        }
+                    }
+                    umma_commit(&ms->empty[rv % C::NS]);
+                    if (more) umma_commit(&ms->empty[rk % C::NS]);
                 }
-                if (!ok) break;
-                commit(&ms->empty[rv % C::NS]);
-                if (more) commit(&ms->empty[rk % C::NS]);
+                ring += 2 * (it.t1 - it.t0);
             }
-            ring += 2 * (it.t1 - it.t0);
-        }
-        if (*s_abort && lane == 0) {   // let the MMAs in flight finish before tensor memory is freed
-            volatile int never = 0;
-            umma_commit(&ms->drain);
-            mbar_wait(&ms->drain, 0, &never, 200000000ull);
+            if (*s_abort) {   // let the MMAs in flight finish before tensor memory is freed
+                volatile int never = 0;
+                umma_commit(&ms->drain);
+                mbar_wait(&ms->drain, 0, &never, 200000000ull);
+            }
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -505,15 +529,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + C::COL_S + 128 * x + lane_base, tO = tmem + C::COL_O + D * x + lane_base;
         const float sl2 = a.scale_log2;
-        uint32_t n_item = 0, ns = 0, no = 0;
+        const uint64_t sl2x2 = f2_pack(sl2, sl2);
+        uint32_t n_item = 0, ns = 0, no = 0, ring = 0;
         bool ok = true;
-        Item it;
-        while (ok && take_item(n_item, it)) {
+        while (ok) {
+            const int slot = n_item % NI;
+            if (!warp_wait(&ms->item_full[slot], (n_item / NI) & 1, s_abort)) break;
+            const Item it = ms->items[slot];
+            ++n_item;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms->item_empty[slot]);
+            if (it.h < 0) break;
             const int tk = x * a.tok + token;                          // token of the block
             const bool valid = token < a.tok && tk < it.tokens;
             const int last = valid ? it.last + tk : -1;                  // the last key that this row sees
             const int last0 = it.last + x * a.tok;                       // ... that the tile's first row sees
-            const int end = tile_end(a, it, x);
+            const int end = tile_end(a, it, x), end0 = tile_end(a, it, 0);
             float m = -INFINITY, l = 0.f;
             for (int t = it.t0; t < end; ++t) {
                 if (!(ok = warp_wait(&ms->s_full[x], ns & 1, s_abort))) break;
@@ -542,17 +573,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int u = 0; u < 8; ++u) mx8[u] = fmaxf(mx8[u], __uint_as_float(s[120 + u]));
                 const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
                 const float m_new = fmaxf(m, mx * sl2);
-                float alpha = 1.f;
-                if (t == it.t0) m = m_new;
-                else if (m_new > m + RESCALE_LOG2) {
-                    alpha = m == -INFINITY ? 0.f : ex2(m - m_new);
+                if (t == it.t0) {
                     m = m_new;
-                }
-                // a row that sees no key so far: its scores are all -inf and give p = 0 with the offset 0
-                const float m_sub = m == -INFINITY ? 0.f : m;
-                l *= alpha;
-                // S(t) is complete, so PV(t - 1), issued before it, is too
-                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                } else if (__any_sync(0xffffffffu, m_new > m + RESCALE_LOG2)) {
+                    // S(t) is complete, so PV(t - 1), issued before it, is too
+                    const bool up = m_new > m + RESCALE_LOG2;
+                    const float alpha = !up ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
+                    if (up) m = m_new;
+                    l *= alpha;
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
@@ -563,7 +591,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_st32(tO + c * 32, o);
                     }
                 }
-                const uint64_t sl2x2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_sub, -m_sub);
+                // a row that sees no key so far: its scores are all -inf and give p = 0 with the offset 0
+                const float m_sub = m == -INFINITY ? 0.f : m;
+                const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
                 uint64_t rs4[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -578,15 +608,36 @@ __global__ void __launch_bounds__(THREADS, 1)
                         pk[e >> 1] = pack16<BF16>(x0, x1);
                     }
                     tmem_st16(tS + c * 16, pk);
+                    if (c == 1) {
+                        // the first half of P: its product may start
+                        if ((t + 1) * BN > it.keys && (x == 0 || t >= end0)) {
+                            // The rows of V behind the sequence are another's or nobody's, and a NaN times a zero weight
+                            // would be a NaN: the tile whose PV comes first zeroes them.  (The barrier cannot be a phase
+                            // further: it is that PV that frees the ring entry.)
+                            const uint32_t rv = ring + 1 + 2 * (t - it.t0);
+                            ok = warp_wait(&ms->full[rv % C::NS], (rv / C::NS) & 1, s_abort);
+                            uint8_t *vt = sm + C::OFF_RING + (rv % C::NS) * C::TILE;
+                            for (int i = max(it.keys - t * BN, 0) * 8 + r; ok && i < BN * 8; i += BM)
+#pragma unroll
+                                for (int dh = 0; dh < D / 64; ++dh)
+                                    *reinterpret_cast<uint4 *>(vt + dh * BN * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            fence_proxy_async_smem();
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive(&ms->p_ready[2 * x]);
+                    }
                 }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&ms->p_ready[2 * x + 1]);
                 float r8[8];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) f2_unpack(rs4[u], r8[2 * u], r8[2 * u + 1]);
                 l += ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&ms->p_ready[x]);
+                if (!ok) break;
             }
+            ring += 2 * (it.t1 - it.t0);
             if (!ok) break;
             // ---- O / l, or the partial.  The next item's first PV overwrites O only after this thread's next P,
             // which comes after these reads.
@@ -599,7 +650,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const int64_t row = (int64_t)(it.q_row + tk) * a.H_q + it.h * a.G + head;
             const int64_t prow = ((int64_t)blockIdx.x * 2 + (it.t0 == 0)) * 256 + x * BM + r;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const bool none = !any || l == 0.f;
+            const float inv = none ? 0.f : 1.f / l;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -610,7 +662,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (!valid) continue;
                 if (it.whole) {
-                    const bool none = !any || l == 0.f;
                     uint32_t *dst = reinterpret_cast<uint32_t *>(a.out) + row * (D / 2) + c / 2;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
@@ -629,8 +680,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
             tc_fence_before();
-            if (valid && !it.whole) a.part_ml[prow] = any ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
-            if (valid && it.whole && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+            if (valid) {
+                if (!it.whole) a.part_ml[prow] = any ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+                else if (a.lse) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * LN2;
+            }
         }
     }
     tc_fence_before();
