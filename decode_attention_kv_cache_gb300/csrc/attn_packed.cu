@@ -7,27 +7,28 @@
 // bounds it is the tensor cores' rate for long prompts, and for short ones the chain load - product - softmax -
 // product - store of each block.
 //
-// Work split.  The G query heads of a kv head see the same keys, so a tile of 128 rows holds 128 / G tokens
-// with all their heads: a prompt of 25 tokens with five heads fills one tile where a tile for each head would
-// leave four fifths of five empty.  A block is two such tiles of a (sequence, kv head), which share each K and V tile of 128 keys.  The
-// blocks of all kv heads and sequences, each as long as the keys that it sees plus a charge, form one list that
-// is cut into equal runs, one for each CTA (one per SM); lengths are read on the device.  A block cut by a run's
-// end leaves partial results (O, maximum, sum; at most two blocks for each CTA) that a second kernel joins in the
-// runs' order; cuts close to a block's end move there.
+// Work split.  The G query heads of a kv head see the same keys, so a block of 128 rows holds 128 / G tokens with all
+// their heads: a prompt of 25 tokens with five heads fills one block where a block for each head would leave four
+// fifths of five empty.  The blocks of all kv heads and sequences, each as long as the keys that it sees plus a
+// charge, form one list that is cut into equal runs, one for each CTA (one per SM); lengths are read on the device.  A
+// block cut by a run's end leaves partial results (O, maximum, sum; at most two blocks for each CTA) that a second
+// kernel joins in the runs' order; cuts close to a block's end move there.
 //
-// Tensor memory (512 columns): for each of the two tiles S (128 columns, then overwritten by P as 16-bit
-// pairs, the A operand of the second product) and O (D columns).  The MMA thread alternates between the tiles - PV(k)
-// and QK(k+1) of one run while the other's softmax does - and the MMAs of one thread execute in order, so QK(k+1) may
-// be issued as soon as PV(k) is, although it overwrites the P that PV(k) reads.
+// Tensor memory (512 columns): S = Q K^T of a tile of 128 keys, twice (256 columns), P (its softmax numerators as 16-bit
+// pairs), twice (128), and O (D).  With two of each no step of a tile waits for another step of the same tile's
+// neighbours: S of the next two tiles - of the next block, at a block's end - are computed while the softmax of this
+// one runs, and P of the next is written while PV of this one runs.
 //
 // One CTA (12 warps):
 //   warp 0     producer: walks the CTA's run of the list, passes each block on through a ring of items and
-//              loads Q tiles and a ring of K and V tiles (in the order K(0) V(0) K(1) V(1) ...) by TMA;
-//   warp 1     allocates tensor memory; one lane issues the MMAs;
-//   warps 4-7, 8-11   softmax of the first and the second tile, a thread for each row: the row's maximum needs no
-//              exchange between threads.  A tile's QK - softmax - PV is a chain, so PV starts on the first 64 keys
-//              while the numerators of the others are computed.  O is rescaled only when the running maximum has grown by
-//              more than 2^8.  Where a sequence ends inside a V tile they also set the rows behind it to zero.
+//              loads Q (two buffers) and K and V through a ring, in the order K(0) K(1) V(0) K(2) V(1) ..., by TMA;
+//   warps 1, 2   one lane of each issues the MMAs: those with K, and those with V (one thread for both spends as long in their
+//              waits and commits, about 100 and 60 cycles each, as the tensor cores on the products); warp 1 also
+//              allocates tensor memory;
+//   warps 4-7, 8-11   softmax, two threads for each row, 64 keys of each tile each.  They exchange their maxima through
+//              shared memory, but go on with the reference that the row has: it is raised, and O rescaled, only where
+//              a score passes it by more than 2^8.  Where a sequence ends inside a V tile they also set the rows
+//              behind it to zero.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,12 +45,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int BM = 128;             // rows of a tile
+constexpr int BM = 128;             // rows of a block
 constexpr int BN = 128;             // keys of a tile
 constexpr int THREADS = 384;        // a warpgroup with the producer and the MMA warp, two of softmax
 constexpr int NI = 4;               // items on their way from the producer
-constexpr int BLOCK_COST = 128;     // what a block costs besides its keys, in keys
-constexpr int SNAP = 2;             // a cut fewer tiles than this from an end of a block moves there
+constexpr int BLOCK_COST = 256;     // what a block costs besides its keys, in keys
+constexpr int SNAP = 4;             // a cut fewer tiles than this from an end of a block moves there
 constexpr int MAX_DYN_SMEM = 232448;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994531f;
@@ -57,14 +58,14 @@ constexpr uint32_t TMEM_COLS = 512;
 
 template <int D>
 struct Cfg {
-    static constexpr int TILE = 128 * D * 2;               // a Q, K or V tile
-    static constexpr int NS = D == 128 ? 5 : 11;            // ring of K and V tiles
-    static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE, OFF_MISC = OFF_RING + NS * TILE;
-    static constexpr int USED = OFF_MISC + 1024;
+    static constexpr int PIECE = 128 * D * 2;              // 128 rows of Q, K or V
+    static constexpr int NS = D == 128 ? 5 : 11;            // ring of K and V pieces
+    static constexpr int OFF_Q = 0, OFF_RING = 2 * PIECE, OFF_MISC = OFF_RING + NS * PIECE, OFF_MAIL = OFF_MISC + 1024;
+    static constexpr int USED = OFF_MAIL + 4 * BM * 4;
     static constexpr int ALLOC = USED + 1024 <= MAX_DYN_SMEM ? USED + 1024 : MAX_DYN_SMEM;
     static_assert(USED <= MAX_DYN_SMEM, "shared memory plan");
-    static constexpr uint32_t COL_S = 0, COL_O = 256;       // tile x: S at 128 x, O at 256 + D x
 };
+constexpr uint32_t COL_S = 0, COL_P = 256, COL_O = 384;   // two S of 128 columns, two P of 64, O
 
 // A block, or the part of its keys that falls into this CTA's run.
 struct Item {
@@ -75,10 +76,8 @@ struct Item {
     int t0, t1;               // key tiles
     int whole;                // the run holds the whole block
 };
-
 struct Misc {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[4], o_done[2], full[12], empty[12], item_full[NI], item_empty[NI],
-        drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_ready[2], o_done[2], full[12], empty[12], item_full[NI], item_empty[NI], drain[2];
     Item items[NI];
     unsigned long long warp_units[THREADS / 32], total, rest;
     int first_seq, abort;
@@ -89,12 +88,12 @@ static_assert(sizeof(Misc) <= 1024, "small area");
 struct Args {
     const int32_t *q_start, *k_start;
     int n_seq, n_q, n_k, H_q, H_kv, G;
-    int tok;                  // tokens of a tile: 128 / G
+    int tok;                  // tokens of a block: 128 / G
     void *out;
     float *lse;
-    float *part_o;            // [CTA][2][256][D]
-    float2 *part_ml;          // [CTA][2][256]
-    int4 *desc;               // [CTA][2]: the block that this CTA begins and others finish (see combine)
+    float *part_o;            // [CTA][2][128][D]
+    float2 *part_ml;          // [CTA][2][128]
+    int4 *desc;               // [CTA]: the block that this CTA begins and others finish (see combine)
     float scale_log2;
 };
 
@@ -118,17 +117,17 @@ __device__ __forceinline__ Seq load_seq(const Args &a, int i) {
 }
 __device__ __forceinline__ int blocks_of(const Args &a, const Seq &s) {
     const int rows = min(s.nq, a.n_q - s.q0);   // rows that exist
-    return s.nq > 0 ? (rows + 2 * a.tok - 1) / (2 * a.tok) : 0;
+    return s.nq > 0 ? (rows + a.tok - 1) / a.tok : 0;
 }
 // keys that block b sees, at least 1 (a block without keys still writes its rows)
 __device__ __forceinline__ int keys_of(const Args &a, const Seq &s, int b) {
-    const long long t2 = 2 * a.tok, end = min((long long)s.nq, (b + 1) * t2) + s.nk - s.nq;
+    const long long t2 = a.tok, end = min((long long)s.nq, (b + 1) * t2) + s.nk - s.nq;
     return (int)max(min(end, (long long)s.nk), 1ll);
 }
 // units of the blocks before b: with off = nk - nq, a block sees off + (b + 1) t2 keys, or 1 where that is less;
 // only the last, which is never summed here before the end, is cut at nk
 __device__ __forceinline__ long long units_before(const Args &a, const Seq &s, int b, int blocks) {
-    const long long t2 = 2 * a.tok, off = s.nk - s.nq;
+    const long long t2 = a.tok, off = s.nk - s.nq;
     const int n = min(b, blocks - 1);                                     // blocks summed by the formula
     const long long b0 = off >= 0 ? 0 : min((long long)n, -off / t2);        // of which the first b0 see nothing
     long long u = (long long)b * BLOCK_COST + b0 + (n - b0) * off + t2 * ((long long)n * (n + 1) / 2 - b0 * (b0 + 1) / 2);
@@ -175,6 +174,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 // MMAs with the descriptors' two words apart.
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
     asm volatile(
@@ -193,14 +201,6 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, u
         : "memory");
 }
 
-// key tiles [t0, t1) of one of an item's two tiles: the first tile's tokens see fewer keys than the second's
-__device__ __forceinline__ int tile_end(const Args &a, const Item &it, int x) {
-    if (x == 1) return it.tokens > a.tok ? it.t1 : it.t0;   // no second tile
-    if (it.tokens <= a.tok) return it.t1;
-    const int n = min(it.last + a.tok, it.keys);             // keys that the first tile sees
-    return max(min(it.t1, n > 0 ? (n + BN - 1) / BN : 1), it.t0);
-}
-
 template <int D, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1)
     packed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -216,14 +216,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     Misc *ms = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
     volatile int *s_abort = &ms->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < 4 * BM; i += THREADS) reinterpret_cast<uint32_t *>(sm + C::OFF_MAIL)[i] = 1u;
     if (threadIdx.x == 0) {
         ms->abort = 0;
         for (int x = 0; x < 2; ++x) {
             mbar_init(&ms->q_full[x], 1);
             mbar_init(&ms->q_empty[x], 1);
             mbar_init(&ms->s_full[x], 1);
-            mbar_init(&ms->p_ready[2 * x], 128);
-            mbar_init(&ms->p_ready[2 * x + 1], 128);
+            mbar_init(&ms->s_free[x], 256);
+            mbar_init(&ms->p_ready[x], 256);
             mbar_init(&ms->o_done[x], 1);
         }
         for (int s = 0; s < C::NS; ++s) {
@@ -232,9 +233,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int s = 0; s < NI; ++s) {
             mbar_init(&ms->item_full[s], 1);
-            mbar_init(&ms->item_empty[s], 9);   // MMA warp, eight softmax warps
+            mbar_init(&ms->item_empty[s], 10);   // two MMA issuers, eight softmax warps
         }
-        mbar_init(&ms->drain, 1);
+        mbar_init(&ms->drain[0], 1);
+        mbar_init(&ms->drain[1], 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------------------ producer
         const unsigned long long W = ms->total * a.H_kv, u0 = run_start(W, blockIdx.x), u1 = run_start(W, blockIdx.x + 1);
         unsigned long long left = u1 - u0;
-        uint32_t n_item = 0, n_ring = 0, nq[2] = {0, 0};
+        uint32_t n_item = 0, n_ring = 0, nq = 0;
         bool ok = true;
         int owner_first = 0;   // this CTA begins a block that others finish
         if (lane == 0) {
@@ -327,98 +329,107 @@ __global__ void __launch_bounds__(THREADS, 1)
             block = lo;
             x = r - units_before(a, s, lo, blocks);
         }
-        while (ok && left && h < a.H_kv) {
-            if (block >= blocks) {
-                if (++seq == a.n_seq) { seq = 0; ++h; }
-                enter();
-                continue;
-            }
-            Item it;
-            const int seen = keys_of(a, s, block), tiles = (seen + BN - 1) / BN;
-            const long long all = seen + BLOCK_COST, x1 = (long long)min((unsigned long long)all, x + left);
-            it.t0 = cut_tile(x, tiles);
-            it.t1 = x1 == all ? tiles : cut_tile(x1, tiles);
-            it.q_row = s.q0 + block * 2 * a.tok;
-            it.tokens = min(2 * a.tok, min(s.nq, a.n_q - s.q0) - block * 2 * a.tok);
-            it.h = h;
-            it.k_row = s.k0;
-            it.keys = s.nk;
-            it.last = block * 2 * a.tok + s.nk - s.nq;
-            it.whole = it.t0 == 0 && it.t1 == tiles;
-            left -= x1 - x;
-            if (it.t0 == 0 && it.t1 > 0 && it.t1 < tiles) {
-                // others finish this block: those of the next runs whose cuts leave them a part of it
-                owner_first = 1;
-                if (lane == 0) {
-                    const unsigned long long begin = u1 - x1;   // the block's first unit
-                    int n = 1;
-                    for (unsigned c = blockIdx.x + 1;; ++c, ++n) {
-                        const unsigned long long e = run_start(W, c + 1);
-                        if (e >= begin + all || cut_tile((long long)(e - begin), tiles) == tiles) { ++n; break; }
+        // the next item of the run, or h = -1
+        auto next_item = [&](Item &it) {
+            it.h = -1;
+            while (left && h < a.H_kv) {
+                if (block >= blocks) {
+                    if (++seq == a.n_seq) { seq = 0; ++h; }
+                    enter();
+                    continue;
+                }
+                const int seen = keys_of(a, s, block), tiles = (seen + BN - 1) / BN;
+                const long long all = seen + BLOCK_COST, x1 = (long long)min((unsigned long long)all, x + left);
+                it.t0 = cut_tile(x, tiles);
+                it.t1 = x1 == all ? tiles : cut_tile(x1, tiles);
+                it.q_row = s.q0 + block * a.tok;
+                it.tokens = min(a.tok, min(s.nq, a.n_q - s.q0) - block * a.tok);
+                it.k_row = s.k0;
+                it.keys = s.nk;
+                it.last = block * a.tok + s.nk - s.nq;
+                it.whole = it.t0 == 0 && it.t1 == tiles;
+                left -= x1 - x;
+                if (it.t0 == 0 && it.t1 > 0 && it.t1 < tiles) {
+                    // others finish this block: those of the next runs whose cuts leave them a part of it
+                    owner_first = 1;
+                    if (lane == 0) {
+                        const unsigned long long begin = u1 - x1;   // the block's first unit
+                        int n = 1;
+                        for (unsigned c = blockIdx.x + 1;; ++c, ++n) {
+                            const unsigned long long e = run_start(W, c + 1);
+                            if (e >= begin + all || cut_tile((long long)(e - begin), tiles) == tiles) { ++n; break; }
+                        }
+                        a.desc[blockIdx.x] = make_int4(it.q_row, it.tokens, h, n);
                     }
-                    a.desc[2 * blockIdx.x] = make_int4(it.q_row, it.tokens, h, n);
+                }
+                x = 0;
+                ++block;
+                if (it.t1 > it.t0) {
+                    it.h = h;
+                    return;
                 }
             }
-            x = 0;
-            ++block;
-            if (it.t1 <= it.t0) continue;
+        };
+        auto publish = [&](const Item &it) -> bool {
             const int slot = n_item % NI;
-            if (n_item >= NI && !warp_wait(&ms->item_empty[slot], ((n_item / NI) - 1) & 1, s_abort)) break;
+            if (n_item >= NI && !warp_wait(&ms->item_empty[slot], ((n_item / NI) - 1) & 1, s_abort)) return false;
             if (lane == 0) {
                 ms->items[slot] = it;
                 mbar_arrive(&ms->item_full[slot]);
             }
             ++n_item;
-            auto load_kv = [&](const CUtensorMap *m, int t) -> bool {
-                const int st = n_ring % C::NS;
-                if (n_ring >= (uint32_t)C::NS && !warp_wait(&ms->empty[st], ((n_ring / C::NS) - 1) & 1, s_abort)) return false;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&ms->full[st], C::TILE);
+            return true;
+        };
+        // tile t of K or V
+        auto load_kv = [&](const CUtensorMap *m, const Item &i, int t) -> bool {
+            const int st = n_ring % C::NS;
+            if (n_ring >= (uint32_t)C::NS && !warp_wait(&ms->empty[st], ((n_ring / C::NS) - 1) & 1, s_abort)) return false;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&ms->full[st], C::PIECE);
 #pragma unroll
-                    for (int dh = 0; dh < D / 64; ++dh)
-                        tma_load_3d(sm + C::OFF_RING + st * C::TILE + dh * BN * 128, m, &ms->full[st], dh * 64, h, it.k_row + t * BN);
-                }
-                ++n_ring;
-                return true;
-            };
-            const int two = it.tokens > a.tok ? 2 : 1;
-            for (int i = 0; ok && i < two; ++i) {
-                if (nq[i] > 0 && !warp_wait(&ms->q_empty[i], (nq[i] - 1) & 1, s_abort)) { ok = false; break; }
-                ++nq[i];
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&ms->q_full[i], (D / 64) * a.tok * a.G * 128);
+                for (int dh = 0; dh < D / 64; ++dh)
+                    tma_load_3d(sm + C::OFF_RING + st * C::PIECE + dh * BN * 128, m, &ms->full[st], dh * 64, i.h, i.k_row + t * BN);
+            }
+            ++n_ring;
+            return true;
+        };
+        Item it, nx;
+        next_item(it);
+        ok = publish(it);
+        auto load_q = [&](const Item &q) -> bool {
+            const int i = nq & 1;
+            if (nq >= 2 && !warp_wait(&ms->q_empty[i], ((nq >> 1) - 1) & 1, s_abort)) return false;
+            ++nq;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&ms->q_full[i], (D / 64) * a.tok * a.G * 128);
 #pragma unroll
-                    for (int dh = 0; dh < D / 64; ++dh)
-                        tma_load_3d(sm + C::OFF_Q + i * C::TILE + dh * BM * 128, &tm_q, &ms->q_full[i], dh * 64, h * a.G, it.q_row + i * a.tok);
-                }
-                if (i == 0) ok = load_kv(&tm_k, it.t0);   // the first product waits for these two
+                for (int dh = 0; dh < D / 64; ++dh)
+                    tma_load_3d(sm + C::OFF_Q + i * C::PIECE + dh * BM * 128, &tm_q, &ms->q_full[i], dh * 64, q.h * a.G, q.q_row);
             }
-            for (int t = it.t0; ok && t < it.t1; ++t) {
-                if (t > it.t0) ok = load_kv(&tm_k, t);
-                if (ok) ok = load_kv(&tm_v, t);
-            }
+            return true;
+        };
+        if (ok && it.h >= 0) ok = load_q(it) && load_kv(&tm_k, it, it.t0);
+        while (ok && it.h >= 0) {
+            for (int t = it.t0; ok && t + 1 < it.t1; ++t) ok = load_kv(&tm_k, it, t + 1) && load_kv(&tm_v, it, t);
+            if (!ok) break;
+            next_item(nx);   // the next block's first product comes before this one's last
+            ok = publish(nx);
+            if (ok && nx.h >= 0) ok = load_q(nx) && load_kv(&tm_k, nx, nx.t0);
+            else ++n_ring;   // the n-th V lies in entry 2 n + 2 also behind the last K
+            if (ok) ok = load_kv(&tm_v, it, it.t1 - 1);
+            it = nx;
         }
-        if (!owner_first && lane == 0) a.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
-        if (ok) {   // the end of the items
-            const int slot = n_item % NI;
-            if (n_item < NI || warp_wait(&ms->item_empty[slot], ((n_item / NI) - 1) & 1, s_abort)) {
-                if (lane == 0) {
-                    ms->items[slot].h = -1;
-                    mbar_arrive(&ms->item_full[slot]);
-                }
-            }
-        }
+        if (!owner_first && lane == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
         if (*s_abort) {   // a wait gave up: let the copies in flight land before the CTA exits
             volatile int never = 0;
-            for (uint32_t st = 0; st < (uint32_t)C::NS && st < n_ring; ++st) {
-                const uint32_t last = st + ((n_ring - 1 - st) / C::NS) * C::NS;
-                mbar_wait(&ms->full[st], (last / C::NS) & 1, &never, 200000000ull);
-            }
-            for (int i = 0; i < 2; ++i)
-                if (nq[i] > 0) mbar_wait(&ms->q_full[i], (nq[i] - 1) & 1, &never, 200000000ull);
+            for (uint32_t e = n_ring > (uint32_t)C::NS ? n_ring - C::NS : 0; e < n_ring; ++e)
+                mbar_wait(&ms->full[e % C::NS], (e / C::NS) & 1, &never, 200000000ull);
+            for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(&ms->q_full[i & 1], (i >> 1) & 1, &never, 200000000ull);
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issuer
+    } else if (warp == 1 || warp == 2) {
+        // ------------------------------------------------------------------ MMA issuers
+        // Warp 1 issues the products with K, warp 2 those with V.  The CTA's n-th tile has its K in entry 2 n - 1 of the ring
+        // (the first in entry 0) and its V in entry 2 n + 2.
         if (lane == 0) {
             constexpr uint32_t FMT = BF16 ? (1u << 7) | (1u << 10) : 0u;
             constexpr uint32_t IDESC_S = idesc_f16(BM, BN, 0, 0) | FMT, IDESC_O = idesc_f16(BM, D, 0, 1) | FMT;
@@ -426,112 +437,106 @@ __global__ void __launch_bounds__(THREADS, 1)
             // between the steps of a product only the address moves
             constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
             const uint32_t lo_q = (smem_u32(sm + C::OFF_Q) >> 4) | (1u << 16), lo_ring = smem_u32(sm + C::OFF_RING) >> 4;
-            uint32_t n_item = 0, ring = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
+            uint32_t n = 0, parity = 0;           // the tile, and the parity of its entry's phase
+            int slot = warp == 1 ? 0 : 2;
             bool ok = true;
-            Item it;
-            // S of tile x = Q_x K^T, K in ring entry r
-            auto issue_s = [&](int x, uint32_t r) {
-                const uint32_t kb = (lo_ring + (r % C::NS) * (C::TILE >> 4)) | (1u << 16), qb = lo_q + x * (C::TILE >> 4);
-                const uint32_t d = tmem + C::COL_S + 128 * x;
+            auto advance = [&](int e) {
+                slot += e;
+                if (slot >= C::NS) { slot -= C::NS; parity ^= 1; }
+            };
+            for (uint32_t n_item = 0; ok; ++n_item) {
+                const int sl = n_item % NI;
+                if (!mbar_wait(&ms->item_full[sl], (n_item / NI) & 1, s_abort)) break;
+                const int h = ms->items[sl].h, t0 = ms->items[sl].t0, t1 = ms->items[sl].t1;
+                mbar_arrive(&ms->item_empty[sl]);
+                if (h < 0) break;
+                if (warp == 1) {
+                    const int qb = n_item & 1;
+                    const uint32_t q = lo_q + qb * (C::PIECE >> 4);
+                    if (!mbar_wait(&ms->q_full[qb], (n_item >> 1) & 1, s_abort)) break;
+                    for (int t = t0; t < t1; ++t, ++n) {
+                        const int b = n & 1;
+                        if (!(ok = mbar_wait(&ms->full[slot], parity, s_abort))) break;
+                        // the softmax has read the S that lay here
+                        if (n >= 2 && !(ok = mbar_wait(&ms->s_free[b], ((n >> 1) - 1) & 1, s_abort))) break;
+                        tc_fence_after();
+                        const uint32_t kb = (lo_ring + slot * (C::PIECE >> 4)) | (1u << 16), d = tmem + COL_S + 128 * b;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * (128 * 128 >> 4) + (ks & 3) * 2;
-                    umma_ss(d, qb + off, kb + off, DESC_HI, IDESC_S, ks > 0);
-                }
-                umma_commit(&ms->s_full[x]);
-            };
-            // half of O of tile x (+)= P_x V (keys 64 hf .. + 63 of the tile), V in ring entry r
-            auto issue_pv = [&](int x, int hf, uint32_t r, bool acc) {
-                const uint32_t vb = (lo_ring + (r % C::NS) * (C::TILE >> 4)) | ((BN * 128 >> 4) << 16);
-                const uint32_t d = tmem + C::COL_O + D * x, pa = tmem + C::COL_S + 128 * x;
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t off = (ks >> 2) * (128 * 128 >> 4) + (ks & 3) * 2;
+                            umma_ss(d, q + off, kb + off, DESC_HI, IDESC_S, ks > 0);
+                        }
+                        umma_commit(&ms->s_full[b]);
+                        umma_commit(&ms->empty[slot]);
+                        if (t + 1 == t1) umma_commit(&ms->q_empty[qb]);
+                        advance(n == 0 ? 1 : 2);
+                    }
+                } else {
+                    for (int t = t0; t < t1; ++t, ++n) {
+                        const int b = n & 1;
+                        if (!(ok = mbar_wait(&ms->full[slot], parity, s_abort) &&
+                                   mbar_wait(&ms->p_ready[b], (n >> 1) & 1, s_abort)))
+                            break;
+                        tc_fence_after();
+                        const uint32_t vb = (lo_ring + slot * (C::PIECE >> 4)) | ((BN * 128 >> 4) << 16);
 #pragma unroll
-                for (int i = 0; i < BN / 32; ++i) {
-                    const int ks = BN / 32 * hf + i;
-                    umma_ts(d, pa + ks * 8, vb + ks * (16 * 128 >> 4), DESC_HI, IDESC_O, i > 0 || acc);
-                }
-            };
-            auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-                const bool k = mbar_wait(bar, parity, s_abort);
-                tc_fence_after();
-                return k;
-            };
-            auto ring_wait = [&](uint32_t r) -> bool { return wait(&ms->full[r % C::NS], (r / C::NS) & 1); };
-            while (ok) {
-                const int slot = n_item % NI;
-                if (!mbar_wait(&ms->item_full[slot], (n_item / NI) & 1, s_abort)) break;
-                it = ms->items[slot];
-                ++n_item;
-                mbar_arrive(&ms->item_empty[slot]);
-                if (it.h < 0) break;
-                const int end0 = tile_end(a, it, 0), end1 = tile_end(a, it, 1);
-                const bool two = it.tokens > a.tok;
-                if (!(ok = ring_wait(ring))) break;
-                if (!(ok = wait(&ms->q_full[0], nq0 & 1))) break;
-                ++nq0;
-                if (it.t0 < end0) issue_s(0, ring);
-                if (it.t0 + 1 >= end0) umma_commit(&ms->q_empty[0]);   // its only product with K: Q may be replaced
-                if (two) {
-                    if (!(ok = wait(&ms->q_full[1], nq1 & 1))) break;
-                    ++nq1;
-                    issue_s(1, ring);
-                    if (it.t0 + 1 >= end1) umma_commit(&ms->q_empty[1]);
-                }
-                umma_commit(&ms->empty[ring % C::NS]);
-                for (int t = it.t0; ok && t < it.t1; ++t) {
-                    const uint32_t rv = ring + 1 + 2 * (t - it.t0), rk = rv + 1;
-                    const bool more = t + 1 < it.t1;
-                    if (!(ok = ring_wait(rv))) break;
-                    if (more && !(ok = ring_wait(rk))) break;
-                    if (t < end0) {
-                        if (!(ok = wait(&ms->p_ready[0], np0 & 1))) break;
-                        issue_pv(0, 0, rv, t > it.t0);
-                        if (!(ok = wait(&ms->p_ready[1], np0 & 1))) break;
-                        issue_pv(0, 1, rv, true);
-                        ++np0;
-                        if (t + 1 < end0) {
-                            issue_s(0, rk);
-                            if (t + 2 >= end0) umma_commit(&ms->q_empty[0]);
-                        } else {
-                            umma_commit(&ms->o_done[0]);
-                        }
+                        for (int ks = 0; ks < BN / 16; ++ks)
+                            umma_ts(tmem + COL_O, tmem + COL_P + 64 * b + ks * 8, vb + ks * (16 * 128 >> 4), DESC_HI, IDESC_O,
+                                    ks > 0 || t > t0);
+                        umma_commit(&ms->o_done[b]);
+                        umma_commit(&ms->empty[slot]);
+                        advance(2);
                     }
-                    if (t < end1) {
-                        if (!(ok = wait(&ms->p_ready[2], np1 & 1))) break;
-                        issue_pv(1, 0, rv, t > it.t0);
-                        if (!(ok = wait(&ms->p_ready[3], np1 & 1))) break;
-                        issue_pv(1, 1, rv, true);
-                        ++np1;
-                        if (t + 1 < end1) {
-                            issue_s(1, rk);
-                            if (t + 2 >= end1) umma_commit(&ms->q_empty[1]);
-                        } else {
-                            umma_commit(&ms->o_done[1]);
-                        }
-                    }
-                    umma_commit(&ms->empty[rv % C::NS]);
-                    if (more) umma_commit(&ms->empty[rk % C::NS]);
                 }
-                ring += 2 * (it.t1 - it.t0);
             }
             if (*s_abort) {   // let the MMAs in flight finish before tensor memory is freed
                 volatile int never = 0;
-                umma_commit(&ms->drain);
-                mbar_wait(&ms->drain, 0, &never, 200000000ull);
+                umma_commit(&ms->drain[warp - 1]);
+                mbar_wait(&ms->drain[warp - 1], 0, &never, 200000000ull);
             }
         }
         __syncwarp();
     } else if (warp >= 4) {
-        // ------------------------------------------------------------------ softmax, a thread for each row
+        // ------------------------------------------------------------------ softmax, two threads for each row
         setmaxnreg_inc<208>();
-        const int x = (warp - 4) >> 2;                 // tile
-        const int r = (warp & 3) * 32 + lane;          // row of the tile = TMEM lane
+        const int grp = (warp - 4) >> 2;               // keys 64 grp .. + 63 of each tile
+        const int r = (warp & 3) * 32 + lane;          // row of the block = TMEM lane
         const int token = r / a.G, head = r - token * a.G;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + C::COL_S + 128 * x + lane_base, tO = tmem + C::COL_O + D * x + lane_base;
+        const uint32_t tS = tmem + COL_S + 64 * grp + lane_base, tP = tmem + COL_P + 32 * grp + lane_base;
+        const uint32_t tO = tmem + COL_O + D / 2 * grp + lane_base;
         const float sl2 = a.scale_log2;
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
-        uint32_t n_item = 0, ns = 0, no = 0, ring = 0;
+        uint32_t n_item = 0, n = 0, n_mail = 0;       // n: tiles
         bool ok = true;
+        // The two threads of a row exchange one float through a word each in shared memory: the value with its lowest
+        // mantissa bit replaced by a flag that alternates.  Two words are used in turn, so that one is written again only
+        // after the partner's next value has been read, which it posted after reading this one.  Both use the two encoded values, so they agree exactly;
+        // -infinity travels as the lowest float.  The wait is bounded.
+        const uint32_t mail = smem_u32(sm + C::OFF_MAIL) + (grp * BM + r) * 4;
+        auto post = [&](float &mine) {
+            const uint32_t flag = (n_mail >> 1) & 1u, at = mail + (n_mail & 1u) * (2 * BM * 4);
+            const uint32_t enc = (__float_as_uint(fmaxf(mine, -3.402823466e38f)) & ~1u) | flag;
+            mine = __uint_as_float(enc & ~1u);
+            asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(at), "r"(enc) : "memory");
+        };
+        auto receive = [&](float &theirs) -> bool {
+            const uint32_t flag = (n_mail >> 1) & 1u, at = (mail ^ (BM * 4)) + (n_mail & 1u) * (2 * BM * 4);
+            ++n_mail;
+            uint32_t w;
+            for (uint32_t n = 0;; ++n) {
+                asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+                if ((w & 1u) == flag) break;
+                if ((n & 1023u) == 1023u && (*s_abort || n > (1u << 26))) {
+                    *s_abort = 1;
+                    break;
+                }
+            }
+            theirs = __uint_as_float(w & ~1u);
+            return __all_sync(0xffffffffu, (w & 1u) == flag);
+        };
+        static_assert(C::OFF_MAIL % (2 * BM * 4) == 0, "the partner's word differs in one address bit");
+        constexpr float LOWEST = -3.0e38f;   // maxima at or below: no key seen
         while (ok) {
             const int slot = n_item % NI;
             if (!warp_wait(&ms->item_full[slot], (n_item / NI) & 1, s_abort)) break;
@@ -540,129 +545,162 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms->item_empty[slot]);
             if (it.h < 0) break;
-            const int tk = x * a.tok + token;                          // token of the block
-            const bool valid = token < a.tok && tk < it.tokens;
-            const int last = valid ? it.last + tk : -1;                  // the last key that this row sees
-            const int last0 = it.last + x * a.tok;                       // ... that the tile's first row sees
-            const int end = tile_end(a, it, x), end0 = tile_end(a, it, 0);
-            float m = -INFINITY, l = 0.f;
-            for (int t = it.t0; t < end; ++t) {
-                if (!(ok = warp_wait(&ms->s_full[x], ns & 1, s_abort))) break;
-                ++ns;
+            const bool valid = token < a.tok && token < it.tokens;
+            const int last = valid ? it.last + token : -1;               // the last key that this row sees
+            // the row's reference: numerators are 2^(s sl2 - m), at most 2^8.  Rows that do not exist need none.
+            float m = valid ? -INFINITY : 0.f, l = 0.f;
+            for (int t = it.t0; t < it.t1; ++t, ++n) {
+                const int b = n & 1;
+                if (!(ok = warp_wait(&ms->s_full[b], (n >> 1) & 1, s_abort))) break;
                 tc_fence_after();
-                uint32_t s[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32p(tS + c * 32, s + c * 32);
+                const bool fresh = m == -INFINITY;
+                uint32_t s[64];
+                tmem_ld32p(tS + 128 * b, s);
+                tmem_ld32p(tS + 128 * b + 32, s + 32);
                 tmem_ld_wait();
-                const int key0 = t * BN;
-                if (key0 + BN - 1 > last0) {
+                tc_fence_before();
+                mbar_arrive(&ms->s_free[b]);
+                const int key0 = t * BN + 64 * grp;
+                if (__builtin_expect(key0 + 63 > it.last, 0)) {
+                    const int lim = last - key0;
 #pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        if (key0 + e > last) s[e] = 0xFF800000u;   // -inf
+                    for (int e = 0; e < 64; ++e)
+                        if (e > lim) s[e] = 0xFF800000u;   // -inf
                 }
-                float mx8[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) mx8[u] = __uint_as_float(s[u]);
-#pragma unroll
-                for (int e = 8; e < 120; e += 16) {
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        mx8[u] = fmax3(mx8[u], __uint_as_float(s[e + u]), __uint_as_float(s[e + 8 + u]));
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u) mx8[u] = fmaxf(mx8[u], __uint_as_float(s[120 + u]));
-                const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
-                const float m_new = fmaxf(m, mx * sl2);
-                if (t == it.t0) {
-                    m = m_new;
-                } else if (__any_sync(0xffffffffu, m_new > m + RESCALE_LOG2)) {
-                    // S(t) is complete, so PV(t - 1), issued before it, is too
-                    const bool up = m_new > m + RESCALE_LOG2;
-                    const float alpha = !up ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
-                    if (up) m = m_new;
-                    l *= alpha;
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + c * 32, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st32(tO + c * 32, o);
-                    }
-                }
-                // a row that sees no key so far: its scores are all -inf and give p = 0 with the offset 0
-                const float m_sub = m == -INFINITY ? 0.f : m;
+                // exponents against the reference as it is, and their maximum
+                const float m_sub = fresh ? 0.f : m;
                 const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
-                uint64_t rs4[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
+                for (int e = 0; e < 64; e += 2) {
+                    float x0, x1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl2x2, nm2), x0, x1);
+                    s[e] = __float_as_uint(x0);
+                    s[e + 1] = __float_as_uint(x1);
+                }
+                float mx4[4];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
+                for (int u = 0; u < 4; ++u) mx4[u] = fmax3(__uint_as_float(s[u]), __uint_as_float(s[4 + u]), __uint_as_float(s[8 + u]));
+#pragma unroll
+                for (int e = 12; e < 60; e += 8) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        mx4[u] = fmax3(mx4[u], __uint_as_float(s[e + u]), __uint_as_float(s[e + 4 + u]));
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mx4[u] = fmaxf(mx4[u], __uint_as_float(s[60 + u]));
+                float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]), other;
+                if (!valid) mx = -INFINITY;   // rows that do not exist hold whatever lay in shared memory
+                post(mx);
+                // How far the reference has to rise.  The partner's maximum is waited for only where this thread's own
+                // exponents pass 2^8 or the row has no reference yet; else 2^x may begin, and is scaled in the rare case
+                // that the partner's word, read behind it, asks for it.
+                float d = 0.f;
+                auto rise = [&]() {
+                    mx = fmaxf(mx, other);
+                    d = mx > (fresh ? LOWEST : RESCALE_LOG2) ? mx : 0.f;
+                };
+                const bool early = __any_sync(0xffffffffu, fresh || mx > RESCALE_LOG2);
+                if (__builtin_expect(early, 0)) {
+                    if (!(ok = receive(other))) break;
+                    rise();
+                    const uint64_t nd2 = f2_pack(-d, -d);
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2) {
                         float x0, x1;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[32 * c + e]), __uint_as_float(s[32 * c + e + 1])), sl2x2, nm2), x0, x1);
-                        x0 = ex2(x0);
-                        x1 = ex2(x1);
-                        rs4[(e >> 1) & 3] = f2_add(rs4[(e >> 1) & 3], f2_pack(x0, x1));
-                        pk[e >> 1] = pack16<BF16>(x0, x1);
+                        f2_unpack(f2_add(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), nd2), x0, x1);
+                        s[e] = __float_as_uint(x0);
+                        s[e + 1] = __float_as_uint(x1);
                     }
-                    tmem_st16(tS + c * 16, pk);
-                    if (c == 1) {
-                        // the first half of P: its product may start
-                        if ((t + 1) * BN > it.keys && (x == 0 || t >= end0)) {
-                            // The rows of V behind the sequence are another's or nobody's, and a NaN times a zero weight
-                            // would be a NaN: the tile whose PV comes first zeroes them.  (The barrier cannot be a phase
-                            // further: it is that PV that frees the ring entry.)
-                            const uint32_t rv = ring + 1 + 2 * (t - it.t0);
-                            ok = warp_wait(&ms->full[rv % C::NS], (rv / C::NS) & 1, s_abort);
-                            uint8_t *vt = sm + C::OFF_RING + (rv % C::NS) * C::TILE;
-                            for (int i = max(it.keys - t * BN, 0) * 8 + r; ok && i < BN * 8; i += BM)
+                }
 #pragma unroll
-                                for (int dh = 0; dh < D / 64; ++dh)
-                                    *reinterpret_cast<uint4 *>(vt + dh * BN * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            fence_proxy_async_smem();
-                        }
-                        tmem_st_wait();
-                        tc_fence_before();
-                        mbar_arrive(&ms->p_ready[2 * x]);
+                for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(ex2(__uint_as_float(s[e])));
+                if (!early) {
+                    if (!(ok = receive(other))) break;
+                    rise();
+                    if (__builtin_expect(__any_sync(0xffffffffu, d != 0.f), 0)) {
+                        const float f = ex2(-d);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * f);
                     }
+                }
+                if (__builtin_expect(__any_sync(0xffffffffu, d != 0.f), 0)) {
+                    const float alpha = fresh ? 1.f : ex2(-d);
+                    if (!fresh) m += d;
+                    else if (mx > LOWEST) m = d;
+                    l *= alpha;
+                    if (t > it.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        // O is at rest once PV(n - 1) is complete
+                        if (!(ok = warp_wait(&ms->o_done[b ^ 1], ((n - 1) >> 1) & 1, s_abort))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 2; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st16(tO + c, o);
+                        }
+                    }
+                }
+                uint64_t rs2[2] = {0ull, 0ull};
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 64; e += 2) {
+                    const float p0 = __uint_as_float(s[e]), p1 = __uint_as_float(s[e + 1]);
+                    rs2[(e >> 1) & 1] = f2_add(rs2[(e >> 1) & 1], f2_pack(p0, p1));
+                    pk[e >> 1] = pack16<BF16>(p0, p1);
+                }
+                float r4[4];
+                f2_unpack(rs2[0], r4[0], r4[1]);
+                f2_unpack(rs2[1], r4[2], r4[3]);
+                l += (r4[0] + r4[1]) + (r4[2] + r4[3]);
+                // P(n) goes where P(n - 2) lay: its PV is complete
+                if (n >= 2) {
+                    if (!(ok = warp_wait(&ms->o_done[b], ((n >> 1) - 1) & 1, s_abort))) break;
+                    tc_fence_after();
+                }
+                tmem_st32(tP + 64 * b, pk);
+                if (__builtin_expect(t * BN + 64 * (grp + 1) > it.keys, 0)) {
+                    // The rows of V behind the sequence are another's or nobody's, and a NaN times a zero weight would be a
+                    // NaN: each group zeroes those of its half.  (The entry's barrier is at this phase, not before: what lay in
+                    // the entry is a K whose S has been seen.)
+                    const uint32_t rv = 2 * n + 2;
+                    ok = warp_wait(&ms->full[rv % C::NS], (rv / C::NS) & 1, s_abort);
+                    uint8_t *vt = sm + C::OFF_RING + (rv % C::NS) * C::PIECE;
+                    for (int i = max(it.keys - t * BN, 64 * grp) * 8 + r; ok && i < 64 * (grp + 1) * 8; i += BM)
+#pragma unroll
+                        for (int dh = 0; dh < D / 64; ++dh)
+                            *reinterpret_cast<uint4 *>(vt + dh * BN * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    if (!ok) break;
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&ms->p_ready[2 * x + 1]);
-                float r8[8];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) f2_unpack(rs4[u], r8[2 * u], r8[2 * u + 1]);
-                l += ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
-                if (!ok) break;
+                mbar_arrive(&ms->p_ready[b]);
             }
-            ring += 2 * (it.t1 - it.t0);
             if (!ok) break;
             // ---- O / l, or the partial.  The next item's first PV overwrites O only after this thread's next P,
             // which comes after these reads.
-            if (x == 1 && it.tokens <= a.tok) continue;   // no second tile
-            const bool any = it.t0 < end;
-            if (any) {
-                if (!(ok = warp_wait(&ms->o_done[x], no & 1, s_abort))) break;
-                ++no;
-                tc_fence_after();
-            }
-            const int64_t row = (int64_t)(it.q_row + tk) * a.H_q + it.h * a.G + head;
-            const int64_t prow = ((int64_t)blockIdx.x * 2 + (it.t0 == 0)) * 256 + x * BM + r;
-            const bool none = !any || l == 0.f;
+            if (!(ok = warp_wait(&ms->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, s_abort))) break;
+            tc_fence_after();
+            float other;
+            post(l);
+            if (!(ok = receive(other))) break;
+            l = grp ? other + l : l + other;
+            const int64_t row = (int64_t)(it.q_row + token) * a.H_q + it.h * a.G + head;
+            const int64_t prow = ((int64_t)blockIdx.x * 2 + (it.t0 == 0)) * BM + r;
+            const bool none = l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = 0; c < D / 2; c += 32) {
                 uint32_t o[32];
                 __syncwarp();
-                if (any) {
-                    tmem_ld32(tO + c, o);
-                    tmem_ld_wait();
-                }
+                tmem_ld32(tO + c, o);
+                tmem_ld_wait();
                 if (!valid) continue;
                 if (it.whole) {
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out) + row * (D / 2) + c / 2;
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out) + (row * D + D / 2 * grp + c) / 2;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint32_t w[4];
@@ -671,8 +709,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                             w[j] = none ? 0u : pack16<BF16>(__uint_as_float(o[e + 2 * j]) * inv, __uint_as_float(o[e + 2 * j + 1]) * inv);
                         *reinterpret_cast<uint4 *>(dst + e / 2) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                } else if (any) {
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.part_o) + prow * D + c;
+                } else {
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.part_o) + prow * D + D / 2 * grp + c;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                         *reinterpret_cast<uint4 *>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -680,8 +718,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
             tc_fence_before();
-            if (valid) {
-                if (!it.whole) a.part_ml[prow] = any ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+            if (valid && grp == 0) {
+                if (!it.whole) a.part_ml[prow] = make_float2(m, l);
                 else if (a.lse) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * LN2;
             }
         }
@@ -703,18 +741,17 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(COMBINE_THREADS) packed_combine_kernel(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int4 d = __ldcg(a.desc + 2 * blockIdx.x);   // first query row, tokens, kv head, partials
+    const int4 d = __ldcg(a.desc + blockIdx.x);   // first query row, tokens, kv head, partials
     if (d.w == 0) return;
     constexpr int LANES = D / 4, RPB = COMBINE_THREADS / LANES;
     const int lane = threadIdx.x % LANES;
     for (int i = threadIdx.x / LANES; i < COMBINE_ROWS; i += RPB) {
-        const int r = blockIdx.y * COMBINE_ROWS + i, x = r / BM, rr = r - x * BM;
-        const int token = rr / a.G, head = rr - token * a.G, tk = x * a.tok + token;
-        if (token >= a.tok || tk >= d.y) continue;
+        const int r = blockIdx.y * COMBINE_ROWS + i, token = r / a.G, head = r - token * a.G;
+        if (token >= d.y) continue;
         float m = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int p = 0; p < d.w; ++p) {
-            const int64_t prow = ((int64_t)(blockIdx.x + p) * 2 + (p == 0)) * 256 + r;
+            const int64_t prow = ((int64_t)(blockIdx.x + p) * 2 + (p == 0)) * BM + r;
             const float2 ml = __ldcg(a.part_ml + prow);
             if (ml.x == -INFINITY) continue;
             const float4 o = __ldcg(reinterpret_cast<const float4 *>(a.part_o + prow * D) + lane);
@@ -724,7 +761,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) packed_combine_kernel(const A
             acc.x = acc.x * f + o.x * w; acc.y = acc.y * f + o.y * w;
             acc.z = acc.z * f + o.z * w; acc.w = acc.w * f + o.w * w;
         }
-        const int64_t row = (int64_t)(d.x + tk) * a.H_q + d.z * a.G + head;
+        const int64_t row = (int64_t)(d.x + token) * a.H_q + d.z * a.G + head;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         reinterpret_cast<uint2 *>(a.out)[row * LANES + lane] =
             make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
@@ -746,7 +783,7 @@ int launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, packed_kernel<D, BF16>, tq, tk, tv, a) != cudaSuccess) return KVC_ECUDA;
-    cfg.gridDim = dim3(ctas, 2 * BM / COMBINE_ROWS);
+    cfg.gridDim = dim3(ctas, BM / COMBINE_ROWS);
     cfg.blockDim = dim3(COMBINE_THREADS);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, packed_combine_kernel<D, BF16>, a) != cudaSuccess) return KVC_ECUDA;
@@ -756,7 +793,7 @@ int launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv
 }  // namespace
 
 size_t packed_scratch_bytes(int, int, int, int, int head_dim) {
-    return (size_t)sm_count() * (2 * sizeof(int4) + 2 * 256 * (head_dim * sizeof(float) + sizeof(float2)));
+    return (size_t)sm_count() * (sizeof(int4) + 2 * BM * (head_dim * sizeof(float) + sizeof(float2)));
 }
 
 int launch_packed(const PackedArgs &p, void *scratch, cudaStream_t s) {
@@ -774,8 +811,8 @@ int launch_packed(const PackedArgs &p, void *scratch, cudaStream_t s) {
     a.out = p.out;
     a.lse = p.lse;
     a.desc = static_cast<int4 *>(scratch);
-    a.part_o = reinterpret_cast<float *>(a.desc + 2 * ctas);
-    a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)ctas * 2 * 256 * p.D);
+    a.part_o = reinterpret_cast<float *>(a.desc + ctas);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)ctas * 2 * BM * p.D);
     a.scale_log2 = 1.4426950408889634f / sqrtf((float)p.D);
     const bool bf = p.dtype == KVC_IN_BF16;
     const CUtensorMapDataType dt = bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
