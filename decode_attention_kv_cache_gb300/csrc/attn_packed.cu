@@ -14,21 +14,25 @@
 // block cut by a run's end leaves partial results (O, maximum, sum; at most two blocks for each CTA) that a second
 // kernel joins in the runs' order; cuts close to a block's end move there.
 //
-// Tensor memory (512 columns): S = Q K^T of a tile of 128 keys, twice (256 columns), P (its softmax numerators as 16-bit
-// pairs), twice (128), and O (D).  With two of each no step of a tile waits for another step of the same tile's
-// neighbours: S of the next two tiles - of the next block, at a block's end - are computed while the softmax of this
-// one runs, and P of the next is written while PV of this one runs.
+// Tensor memory (512 columns): S = Q K^T of a tile of 256 keys (256 columns), P (its softmax numerators as 16-bit pairs,
+// 128 columns) and O (D).  S and P are apart, so S of the next tile - of the next block, at a block's end - is computed
+// while the softmax of this one runs.  What a tile costs beside its arithmetic - waits, loads from tensor memory, the
+// exchange of maxima, about 1,500 cycles, in which all of a CTA's softmax warps wait alike - is why a tile has 256 keys:
+// with 128, S and P in two buffers each, 10,041 tokens took 962 us against TILE256 us.
 //
-// One CTA (12 warps):
+// One CTA (20 warps):
 //   warp 0     producer: walks the CTA's run of the list, passes each block on through a ring of items and
-//              loads Q (two buffers) and K and V through a ring, in the order K(0) K(1) V(0) K(2) V(1) ..., by TMA;
+//              loads Q (two buffers) and K and V (a ring each of 128-key pieces), in the order K(0) K(1) V(0) K(2) V(1)
+//              ..., by TMA;
 //   warps 1, 2   one lane of each issues the MMAs: those with K, and those with V (one thread for both spends as long in their
 //              waits and commits, about 100 and 60 cycles each, as the tensor cores on the products); warp 1 also
 //              allocates tensor memory;
-//   warps 4-7, 8-11   softmax, two threads for each row, 64 keys of each tile each.  They exchange their maxima through
-//              shared memory, but go on with the reference that the row has: it is raised, and O rescaled, only where
-//              a score passes it by more than 2^8.  Where a sequence ends inside a V tile they also set the rows
-//              behind it to zero.
+//   warps 4-19  softmax, four threads for each row, 64 keys of each tile each, 32 of either half.  They exchange their
+//              maxima through shared memory, but go on with the reference that the row has: it is raised, and O rescaled,
+//              only where a score passes it by more than 2^8.  A thread keeps 32 scores at a time (96 registers are all
+//              there are): those of the second half stay from the maximum on, so that half of S is free at once; the
+//              first half's are loaded again.  Where a sequence ends inside a piece of V these warps also set the
+//              rows behind it to zero.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -46,11 +50,13 @@ namespace {
 using namespace ptx;
 
 constexpr int BM = 128;             // rows of a block
-constexpr int BN = 128;             // keys of a tile
-constexpr int THREADS = 384;        // a warpgroup with the producer and the MMA warp, two of softmax
+constexpr int BN = 256;             // keys of a tile
+constexpr int HN = 128;             // keys of half a tile
+constexpr int GROUPS = 4;           // softmax threads of a row
+constexpr int THREADS = 128 * (1 + GROUPS);
 constexpr int NI = 4;               // items on their way from the producer
 constexpr int BLOCK_COST = 256;     // what a block costs besides its keys, in keys
-constexpr int SNAP = 4;             // a cut fewer tiles than this from an end of a block moves there
+constexpr int SNAP = 2;             // a cut fewer tiles than this from an end of a block moves there
 constexpr int MAX_DYN_SMEM = 232448;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994531f;
@@ -59,13 +65,14 @@ constexpr uint32_t TMEM_COLS = 512;
 template <int D>
 struct Cfg {
     static constexpr int PIECE = 128 * D * 2;              // 128 rows of Q, K or V
-    static constexpr int NS = D == 128 ? 5 : 11;            // ring of K and V pieces
-    static constexpr int OFF_Q = 0, OFF_RING = 2 * PIECE, OFF_MISC = OFF_RING + NS * PIECE, OFF_MAIL = OFF_MISC + 1024;
-    static constexpr int USED = OFF_MAIL + 4 * BM * 4;
+    static constexpr int KS = D == 128 ? 3 : 6, VS = D == 128 ? 2 : 5;   // pieces of K and V on their way
+    static constexpr int OFF_Q = 0, OFF_K = 2 * PIECE, OFF_V = OFF_K + KS * PIECE, OFF_MISC = OFF_V + VS * PIECE;
+    static constexpr int OFF_MAIL = OFF_MISC + 1024;
+    static constexpr int USED = OFF_MAIL + 2 * BM * GROUPS * 2;
     static constexpr int ALLOC = USED + 1024 <= MAX_DYN_SMEM ? USED + 1024 : MAX_DYN_SMEM;
     static_assert(USED <= MAX_DYN_SMEM, "shared memory plan");
 };
-constexpr uint32_t COL_S = 0, COL_P = 256, COL_O = 384;   // two S of 128 columns, two P of 64, O
+constexpr uint32_t COL_S = 0, COL_P = 256, COL_O = 384;
 
 // A block, or the part of its keys that falls into this CTA's run.
 struct Item {
@@ -73,11 +80,15 @@ struct Item {
     int h;                    // kv head; -1: no more items
     int k_row, keys;          // the sequence's first key and their number
     int last;                 // the last key that the block's first token sees (may be negative)
+    int seen;                 // keys that the block sees, at least 1
     int t0, t1;               // key tiles
     int whole;                // the run holds the whole block
 };
+// halves of tile t that the block sees something of: 1 or 2
+__device__ __forceinline__ int halves(int seen, int t) { return seen - t * BN > HN ? 2 : 1; }
+
 struct Misc {
-    uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_ready[2], o_done[2], full[12], empty[12], item_full[NI], item_empty[NI], drain[2];
+    uint64_t q_full[2], q_empty[2], s_full, s_free[2], p_ready, o_done, k_full[6], k_empty[6], v_full[6], v_empty[6], item_full[NI], item_empty[NI], drain[2];
     Item items[NI];
     unsigned long long warp_units[THREADS / 32], total, rest;
     int first_seq, abort;
@@ -157,6 +168,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
+// One arrival for a whole warp, behind what all its lanes did (32 arrivals on one word are taken one by one).
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     uint32_t r;
@@ -216,24 +233,26 @@ __global__ void __launch_bounds__(THREADS, 1)
     Misc *ms = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
     volatile int *s_abort = &ms->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < 4 * BM; i += THREADS) reinterpret_cast<uint32_t *>(sm + C::OFF_MAIL)[i] = 1u;
+    for (int i = threadIdx.x; i < BM * GROUPS; i += THREADS) reinterpret_cast<uint32_t *>(sm + C::OFF_MAIL)[i] = 0x00010001u;
     if (threadIdx.x == 0) {
         ms->abort = 0;
         for (int x = 0; x < 2; ++x) {
             mbar_init(&ms->q_full[x], 1);
-            mbar_init(&ms->q_empty[x], 1);
-            mbar_init(&ms->s_full[x], 1);
-            mbar_init(&ms->s_free[x], 256);
-            mbar_init(&ms->p_ready[x], 256);
-            mbar_init(&ms->o_done[x], 1);
+            mbar_init(&ms->q_empty[x], 4 * GROUPS);
+            mbar_init(&ms->s_free[x], 4 * GROUPS);
         }
-        for (int s = 0; s < C::NS; ++s) {
-            mbar_init(&ms->full[s], 1);
-            mbar_init(&ms->empty[s], 1);
+        mbar_init(&ms->s_full, 1);
+        mbar_init(&ms->p_ready, 4 * GROUPS);
+        mbar_init(&ms->o_done, 1);
+        for (int s = 0; s < 6; ++s) {
+            mbar_init(&ms->k_full[s], 1);
+            mbar_init(&ms->k_empty[s], 1);
+            mbar_init(&ms->v_full[s], 1);
+            mbar_init(&ms->v_empty[s], 1);
         }
         for (int s = 0; s < NI; ++s) {
             mbar_init(&ms->item_full[s], 1);
-            mbar_init(&ms->item_empty[s], 10);   // two MMA issuers, eight softmax warps
+            mbar_init(&ms->item_empty[s], 2 + 4 * GROUPS);   // the MMA issuers and the softmax warps
         }
         mbar_init(&ms->drain[0], 1);
         mbar_init(&ms->drain[1], 1);
@@ -284,13 +303,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     const uint32_t tmem = ms->tmem;
 
-    // registers: 128 * 88 + 256 * 208 = 384 * 168, what the CTA is launched with
-    if (warp < 4) setmaxnreg_dec<88>();
     if (warp == 0) {
         // ------------------------------------------------------------------ producer
         const unsigned long long W = ms->total * a.H_kv, u0 = run_start(W, blockIdx.x), u1 = run_start(W, blockIdx.x + 1);
         unsigned long long left = u1 - u0;
-        uint32_t n_item = 0, n_ring = 0, nq = 0;
+        uint32_t n_item = 0, n_k = 0, n_v = 0, nq = 0;
         bool ok = true;
         int owner_first = 0;   // this CTA begins a block that others finish
         if (lane == 0) {
@@ -346,6 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 it.tokens = min(a.tok, min(s.nq, a.n_q - s.q0) - block * a.tok);
                 it.k_row = s.k0;
                 it.keys = s.nk;
+                it.seen = seen;
                 it.last = block * a.tok + s.nk - s.nq;
                 it.whole = it.t0 == 0 && it.t1 == tiles;
                 left -= x1 - x;
@@ -380,17 +398,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             ++n_item;
             return true;
         };
-        // tile t of K or V
-        auto load_kv = [&](const CUtensorMap *m, const Item &i, int t) -> bool {
-            const int st = n_ring % C::NS;
-            if (n_ring >= (uint32_t)C::NS && !warp_wait(&ms->empty[st], ((n_ring / C::NS) - 1) & 1, s_abort)) return false;
+        auto load_piece = [&](const CUtensorMap *m, uint8_t *ring, uint64_t *full, uint64_t *empty, int slots, uint32_t &n,
+                              const Item &i, int key) -> bool {
+            const int st = n % slots;
+            if (n >= (uint32_t)slots && !warp_wait(&empty[st], ((n / slots) - 1) & 1, s_abort)) return false;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&ms->full[st], C::PIECE);
+                mbar_arrive_expect_tx(&full[st], C::PIECE);
 #pragma unroll
                 for (int dh = 0; dh < D / 64; ++dh)
-                    tma_load_3d(sm + C::OFF_RING + st * C::PIECE + dh * BN * 128, m, &ms->full[st], dh * 64, i.h, i.k_row + t * BN);
+                    tma_load_3d(ring + st * C::PIECE + dh * HN * 128, m, &full[st], dh * 64, i.h, i.k_row + key);
             }
-            ++n_ring;
+            ++n;
+            return true;
+        };
+        auto load_k = [&](const Item &i, int t) -> bool {   // the second half first
+            for (int x = halves(i.seen, t) - 1; x >= 0; --x)
+                if (!load_piece(&tm_k, sm + C::OFF_K, ms->k_full, ms->k_empty, C::KS, n_k, i, t * BN + x * HN)) return false;
+            return true;
+        };
+        auto load_v = [&](const Item &i, int t) -> bool {
+            for (int x = 0; x < halves(i.seen, t); ++x)
+                if (!load_piece(&tm_v, sm + C::OFF_V, ms->v_full, ms->v_empty, C::VS, n_v, i, t * BN + x * HN)) return false;
             return true;
         };
         Item it, nx;
@@ -408,84 +436,84 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             return true;
         };
-        if (ok && it.h >= 0) ok = load_q(it) && load_kv(&tm_k, it, it.t0);
+        if (ok && it.h >= 0) ok = load_q(it) && load_k(it, it.t0);
         while (ok && it.h >= 0) {
-            for (int t = it.t0; ok && t + 1 < it.t1; ++t) ok = load_kv(&tm_k, it, t + 1) && load_kv(&tm_v, it, t);
+            for (int t = it.t0; ok && t + 1 < it.t1; ++t) ok = load_k(it, t + 1) && load_v(it, t);
             if (!ok) break;
             next_item(nx);   // the next block's first product comes before this one's last
             ok = publish(nx);
-            if (ok && nx.h >= 0) ok = load_q(nx) && load_kv(&tm_k, nx, nx.t0);
-            else ++n_ring;   // the n-th V lies in entry 2 n + 2 also behind the last K
-            if (ok) ok = load_kv(&tm_v, it, it.t1 - 1);
+            if (ok && nx.h >= 0) ok = load_q(nx) && load_k(nx, nx.t0);
+            if (ok) ok = load_v(it, it.t1 - 1);
             it = nx;
         }
         if (!owner_first && lane == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
         if (*s_abort) {   // a wait gave up: let the copies in flight land before the CTA exits
             volatile int never = 0;
-            for (uint32_t e = n_ring > (uint32_t)C::NS ? n_ring - C::NS : 0; e < n_ring; ++e)
-                mbar_wait(&ms->full[e % C::NS], (e / C::NS) & 1, &never, 200000000ull);
+            for (uint32_t e = n_k > (uint32_t)C::KS ? n_k - C::KS : 0; e < n_k; ++e)
+                mbar_wait(&ms->k_full[e % C::KS], (e / C::KS) & 1, &never, 200000000ull);
+            for (uint32_t e = n_v > (uint32_t)C::VS ? n_v - C::VS : 0; e < n_v; ++e)
+                mbar_wait(&ms->v_full[e % C::VS], (e / C::VS) & 1, &never, 200000000ull);
             for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(&ms->q_full[i & 1], (i >> 1) & 1, &never, 200000000ull);
         }
     } else if (warp == 1 || warp == 2) {
         // ------------------------------------------------------------------ MMA issuers
-        // Warp 1 issues the products with K, warp 2 those with V.  The CTA's n-th tile has its K in entry 2 n - 1 of the ring
-        // (the first in entry 0) and its V in entry 2 n + 2.
+        // Warp 1 issues the products with K, warp 2 those with V.
         if (lane == 0) {
             constexpr uint32_t FMT = BF16 ? (1u << 7) | (1u << 10) : 0u;
-            constexpr uint32_t IDESC_S = idesc_f16(BM, BN, 0, 0) | FMT, IDESC_O = idesc_f16(BM, D, 0, 1) | FMT;
+            constexpr uint32_t IDESC_S = idesc_f16(BM, HN, 0, 0) | FMT, IDESC_O = idesc_f16(BM, D, 0, 1) | FMT;
             // descriptors: the high word is fixed, the low word is the address (in 16 bytes) under the leading offset;
             // between the steps of a product only the address moves
             constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
-            const uint32_t lo_q = (smem_u32(sm + C::OFF_Q) >> 4) | (1u << 16), lo_ring = smem_u32(sm + C::OFF_RING) >> 4;
-            uint32_t n = 0, parity = 0;           // the tile, and the parity of its entry's phase
-            int slot = warp == 1 ? 0 : 2;
+            const uint32_t lo_q = (smem_u32(sm + C::OFF_Q) >> 4) | (1u << 16), lo_k = (smem_u32(sm + C::OFF_K) >> 4) | (1u << 16);
+            const uint32_t lo_v = (smem_u32(sm + C::OFF_V) >> 4) | ((HN * 128 >> 4) << 16);
+            uint32_t n = 0, parity = 0;           // the tile, and the parity of the ring's phase
+            int slot = 0;
             bool ok = true;
-            auto advance = [&](int e) {
-                slot += e;
-                if (slot >= C::NS) { slot -= C::NS; parity ^= 1; }
-            };
             for (uint32_t n_item = 0; ok; ++n_item) {
                 const int sl = n_item % NI;
                 if (!mbar_wait(&ms->item_full[sl], (n_item / NI) & 1, s_abort)) break;
-                const int h = ms->items[sl].h, t0 = ms->items[sl].t0, t1 = ms->items[sl].t1;
+                const int h = ms->items[sl].h, t0 = ms->items[sl].t0, t1 = ms->items[sl].t1, seen = ms->items[sl].seen;
                 mbar_arrive(&ms->item_empty[sl]);
                 if (h < 0) break;
                 if (warp == 1) {
                     const int qb = n_item & 1;
                     const uint32_t q = lo_q + qb * (C::PIECE >> 4);
                     if (!mbar_wait(&ms->q_full[qb], (n_item >> 1) & 1, s_abort)) break;
-                    for (int t = t0; t < t1; ++t, ++n) {
-                        const int b = n & 1;
-                        if (!(ok = mbar_wait(&ms->full[slot], parity, s_abort))) break;
-                        // the softmax has read the S that lay here
-                        if (n >= 2 && !(ok = mbar_wait(&ms->s_free[b], ((n >> 1) - 1) & 1, s_abort))) break;
-                        tc_fence_after();
-                        const uint32_t kb = (lo_ring + slot * (C::PIECE >> 4)) | (1u << 16), d = tmem + COL_S + 128 * b;
+                    for (int t = t0; ok && t < t1; ++t, ++n) {
+#pragma unroll 1
+                        for (int x = halves(seen, t) - 1; x >= 0; --x) {
+                            // the piece has landed, and the softmax has read what lay in this half of S
+                            if (!(ok = mbar_wait(&ms->k_full[slot], parity, s_abort))) break;
+                            if (n > 0 && !(ok = mbar_wait(&ms->s_free[x], (n - 1) & 1, s_abort))) break;
+                            tc_fence_after();
+                            const uint32_t kb = lo_k + slot * (C::PIECE >> 4), d = tmem + COL_S + HN * x;
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t off = (ks >> 2) * (128 * 128 >> 4) + (ks & 3) * 2;
-                            umma_ss(d, q + off, kb + off, DESC_HI, IDESC_S, ks > 0);
+                            for (int ks = 0; ks < D / 16; ++ks) {
+                                const uint32_t off = (ks >> 2) * (128 * 128 >> 4) + (ks & 3) * 2;
+                                umma_ss(d, q + off, kb + off, DESC_HI, IDESC_S, ks > 0);
+                            }
+                            if (x == 0) umma_commit(&ms->s_full);
+                            umma_commit(&ms->k_empty[slot]);
+                            if (++slot == C::KS) { slot = 0; parity ^= 1; }
                         }
-                        umma_commit(&ms->s_full[b]);
-                        umma_commit(&ms->empty[slot]);
-                        if (t + 1 == t1) umma_commit(&ms->q_empty[qb]);
-                        advance(n == 0 ? 1 : 2);
                     }
                 } else {
-                    for (int t = t0; t < t1; ++t, ++n) {
-                        const int b = n & 1;
-                        if (!(ok = mbar_wait(&ms->full[slot], parity, s_abort) &&
-                                   mbar_wait(&ms->p_ready[b], (n >> 1) & 1, s_abort)))
-                            break;
-                        tc_fence_after();
-                        const uint32_t vb = (lo_ring + slot * (C::PIECE >> 4)) | ((BN * 128 >> 4) << 16);
+                    for (int t = t0; ok && t < t1; ++t, ++n) {
+                        const int e = halves(seen, t);
+#pragma unroll 1
+                        for (int x = 0; x < e; ++x) {
+                            if (!(ok = mbar_wait(&ms->v_full[slot], parity, s_abort))) break;
+                            if (x == 0 && !(ok = mbar_wait(&ms->p_ready, n & 1, s_abort))) break;
+                            tc_fence_after();
+                            const uint32_t vb = lo_v + slot * (C::PIECE >> 4);
 #pragma unroll
-                        for (int ks = 0; ks < BN / 16; ++ks)
-                            umma_ts(tmem + COL_O, tmem + COL_P + 64 * b + ks * 8, vb + ks * (16 * 128 >> 4), DESC_HI, IDESC_O,
-                                    ks > 0 || t > t0);
-                        umma_commit(&ms->o_done[b]);
-                        umma_commit(&ms->empty[slot]);
-                        advance(2);
+                            for (int ks = 0; ks < HN / 16; ++ks)
+                                umma_ts(tmem + COL_O, tmem + COL_P + 64 * x + ks * 8, vb + ks * (16 * 128 >> 4), DESC_HI, IDESC_O,
+                                        ks > 0 || x > 0 || t > t0);
+                            if (x + 1 == e) umma_commit(&ms->o_done);
+                            umma_commit(&ms->v_empty[slot]);
+                            if (++slot == C::VS) { slot = 0; parity ^= 1; }
+                        }
                     }
                 }
             }
@@ -497,143 +525,158 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
     } else if (warp >= 4) {
-        // ------------------------------------------------------------------ softmax, two threads for each row
-        setmaxnreg_inc<208>();
-        const int grp = (warp - 4) >> 2;               // keys 64 grp .. + 63 of each tile
+        // ------------------------------------------------------------------ softmax, four threads for each row
+        const int grp = (warp - 4) >> 2;               // keys 32 grp .. + 31 of each half
         const int r = (warp & 3) * 32 + lane;          // row of the block = TMEM lane
-        const int token = r / a.G, head = r - token * a.G;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + COL_S + 64 * grp + lane_base, tP = tmem + COL_P + 32 * grp + lane_base;
-        const uint32_t tO = tmem + COL_O + D / 2 * grp + lane_base;
+        const uint32_t tS = tmem + COL_S + 32 * grp + lane_base, tP = tmem + COL_P + 16 * grp + lane_base;
+        const uint32_t tO = tmem + COL_O + D / GROUPS * grp + lane_base;
         const float sl2 = a.scale_log2;
-        const uint64_t sl2x2 = f2_pack(sl2, sl2);
-        uint32_t n_item = 0, n = 0, n_mail = 0;       // n: tiles
+        uint32_t n = 0, n_v = 0, n_mail = 0;           // tiles, pieces of V, exchanges
         bool ok = true;
-        // The two threads of a row exchange one float through a word each in shared memory: the value with its lowest
-        // mantissa bit replaced by a flag that alternates.  Two words are used in turn, so that one is written again only
-        // after the partner's next value has been read, which it posted after reading this one.  Both use the two encoded values, so they agree exactly;
-        // -infinity travels as the lowest float.  The wait is bounded.
-        const uint32_t mail = smem_u32(sm + C::OFF_MAIL) + (grp * BM + r) * 4;
-        auto post = [&](float &mine) {
-            const uint32_t flag = (n_mail >> 1) & 1u, at = mail + (n_mail & 1u) * (2 * BM * 4);
-            const uint32_t enc = (__float_as_uint(fmaxf(mine, -3.402823466e38f)) & ~1u) | flag;
-            mine = __uint_as_float(enc & ~1u);
-            asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(at), "r"(enc) : "memory");
+        // The four threads of a row exchange 15 bits each through shared memory; the 16th is a flag that alternates, so that
+        // a word says by itself that it is new.  Two sets of words are used in turn: one is written again only after all
+        // four have posted to the other, which each does after reading this one.  All read the same four words, so they
+        // agree exactly.  The wait is bounded.
+        const uint32_t mail = smem_u32(sm + C::OFF_MAIL) + r * (2 * GROUPS);
+        auto post = [&](uint32_t bits) {
+            const uint16_t w = (uint16_t)((bits & 0xFFFEu) | ((n_mail >> 1) & 1u));
+            asm volatile("st.volatile.shared.b16 [%0], %1;" ::"r"(mail + (n_mail & 1u) * (BM * GROUPS * 2) + 2 * grp), "h"(w) : "memory");
         };
-        auto receive = [&](float &theirs) -> bool {
-            const uint32_t flag = (n_mail >> 1) & 1u, at = (mail ^ (BM * 4)) + (n_mail & 1u) * (2 * BM * 4);
+        auto receive = [&](uint32_t &w0, uint32_t &w1) -> bool {
+            const uint32_t flags = ((n_mail >> 1) & 1u) * 0x00010001u, at = mail + (n_mail & 1u) * (BM * GROUPS * 2);
             ++n_mail;
-            uint32_t w;
-            for (uint32_t n = 0;; ++n) {
-                asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
-                if ((w & 1u) == flag) break;
-                if ((n & 1023u) == 1023u && (*s_abort || n > (1u << 26))) {
+            bool here = false;
+            for (uint32_t i = 0;; ++i) {
+                asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
+                here = (((w0 ^ flags) | (w1 ^ flags)) & 0x00010001u) == 0;
+                if (here) break;
+                if ((i & 1023u) == 1023u && (*s_abort || i > (1u << 26))) {
                     *s_abort = 1;
                     break;
                 }
             }
-            theirs = __uint_as_float(w & ~1u);
-            return __all_sync(0xffffffffu, (w & 1u) == flag);
+            return __all_sync(0xffffffffu, here);
         };
-        static_assert(C::OFF_MAIL % (2 * BM * 4) == 0, "the partner's word differs in one address bit");
-        constexpr float LOWEST = -3.0e38f;   // maxima at or below: no key seen
-        while (ok) {
-            const int slot = n_item % NI;
-            if (!warp_wait(&ms->item_full[slot], (n_item / NI) & 1, s_abort)) break;
-            const Item it = ms->items[slot];
-            ++n_item;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ms->item_empty[slot]);
+        // The maximum of four values, as fp16 without the last bit: the values are exponents relative to the row's reference,
+        // which may be any number not far from their maximum.  -infinity travels as the lowest number.
+        auto maximum4 = [&](float v, float &all) -> bool {
+            uint32_t w0, w1;
+            post(__half_as_ushort(__float2half_rn(fminf(fmaxf(v, -65000.f), 65000.f))));
+            const bool k = receive(w0, w1);
+            const __half2 mx = __hmax2(*reinterpret_cast<__half2 *>(&w0), *reinterpret_cast<__half2 *>(&w1));
+            all = fmaxf(__low2float(mx), __high2float(mx));
+            return k;
+        };
+        // The sum of four float32, in the groups' order, in two exchanges: all but the last two bits of each.
+        auto sum4 = [&](float v, float &all) -> bool {
+            const uint32_t u = __float_as_uint(v);
+            uint32_t h0, h1, l0, l1;
+            post(u >> 16);
+            bool k = receive(h0, h1);
+            post(u >> 1);
+            k = receive(l0, l1) && k;
+            auto join = [](uint32_t h, uint32_t lo) { return __uint_as_float((h & 0xFFFEu) << 16 | (lo & 0xFFFEu) << 1); };
+            all = ((join(h0, l0) + join(h0 >> 16, l0 >> 16)) + join(h1, l1)) + join(h1 >> 16, l1 >> 16);
+            return k;
+        };
+        constexpr float LOWEST = -60000.f, HIGHEST = 60000.f;   // at or below: no key seen; at or above: more to come
+        for (uint32_t n_item = 0; ok; ++n_item) {
+            // the item stays in its slot until the block is done
+            if (!warp_wait(&ms->item_full[n_item % NI], (n_item / NI) & 1, s_abort)) break;
+            const volatile Item &it = const_cast<const volatile Item &>(ms->items[n_item % NI]);
             if (it.h < 0) break;
-            const bool valid = token < a.tok && token < it.tokens;
-            const int last = valid ? it.last + token : -1;               // the last key that this row sees
+            const int t0 = it.t0, t1 = it.t1, first_last = it.last;
+            int last;       // the last key that this row sees
+            bool valid;
+            {
+                const int token = r / a.G;
+                valid = token < a.tok && token < it.tokens;
+                last = valid ? first_last + token : -1;
+            }
             // the row's reference: numerators are 2^(s sl2 - m), at most 2^8.  Rows that do not exist need none.
             float m = valid ? -INFINITY : 0.f, l = 0.f;
-            for (int t = it.t0; t < it.t1; ++t, ++n) {
-                const int b = n & 1;
-                if (!(ok = warp_wait(&ms->s_full[b], (n >> 1) & 1, s_abort))) break;
-                tc_fence_after();
-                const bool fresh = m == -INFINITY;
-                uint32_t s[64];
-                tmem_ld32p(tS + 128 * b, s);
-                tmem_ld32p(tS + 128 * b + 32, s + 32);
+            // this thread's 32 scores of a half; keys that the row does not see get -infinity
+            auto load = [&](uint32_t (&s)[32], int t, int x) {
+                tmem_ld32p(tS + HN * x, s);
                 tmem_ld_wait();
-                tc_fence_before();
-                mbar_arrive(&ms->s_free[b]);
-                const int key0 = t * BN + 64 * grp;
-                if (__builtin_expect(key0 + 63 > it.last, 0)) {
+                const int key0 = t * BN + HN * x + 32 * grp;
+                if (__builtin_expect(key0 + 31 > first_last, 0)) {
                     const int lim = last - key0;
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        if (e > lim) s[e] = 0xFF800000u;   // -inf
+                    for (int e = 0; e < 32; ++e)
+                        if (e > lim) s[e] = 0xFF800000u;
                 }
-                // exponents against the reference as it is, and their maximum
-                const float m_sub = fresh ? 0.f : m;
-                const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
+            };
+            auto maximum = [&](const uint32_t (&s)[32], float from) {
+                float m4[4];
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) {
-                    float x0, x1;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl2x2, nm2), x0, x1);
-                    s[e] = __float_as_uint(x0);
-                    s[e + 1] = __float_as_uint(x1);
-                }
-                float mx4[4];
+                for (int u = 0; u < 4; ++u) m4[u] = fmax3(__uint_as_float(s[u]), __uint_as_float(s[4 + u]), __uint_as_float(s[8 + u]));
 #pragma unroll
-                for (int u = 0; u < 4; ++u) mx4[u] = fmax3(__uint_as_float(s[u]), __uint_as_float(s[4 + u]), __uint_as_float(s[8 + u]));
-#pragma unroll
-                for (int e = 12; e < 60; e += 8) {
+                for (int e = 12; e < 28; e += 8)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        mx4[u] = fmax3(mx4[u], __uint_as_float(s[e + u]), __uint_as_float(s[e + 4 + u]));
+                        m4[u] = fmax3(m4[u], __uint_as_float(s[e + u]), __uint_as_float(s[e + 4 + u]));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) m4[u] = fmaxf(m4[u], __uint_as_float(s[28 + u]));
+                return fmaxf(fmax3(m4[0], m4[1], m4[2]), fmaxf(m4[3], from));
+            };
+            // numerators in place: the first 16 words become the pairs; their sum is added to l
+            auto numerators = [&](uint32_t (&s)[32]) {
+                const float m_sub = m == -INFINITY ? 0.f : m;
+                const uint64_t nm2 = f2_pack(-m_sub, -m_sub), sl2x2 = f2_pack(sl2, sl2);
+                uint64_t rs2[2] = {0ull, 0ull};
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float x0, x1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl2x2, nm2), x0, x1);
+                    x0 = ex2(x0);
+                    x1 = ex2(x1);
+                    rs2[(e >> 1) & 1] = f2_add(rs2[(e >> 1) & 1], f2_pack(x0, x1));
+                    s[e >> 1] = pack16<BF16>(x0, x1);
                 }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) mx4[u] = fmaxf(mx4[u], __uint_as_float(s[60 + u]));
-                float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]), other;
-                if (!valid) mx = -INFINITY;   // rows that do not exist hold whatever lay in shared memory
-                post(mx);
-                // How far the reference has to rise.  The partner's maximum is waited for only where this thread's own
-                // exponents pass 2^8 or the row has no reference yet; else 2^x may begin, and is scaled in the rare case
-                // that the partner's word, read behind it, asks for it.
-                float d = 0.f;
-                auto rise = [&]() {
-                    mx = fmaxf(mx, other);
-                    d = mx > (fresh ? LOWEST : RESCALE_LOG2) ? mx : 0.f;
-                };
-                const bool early = __any_sync(0xffffffffu, fresh || mx > RESCALE_LOG2);
-                if (__builtin_expect(early, 0)) {
-                    if (!(ok = receive(other))) break;
-                    rise();
-                    const uint64_t nd2 = f2_pack(-d, -d);
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        float x0, x1;
-                        f2_unpack(f2_add(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), nd2), x0, x1);
-                        s[e] = __float_as_uint(x0);
-                        s[e + 1] = __float_as_uint(x1);
+                float r4[4];
+                f2_unpack(rs2[0], r4[0], r4[1]);
+                f2_unpack(rs2[1], r4[2], r4[3]);
+                l += (r4[0] + r4[1]) + (r4[2] + r4[3]);
+            };
+            for (int t = t0; t < t1; ++t, ++n) {
+                if (!(ok = warp_wait(&ms->s_full, n & 1, s_abort))) break;
+                tc_fence_after();
+                const bool both = halves(it.seen, t) == 2;
+                uint32_t s0[32], s1[32];
+                load(s0, t, 0);
+                float mx = maximum(s0, -INFINITY);
+                if (both) {
+                    load(s1, t, 1);
+                    mx = maximum(s1, mx);
+                }
+                tc_fence_before();
+                arrive_warp(&ms->s_free[1]);
+                // how far the scores pass the reference
+                const bool fresh = m == -INFINITY;
+                const float m_sub = fresh ? 0.f : m;
+                if (!valid) mx = -INFINITY;   // rows that do not exist hold anything
+                float up;
+                if (!(ok = maximum4(mx * sl2 - m_sub, up))) break;
+                const bool seen = up > LOWEST;
+                if (__builtin_expect(__any_sync(0xffffffffu, fresh ? seen : up > RESCALE_LOG2), 0)) {
+                    // the reference rises, or is set; where the maximum was too large to be told, again
+                    float sum = (fresh ? seen : up > RESCALE_LOG2) ? up : 0.f;
+                    while (!__all_sync(0xffffffffu, up < HIGHEST)) {
+                        if (!(ok = maximum4(mx * sl2 - m_sub - sum, up))) break;
+                        sum += fmaxf(up, 0.f);
                     }
-                }
-#pragma unroll
-                for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(ex2(__uint_as_float(s[e])));
-                if (!early) {
-                    if (!(ok = receive(other))) break;
-                    rise();
-                    if (__builtin_expect(__any_sync(0xffffffffu, d != 0.f), 0)) {
-                        const float f = ex2(-d);
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * f);
-                    }
-                }
-                if (__builtin_expect(__any_sync(0xffffffffu, d != 0.f), 0)) {
-                    const float alpha = fresh ? 1.f : ex2(-d);
-                    if (!fresh) m += d;
-                    else if (mx > LOWEST) m = d;
+                    if (!ok) break;
+                    const float alpha = fresh ? 1.f : ex2(-sum);
+                    if (!fresh || seen) m = m_sub + sum;
                     l *= alpha;
-                    if (t > it.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    if (t > t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         // O is at rest once PV(n - 1) is complete
-                        if (!(ok = warp_wait(&ms->o_done[b ^ 1], ((n - 1) >> 1) & 1, s_abort))) break;
+                        if (!(ok = warp_wait(&ms->o_done, (n - 1) & 1, s_abort))) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D / 2; c += 16) {
+                        for (int c = 0; c < D / GROUPS; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(tO + c, o);
                             tmem_ld_wait();
@@ -643,85 +686,107 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                uint64_t rs2[2] = {0ull, 0ull};
-                uint32_t pk[32];
-#pragma unroll
-                for (int e = 0; e < 64; e += 2) {
-                    const float p0 = __uint_as_float(s[e]), p1 = __uint_as_float(s[e + 1]);
-                    rs2[(e >> 1) & 1] = f2_add(rs2[(e >> 1) & 1], f2_pack(p0, p1));
-                    pk[e >> 1] = pack16<BF16>(p0, p1);
+                if (both) {
+                    numerators(s1);
+                    load(s0, t, 0);
+                    tc_fence_before();
                 }
-                float r4[4];
-                f2_unpack(rs2[0], r4[0], r4[1]);
-                f2_unpack(rs2[1], r4[2], r4[3]);
-                l += (r4[0] + r4[1]) + (r4[2] + r4[3]);
-                // P(n) goes where P(n - 2) lay: its PV is complete
-                if (n >= 2) {
-                    if (!(ok = warp_wait(&ms->o_done[b], ((n >> 1) - 1) & 1, s_abort))) break;
+                arrive_warp(&ms->s_free[0]);
+                numerators(s0);
+                // P is free once PV(n - 1) is complete
+                if (n > 0) {
+                    if (!(ok = warp_wait(&ms->o_done, (n - 1) & 1, s_abort))) break;
                     tc_fence_after();
                 }
-                tmem_st32(tP + 64 * b, pk);
-                if (__builtin_expect(t * BN + 64 * (grp + 1) > it.keys, 0)) {
+                if (both) tmem_st16(tP + 64, s1);
+                tmem_st16(tP, s0);
+                if (__builtin_expect(t + 1 == t1 && t * BN + HN * (both + 1) > it.keys, 0)) {
                     // The rows of V behind the sequence are another's or nobody's, and a NaN times a zero weight would be a
-                    // NaN: each group zeroes those of its half.  (The entry's barrier is at this phase, not before: what lay in
-                    // the entry is a K whose S has been seen.)
-                    const uint32_t rv = 2 * n + 2;
-                    ok = warp_wait(&ms->full[rv % C::NS], (rv / C::NS) & 1, s_abort);
-                    uint8_t *vt = sm + C::OFF_RING + (rv % C::NS) * C::PIECE;
-                    for (int i = max(it.keys - t * BN, 64 * grp) * 8 + r; ok && i < 64 * (grp + 1) * 8; i += BM)
+                    // NaN: they are zeroed in the tile's last piece.  (The piece's barrier is at this phase, not before: what
+                    // lay there has been used by a PV that is complete.)
+                    const uint32_t rv = n_v + both;
+                    if (!(ok = warp_wait(&ms->v_full[rv % C::VS], (rv / C::VS) & 1, s_abort))) break;
+                    uint8_t *vt = sm + C::OFF_V + (rv % C::VS) * C::PIECE;
+                    for (int i = max(it.keys - t * BN - HN * both, 0) * 8 + grp * BM + r; i < HN * 8; i += GROUPS * BM)
 #pragma unroll
                         for (int dh = 0; dh < D / 64; ++dh)
-                            *reinterpret_cast<uint4 *>(vt + dh * BN * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(vt + dh * HN * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
-                    if (!ok) break;
                 }
+                n_v += 1 + both;
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&ms->p_ready[b]);
+                arrive_warp(&ms->p_ready);
             }
             if (!ok) break;
             // ---- O / l, or the partial.  The next item's first PV overwrites O only after this thread's next P,
             // which comes after these reads.
-            if (!(ok = warp_wait(&ms->o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, s_abort))) break;
+            if (!(ok = warp_wait(&ms->o_done, (n - 1) & 1, s_abort))) break;
             tc_fence_after();
-            float other;
-            post(l);
-            if (!(ok = receive(other))) break;
-            l = grp ? other + l : l + other;
-            const int64_t row = (int64_t)(it.q_row + token) * a.H_q + it.h * a.G + head;
-            const int64_t prow = ((int64_t)blockIdx.x * 2 + (it.t0 == 0)) * BM + r;
+            if (!(ok = sum4(l, l))) break;
+            const int token = r / a.G, head = r - token * a.G, h = it.h;
+            const bool whole = it.whole;
+            const int64_t row = (int64_t)(it.q_row + token) * a.H_q + h * a.G + head;
+            const int64_t prow = ((int64_t)blockIdx.x * 2 + (t0 == 0)) * BM + r;
+            arrive_warp(&ms->item_empty[n_item % NI]);
             const bool none = l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
-#pragma unroll 1
-            for (int c = 0; c < D / 2; c += 32) {
-                uint32_t o[32];
+            // A row's columns lie in one lane, so a store of them by all lanes would touch 32 lines: the warp turns its rows
+            // by RS bytes each in a patch of its own in the item's Q buffer (its last S is complete), and stores eight (D =
+            // 64: sixteen) rows' pieces at a time.
+            constexpr int RS = D / 2, CH = RS / 16;   // bytes and 16-byte chunks of a row in the patch
+            const uint32_t patch = smem_u32(sm + C::OFF_Q + (n_item & 1) * C::PIECE) + (warp - 4) * 32 * RS;
+            auto place = [](int row, int chunk) { return row * RS + ((chunk ^ (CH == 4 ? (row >> 1) & 3 : (row >> 2) & 1)) << 4); };
+            auto put = [&](int chunk, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(patch + place(lane, chunk)), "r"(w0), "r"(w1), "r"(w2), "r"(w3) : "memory");
+            };
+            // the patch to each row's place: base + RS bytes from `at` of the lane that holds the row, or nowhere if negative
+            auto flush = [&](uint8_t *base, int64_t at) {
                 __syncwarp();
-                tmem_ld32(tO + c, o);
-                tmem_ld_wait();
-                if (!valid) continue;
-                if (it.whole) {
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out) + (row * D + D / 2 * grp + c) / 2;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = none ? 0u : pack16<BF16>(__uint_as_float(o[e + 2 * j]) * inv, __uint_as_float(o[e + 2 * j + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(dst + e / 2) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else {
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.part_o) + prow * D + D / 2 * grp + c;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4 *>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                for (int i = 0; i < CH; ++i) {
+                    const int rr = i * (32 / CH) + lane / CH, ch = lane % CH;
+                    const int64_t to = __shfl_sync(0xffffffffu, at, rr);
+                    uint32_t w0, w1, w2, w3;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w0), "=r"(w1), "=r"(w2), "=r"(w3) : "r"(patch + place(rr, ch)) : "memory");
+                    if (to >= 0) *reinterpret_cast<uint4 *>(base + to + 16 * ch) = make_uint4(w0, w1, w2, w3);
                 }
+                __syncwarp();
+            };
+            constexpr int EC = D / GROUPS;            // this thread's columns of O
+            if (whole) {
+#pragma unroll 1
+                for (int c = 0; c < EC; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(tO + c, o);
+                    tmem_ld_wait();
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = none ? 0u : pack16<BF16>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                    put(c / 8, w[0], w[1], w[2], w[3]);
+                    put(c / 8 + 1, w[4], w[5], w[6], w[7]);
+                }
+                flush(static_cast<uint8_t *>(a.out), valid ? (row * D + EC * grp) * 2 : -1);
+                if (valid && grp == 0 && a.lse) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * LN2;
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < EC; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(tO + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4 * CH) {
+#pragma unroll
+                        for (int k = 0; k < CH; ++k) put(k, o[j + 4 * k], o[j + 4 * k + 1], o[j + 4 * k + 2], o[j + 4 * k + 3]);
+                        flush(reinterpret_cast<uint8_t *>(a.part_o), valid ? (prow * D + EC * grp + c + j) * 4 : -1);
+                    }
+                }
+                if (valid && grp == 0) a.part_ml[prow] = make_float2(m, l);
             }
-            __syncwarp();
             tc_fence_before();
-            if (valid && grp == 0) {
-                if (!it.whole) a.part_ml[prow] = make_float2(m, l);
-                else if (a.lse) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * LN2;
-            }
+            fence_proxy_async_smem();
+            arrive_warp(&ms->q_empty[n_item & 1]);
         }
     }
     tc_fence_before();
@@ -823,8 +888,8 @@ int launch_packed(const PackedArgs &p, void *scratch, cudaStream_t s) {
                            CU_TENSOR_MAP_SWIZZLE_128B);
     };
     if (!map(&tq, p.q, p.H_q, p.n_q, p.ld_q, a.G, a.tok) ||
-        !map(&tk, none ? p.q : p.k, p.H_kv, none ? 1 : p.n_k, none ? p.ld_q : p.ld_k, 1, BN) ||
-        !map(&tv, none ? p.q : p.v, p.H_kv, none ? 1 : p.n_k, none ? p.ld_q : p.ld_v, 1, BN))
+        !map(&tk, none ? p.q : p.k, p.H_kv, none ? 1 : p.n_k, none ? p.ld_q : p.ld_k, 1, HN) ||
+        !map(&tv, none ? p.q : p.v, p.H_kv, none ? 1 : p.n_k, none ? p.ld_q : p.ld_v, 1, HN))
         return KVC_ECUDA;
     if (p.D == 128) return bf ? launch_t<128, true>(tq, tk, tv, a, ctas, s) : launch_t<128, false>(tq, tk, tv, a, ctas, s);
     return bf ? launch_t<64, true>(tq, tk, tv, a, ctas, s) : launch_t<64, false>(tq, tk, tv, a, ctas, s);
