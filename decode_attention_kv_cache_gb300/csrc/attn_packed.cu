@@ -29,10 +29,8 @@
 //              allocates tensor memory;
 //   warps 4-19  softmax, four threads for each row, 64 keys of each tile each, 32 of either half.  They exchange their
 //              maxima through shared memory, but go on with the reference that the row has: it is raised, and O rescaled,
-//              only where a score passes it by more than 2^8.  A thread keeps 32 scores at a time (96 registers are all
-//              there are): those of the second half stay from the maximum on, so that half of S is free at once; the
-//              first half's are loaded again.  Where a sequence ends inside a piece of V these warps also set the
-//              rows behind it to zero.
+//              only where a score passes it by more than 2^8.  Where a sequence ends inside a piece of V these warps
+//              also set the rows behind it to zero.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -55,7 +53,7 @@ constexpr int HN = 128;             // keys of half a tile
 constexpr int GROUPS = 4;           // softmax threads of a row
 constexpr int THREADS = 128 * (1 + GROUPS);
 constexpr int NI = 4;               // items on their way from the producer
-constexpr int BLOCK_COST = 256;     // what a block costs besides its keys, in keys
+constexpr int BLOCK_COST = 512;     // what a block costs besides its keys, in keys
 constexpr int SNAP = 2;             // a cut fewer tiles than this from an end of a block moves there
 constexpr int MAX_DYN_SMEM = 232448;
 constexpr float RESCALE_LOG2 = 8.0f;
@@ -88,7 +86,7 @@ struct Item {
 __device__ __forceinline__ int halves(int seen, int t) { return seen - t * BN > HN ? 2 : 1; }
 
 struct Misc {
-    uint64_t q_full[2], q_empty[2], s_full, s_free[2], p_ready, o_done, k_full[6], k_empty[6], v_full[6], v_empty[6], item_full[NI], item_empty[NI], drain[2];
+    uint64_t q_full[2], q_empty[2], s_full, s_free, p_ready, o_done, k_full[6], k_empty[6], v_full[6], v_empty[6], item_full[NI], item_empty[NI], drain[2];
     Item items[NI];
     unsigned long long warp_units[THREADS / 32], total, rest;
     int first_seq, abort;
@@ -239,8 +237,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int x = 0; x < 2; ++x) {
             mbar_init(&ms->q_full[x], 1);
             mbar_init(&ms->q_empty[x], 4 * GROUPS);
-            mbar_init(&ms->s_free[x], 4 * GROUPS);
         }
+        mbar_init(&ms->s_free, 4 * GROUPS);
         mbar_init(&ms->s_full, 1);
         mbar_init(&ms->p_ready, 4 * GROUPS);
         mbar_init(&ms->o_done, 1);
@@ -303,6 +301,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     const uint32_t tmem = ms->tmem;
 
+    // registers: 128 * 64 + 512 * 104 = 640 * 96, what the CTA is launched with
+    if (warp < 4) setmaxnreg_dec<64>();
     if (warp == 0) {
         // ------------------------------------------------------------------ producer
         const unsigned long long W = ms->total * a.H_kv, u0 = run_start(W, blockIdx.x), u1 = run_start(W, blockIdx.x + 1);
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int x = halves(seen, t) - 1; x >= 0; --x) {
                             // the piece has landed, and the softmax has read what lay in this half of S
                             if (!(ok = mbar_wait(&ms->k_full[slot], parity, s_abort))) break;
-                            if (n > 0 && !(ok = mbar_wait(&ms->s_free[x], (n - 1) & 1, s_abort))) break;
+                            if (n > 0 && !(ok = mbar_wait(&ms->s_free, (n - 1) & 1, s_abort))) break;
                             tc_fence_after();
                             const uint32_t kb = lo_k + slot * (C::PIECE >> 4), d = tmem + COL_S + HN * x;
 #pragma unroll
@@ -526,6 +526,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------------ softmax, four threads for each row
+        setmaxnreg_inc<104>();
         const int grp = (warp - 4) >> 2;               // keys 32 grp .. + 31 of each half
         const int r = (warp & 3) * 32 + lane;          // row of the block = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -596,11 +597,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             // the row's reference: numerators are 2^(s sl2 - m), at most 2^8.  Rows that do not exist need none.
             float m = valid ? -INFINITY : 0.f, l = 0.f;
-            // this thread's 32 scores of a half; keys that the row does not see get -infinity
-            auto load = [&](uint32_t (&s)[32], int t, int x) {
-                tmem_ld32p(tS + HN * x, s);
-                tmem_ld_wait();
-                const int key0 = t * BN + HN * x + 32 * grp;
+            // keys that the row does not see get -infinity
+            auto mask = [&](uint32_t (&s)[32], int key0) {
                 if (__builtin_expect(key0 + 31 > first_last, 0)) {
                     const int lim = last - key0;
 #pragma unroll
@@ -644,15 +642,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!(ok = warp_wait(&ms->s_full, n & 1, s_abort))) break;
                 tc_fence_after();
                 const bool both = halves(it.seen, t) == 2;
-                uint32_t s0[32], s1[32];
-                load(s0, t, 0);
+                uint32_t s0[32], s1[32];           // this thread's scores of either half
+                tmem_ld32p(tS, s0);
+                if (both) tmem_ld32p(tS + HN, s1);
+                tmem_ld_wait();
+                tc_fence_before();
+                arrive_warp(&ms->s_free);
+                mask(s0, t * BN + 32 * grp);
                 float mx = maximum(s0, -INFINITY);
                 if (both) {
-                    load(s1, t, 1);
+                    mask(s1, t * BN + HN + 32 * grp);
                     mx = maximum(s1, mx);
                 }
-                tc_fence_before();
-                arrive_warp(&ms->s_free[1]);
                 // how far the scores pass the reference
                 const bool fresh = m == -INFINITY;
                 const float m_sub = fresh ? 0.f : m;
@@ -686,12 +687,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                if (both) {
-                    numerators(s1);
-                    load(s0, t, 0);
-                    tc_fence_before();
-                }
-                arrive_warp(&ms->s_free[0]);
+                if (both) numerators(s1);
                 numerators(s0);
                 // P is free once PV(n - 1) is complete
                 if (n > 0) {
