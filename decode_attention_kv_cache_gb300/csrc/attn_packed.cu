@@ -533,6 +533,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t tS = tmem + COL_S + 32 * grp + lane_base, tP = tmem + COL_P + 16 * grp + lane_base;
         const uint32_t tO = tmem + COL_O + D / GROUPS * grp + lane_base;
         const float sl2 = a.scale_log2;
+        // token of the block (one that no block has, for rows behind its last) and place among its rows of the output
+        const int token = r / a.G < a.tok ? r / a.G : INT32_MAX, row_off = r / a.G * a.H_q + r % a.G;
         uint32_t n = 0, n_v = 0, n_mail = 0;           // tiles, pieces of V, exchanges
         bool ok = true;
         // The four threads of a row exchange 15 bits each through shared memory; the 16th is a flag that alternates, so that
@@ -590,11 +592,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int t0 = it.t0, t1 = it.t1, first_last = it.last;
             int last;       // the last key that this row sees
             bool valid;
-            {
-                const int token = r / a.G;
-                valid = token < a.tok && token < it.tokens;
-                last = valid ? first_last + token : -1;
-            }
+            valid = token < it.tokens;
+            last = valid ? first_last + token : -1;
             // the row's reference: numerators are 2^(s sl2 - m), at most 2^8.  Rows that do not exist need none.
             float m = valid ? -INFINITY : 0.f, l = 0.f;
             // keys that the row does not see get -infinity
@@ -715,18 +714,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 arrive_warp(&ms->p_ready);
             }
             if (!ok) break;
-            // ---- O / l, or the partial.  The next item's first PV overwrites O only after this thread's next P,
-            // which comes after these reads.
-            if (!(ok = warp_wait(&ms->o_done, (n - 1) & 1, s_abort))) break;
-            tc_fence_after();
+            // ---- O / l, or the partial: all that does not need O first, while the last PV runs
             if (!(ok = sum4(l, l))) break;
-            const int token = r / a.G, head = r - token * a.G, h = it.h;
+            const int h = it.h, q_row = it.q_row;
             const bool whole = it.whole;
-            const int64_t row = (int64_t)(it.q_row + token) * a.H_q + h * a.G + head;
-            const int64_t prow = ((int64_t)blockIdx.x * 2 + (t0 == 0)) * BM + r;
             arrive_warp(&ms->item_empty[n_item % NI]);
+            const int64_t row = ((int64_t)q_row * a.H_q + h * a.G) + row_off;
+            const int64_t prow = ((int64_t)blockIdx.x * 2 + (t0 == 0)) * BM + r;
             const bool none = l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
+            // the next item's first PV overwrites O only after this thread's next P, which comes after the reads below
+            if (!(ok = warp_wait(&ms->o_done, (n - 1) & 1, s_abort))) break;
+            tc_fence_after();
             // A row's columns lie in one lane, so a store of them by all lanes would touch 32 lines: the warp turns its rows
             // by RS bytes each in a patch of its own in the item's Q buffer (its last S is complete), and stores eight (D =
             // 64: sixteen) rows' pieces at a time.
