@@ -571,6 +571,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             all = fmaxf(__low2float(mx), __high2float(mx));
             return k;
         };
+        // The same of any four values, all their bits, in three exchanges.
+        auto maximum4_exact = [&](float v, float &all) -> bool {
+            const uint32_t u = __float_as_uint(v);
+            uint32_t b[4] = {0u, 0u, 0u, 0u};
+            bool k = true;
+#pragma unroll 1
+            for (int i = 0; i < 3; ++i) {   // bits 31 to 17, 16 to 2, 1 and 0
+                uint32_t w0, w1;
+                post(i == 0 ? u >> 16 : i == 1 ? u >> 1 : u << 14);
+                k = receive(w0, w1) && k;
+                const uint32_t w[4] = {w0 & 0xFFFEu, w0 >> 16 & 0xFFFEu, w1 & 0xFFFEu, w1 >> 16 & 0xFFFEu};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] |= i == 0 ? w[j] << 16 : i == 1 ? w[j] << 1 : w[j] >> 14;
+            }
+            all = fmaxf(fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1])), fmaxf(__uint_as_float(b[2]), __uint_as_float(b[3])));
+            return k;
+        };
         // The sum of four float32, in the groups' order, in two exchanges: all but the last two bits of each.
         auto sum4 = [&](float v, float &all) -> bool {
             const uint32_t u = __float_as_uint(v);
@@ -583,7 +600,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             all = ((join(h0, l0) + join(h0 >> 16, l0 >> 16)) + join(h1, l1)) + join(h1 >> 16, l1 >> 16);
             return k;
         };
-        constexpr float LOWEST = -60000.f, HIGHEST = 60000.f;   // at or below: no key seen; at or above: more to come
+        constexpr float LOWEST = -60000.f, HIGHEST = 60000.f;   // what maximum4 tells apart lies between
         for (uint32_t n_item = 0; ok; ++n_item) {
             // the item stays in its slot until the block is done
             if (!warp_wait(&ms->item_full[n_item % NI], (n_item / NI) & 1, s_abort)) break;
@@ -659,17 +676,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!valid) mx = -INFINITY;   // rows that do not exist hold anything
                 float up;
                 if (!(ok = maximum4(mx * sl2 - m_sub, up))) break;
-                const bool seen = up > LOWEST;
-                if (__builtin_expect(__any_sync(0xffffffffu, fresh ? seen : up > RESCALE_LOG2), 0)) {
-                    // the reference rises, or is set; where the maximum was too large to be told, again
-                    float sum = (fresh ? seen : up > RESCALE_LOG2) ? up : 0.f;
-                    while (!__all_sync(0xffffffffu, up < HIGHEST)) {
-                        if (!(ok = maximum4(mx * sl2 - m_sub - sum, up))) break;
-                        sum += fmaxf(up, 0.f);
+                if (__builtin_expect(__any_sync(0xffffffffu, fresh || up > RESCALE_LOG2), 0)) {
+                    // the reference rises, or is set
+                    const bool told = up < HIGHEST && (!fresh || up > LOWEST);
+                    if (!__all_sync(0xffffffffu, told)) {
+                        float exact;
+                        if (!(ok = maximum4_exact(mx * sl2 - m_sub, exact))) break;
+                        if (!told) up = exact;
                     }
-                    if (!ok) break;
-                    const float alpha = fresh ? 1.f : ex2(-sum);
-                    if (!fresh || seen) m = m_sub + sum;
+                    if (fresh ? up > -INFINITY : up > RESCALE_LOG2) m = m_sub + up;   // a fresh row that sees nothing stays fresh
+                    const float alpha = fresh ? 1.f : ex2(m_sub - m);
                     l *= alpha;
                     if (t > t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         // O is at rest once PV(n - 1) is complete
@@ -777,7 +793,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         flush(reinterpret_cast<uint8_t *>(a.part_o), valid ? (prow * D + EC * grp + c + j) * 4 : -1);
                     }
                 }
-                if (valid && grp == 0) a.part_ml[prow] = make_float2(m, l);
+                if (valid && grp == 0) a.part_ml[prow] = make_float2(isnan(l) ? l : m, l);   // the join passes over parts with m = -infinity
             }
             tc_fence_before();
             fence_proxy_async_smem();

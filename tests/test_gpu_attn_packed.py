@@ -204,3 +204,37 @@ def test_a_serving_run(kvc, cache_type, layout, dtype):
             o, _, b, _ = attend64(q[i:i + 1], K, V, i32([have[i]]), v_step=2.0 ** -11)
             check(out[i], o[0], b[0], "step %d seq %d" % (step, i))
     assert kvc.kvc_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,sign,size", [("bf16", -1, 100), ("bf16", 1, 100), ("f16", -1, 200), ("f16", 1, 200)])
+def test_scores_far_from_zero(kvc, dtype, sign, size):
+    # all scores of a row lie near sign * size^2 * sqrt(128) (113,000 or 450,000) and differ by a few units
+    n, t = 700, TYPES[dtype]
+    q = torch.full((n, 4, 128), float(size), device="cuda").to(t)
+    k = torch.full((n, 2, 128), float(sign * size), device="cuda").to(t)
+    k[:, :, 0] += (inputs((n, 2), torch.float32, 2) * 0.25 * size).to(t)
+    v = inputs((n, 2, 128), t, 3)
+    run(kvc, q, k, v, [n], [n])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan"), 3e38])
+def test_calls_with_infinities_end(kvc, bad):
+    # a key of infinities, of NaN or of the largest numbers: the rows that see it hold anything, the others what they would
+    n = [300, 700, 130]
+    q, k, v = (inputs((sum(n), h, 128), torch.bfloat16, s) for h, s in ((10, 1), (2, 2), (2, 3)))
+    clean = kvc.attn_packed(q, k, v, starts(n))
+    k[700] = bad
+    q[800, :5] = bad
+    out = kvc.attn_packed(q, k, v, starts(n))
+    assert kvc.kvc_device_status() == 0
+    assert torch.equal(out[:700], clean[:700]) and torch.equal(out[1000:], clean[1000:])
+
+
+def test_a_row_of_nan_is_nan(kvc):
+    # whole or cut: the long prompt's blocks are shared among the CTAs
+    for n in (40, 9000):
+        q, k, v = (inputs((n, h, 128), torch.bfloat16, s) for h, s in ((4, 1), (1, 2), (1, 3)))
+        q[n - 1, 2] = float("nan")
+        out = kvc.attn_packed(q, k, v, starts([n]))
+        bad = torch.isnan(out)
+        assert bad[n - 1, 2].all() and int(bad.sum()) == 128
