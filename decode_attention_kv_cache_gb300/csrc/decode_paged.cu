@@ -510,8 +510,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float e[4];
+                        // a reference of -infinity (no score above it yet): the numerators are zero, or NaN where a score is
+                        const float ref[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0], m[nt][1] == -INFINITY ? 0.f : m[nt][1]};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) e[i] = ex2(fmaf(s[nt][i], a.scale_log2, -m[nt][i & 1]));
+                        for (int i = 0; i < 4; ++i) e[i] = ex2(fmaf(s[nt][i], a.scale_log2, -ref[i & 1]));
                         l[nt][0] += e[0] + e[2];
                         l[nt][1] += e[1] + e[3];
                         pb[nt][0] = movmatrix_trans(pack_half2(e[0], e[1]));
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                         mx = fmaxf(mx, x[w].x);
                     }
 #pragma unroll
-                    for (int w = 0; w < CW; ++w) sum += x[w].x == -INFINITY ? 0.f : x[w].y * ex2(x[w].x - mx);
+                    for (int w = 0; w < CW; ++w) sum += x[w].x == -INFINITY ? x[w].y : x[w].y * ex2(x[w].x - mx);   // zero or NaN
                     M[nt][e] = mx;
                     L[nt][e] = sum;
                     f[nt][e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mx);
@@ -644,7 +646,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                     for (int e = 0; e < 2; ++e) {
                         const int head = nt * 8 + 2 * t4 + e;
                         if (head >= a.G) continue;
-                        if (!whole) a.part_ml[slot + head] = make_float2(M[nt][e], L[nt][e]);
+                        if (!whole)   // the join passes over parts with M = -infinity, but a NaN has to reach it
+                            a.part_ml[slot + head] = make_float2(isnan(L[nt][e]) ? INFINITY : M[nt][e], L[nt][e]);
                         else if (a.lse)
                             a.lse[(int64_t)p.seq * a.H_q + p.h * a.G + head] =
                                 L[nt][e] == 0.f ? -INFINITY : (M[nt][e] + log2f(L[nt][e])) * LN2;

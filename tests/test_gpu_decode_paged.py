@@ -188,3 +188,34 @@ def test_no_sequences(kvc):
     nobody = kvc.PageTable(torch.empty(0, 1, dtype=torch.int32, device="cuda"), i32([]), 16)
     out = kvc.decode_attn_paged(cache, 0, nobody, torch.empty(0, 4, 64, device="cuda"))
     assert out.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("cache_type", ["q8_0", "f16"])
+def test_a_query_of_nan_is_nan(kvc, cache_type):
+    # one inside a run, one cut into many; the other heads and sequences are what they would be
+    held = [40, 30000, 333]
+    cache, pages, slots = make_pool(kvc, held, 16, 2, 128, cache_type, "head_major", seed=5)
+    q = inputs((3, 10, 128), torch.bfloat16, 6)
+    clean = kvc.decode_attn_paged(cache, 0, pages, q)
+    q[0, 3, 7] = q[1, 8] = float("nan")
+    out = kvc.decode_attn_paged(cache, 0, pages, q)
+    want = clean.clone()
+    want[0, 3] = want[1, 8] = float("nan")
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out.nan_to_num(0.0), want.nan_to_num(0.0))
+
+
+def test_keys_of_infinity_have_no_weight(kvc):
+    # scores of -infinity, over whole tiles and among others, count nothing
+    held = [500, 20000]
+    cache, pages, slots = make_pool(kvc, held, 16, 1, 64, "f16", "head_major", seed=5, layers=1)
+    q = inputs((2, 4, 64), torch.float16, 6).abs() + 0.01
+    gone = [list(range(0, 200)) + [300], list(range(3000, 9000)) + [19999]]
+    at = [s for sl, g in zip(slots, gone) for s in (sl[j] for j in g)]
+    cache.codes(0)[:, 0, torch.tensor(at, device="cuda")] = -float("inf")
+    kept = [[s for j, s in enumerate(sl) if j not in set(g)] for sl, g in zip(slots, gone)]
+    lse = torch.full((2, 4), 5.0, device="cuda")
+    out = kvc.decode_attn_paged(cache, 0, pages, q, lse=lse)
+    for i, (o, l, b, lb) in enumerate(expect(cache, 0, kept, q)):
+        check(out[i], o, b, "seq %d" % i)
+        check_lse(lse[i], l, lb, "seq %d" % i)
