@@ -3,9 +3,17 @@
 // Sequence s has nq query rows and nk keys; row i sees the keys j <= i + nk - nq:
 //   out[i][h] = sum_j softmax_j(q[i][h] . k[j][h/G] / sqrt(D)) v[j][h/G].
 // Both products are contractions of the inputs' own type (bf16 or fp16) with float32 accumulators in tensor
-// memory; the softmax runs in one pass over the keys with the row's running maximum and sum in float32.  What
-// bounds it is the tensor cores' rate for long prompts, and for short ones the chain load - product - softmax -
-// product - store of each block.
+// memory; the softmax runs in one pass over the keys with the row's running maximum and sum in float32; its
+// numerators are rounded to the inputs' type for the second product.  What bounds long prompts is the softmax
+// warps' chain of each tile (below), and short ones the chain load - product - softmax - product - store of
+// each block.
+//
+// Measured (of the rate of a large matrix product): one prompt of 10,041 tokens, 40 query and 8 kv heads of 128, 797 us
+// (1,295 TF/s, 0.67); 48 prompts of 1 to 513 tokens 60 us; 512-token chunks over prefixes of 2,500 to 9,000, 16
+// and 4 heads of 64, 78 us (610 TF/s, 0.32).  The long prompt with parts of the work left out: neither loads, products nor
+// softmax (the barriers, tensor memory's loads and stores) 363 us, loads alone 509, products alone 590, both 640, all
+// but the products 718.  The softmax's arithmetic and the waits around it hardly overlap, since all of a CTA's softmax
+// warps are in the same phase.
 //
 // Work split.  The G query heads of a kv head see the same keys, so a block of 128 rows holds 128 / G tokens with all
 // their heads: a prompt of 25 tokens with five heads fills one block where a block for each head would leave four
@@ -17,8 +25,9 @@
 // Tensor memory (512 columns): S = Q K^T of a tile of 256 keys (256 columns), P (its softmax numerators as 16-bit pairs,
 // 128 columns) and O (D).  S and P are apart, so S of the next tile - of the next block, at a block's end - is computed
 // while the softmax of this one runs.  What a tile costs beside its arithmetic - waits, loads from tensor memory, the
-// exchange of maxima, about 1,500 cycles, in which all of a CTA's softmax warps wait alike - is why a tile has 256 keys:
-// with 128, S and P in two buffers each, 10,041 tokens took 962 us against TILE256 us.
+// exchange of maxima, about 1,500 cycles - is why a tile has 256 keys.  Two sets of eight softmax warps that take tiles
+// of 128 keys in turn, S and P in two buffers each, so that one set's waits are the other's arithmetic, took 808 us
+// for the long prompt, 63 for the short ones and 74 for the chunks.
 //
 // One CTA (20 warps):
 //   warp 0     producer: walks the CTA's run of the list, passes each block on through a ring of items and
@@ -53,8 +62,12 @@ constexpr int HN = 128;             // keys of half a tile
 constexpr int GROUPS = 4;           // softmax threads of a row
 constexpr int THREADS = 128 * (1 + GROUPS);
 constexpr int NI = 4;               // items on their way from the producer
-constexpr int BLOCK_COST = 512;     // what a block costs besides its keys, in keys
-constexpr int SNAP = 2;             // a cut fewer tiles than this from an end of a block moves there
+// What a block costs besides its keys, in keys.  With 256, 384, 512 and 1,024 the long prompt above takes 865, 839, 797 and
+// 798 us, the short ones 63.6, 60.6, 59.8 and 62.4.
+constexpr int BLOCK_COST = 512;
+// A cut fewer tiles than this from an end of a block moves there.  With 1, 2 and 4 the short prompts take 65.9, 59.8 and
+// 61.2 us, the chunks 77.4, 77.6 and 80.7.
+constexpr int SNAP = 2;
 constexpr int MAX_DYN_SMEM = 232448;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994531f;

@@ -9,9 +9,9 @@
 // one list that is cut into equal runs, one for each CTA (two per SM), wherever the boundaries fall: ragged
 // lengths, one long sequence and many short ones all fill the GPU.  Heads are outermost, so where their number
 // divides the CTAs' the CTAs of all heads pass the same tokens at the same time, which is what a layer-major
-// pool (a token's heads side by side) wants of DRAM and L2.  The lengths are read on the device.  A pair inside one run is written
-// straight to out; a pair cut by run boundaries leaves one partial (O, maximum, sum) per run in scratch - at
-// most two per CTA - and a second kernel joins them in run order.
+// pool (a token's heads side by side) wants of DRAM and L2.  The lengths are read on the device.  A pair inside one
+// run is written straight to out; a pair cut by run boundaries leaves one partial (O, maximum, sum) per run in
+// scratch - at most two per CTA - and a second kernel joins them in run order.
 //
 // One CTA: a producer warp looks up the pages and keeps a ring of tiles in flight by TMA (one box per page piece,
 // swizzled so that both products read them without bank conflicts, scales by 8-byte asynchronous copies); four
@@ -27,6 +27,11 @@
 //   - S^T leaves the first product with a lane per key and enters the second with a lane per head: one 8x8
 //     transposition for each half of the subtile.
 // Keys past the length and pages outside the pool are never loaded, or are given zero weight and zeroed values.
+//
+// Measured (40 query heads, 8 kv heads of 128; of the rate of a copy): 96 sequences of 5 to 16,384 tokens, q8_0 pool,
+// 84 us (4.8 TB/s, 0.71), f16 pool 0.91; one sequence of 58,300, q8_0, 30 us (4.2 TB/s, 0.62); eight of about 2,100,
+// f16, 19 us (3.6 TB/s, 0.54).  The last two pay about 8 us for the two launches, the list, the first loads and the
+// join; q8_0 pools are bound by the consumers' chains of loads, conversions and products.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -50,7 +55,8 @@ constexpr int THREADS = 32 * (CW + 1);
 constexpr int CTAS_PER_SM = 2;
 constexpr int SMEM_BUDGET = 115712;  // 113 KB: two CTAs per SM
 constexpr int COMBINE_THREADS = 256;
-constexpr int PIECE_COST = 2;       // what starting and ending a pair costs, in tiles
+// What starting and ending a pair costs, in tiles.  The 96 sequences above with 0, 1, 2 and 4: 90.7, 85.8, 84.0, 87.8 us.
+constexpr int PIECE_COST = 2;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994531f;
 
