@@ -6,7 +6,7 @@
 // is the pool's bytes over the HBM rate (a few operations per byte; q8_0 also has to turn each code into fp16).
 //
 // Work split.  The keys of all (kv head, sequence) pairs, in tiles of 64 and with a charge for each pair, form
-// one list that is cut into equal runs, one for each CTA (two per SM), wherever the boundaries fall: ragged
+// one list that is cut into equal runs, one for each CTA (two or three per SM), wherever the boundaries fall: ragged
 // lengths, one long sequence and many short ones all fill the GPU.  Heads are outermost, so where their number
 // divides the CTAs' the CTAs of all heads pass the same tokens at the same time, which is what a layer-major
 // pool (a token's heads side by side) wants of DRAM and L2.  The lengths are read on the device.  A pair inside one
@@ -29,9 +29,9 @@
 // Keys past the length and pages outside the pool are never loaded, or are given zero weight and zeroed values.
 //
 // Measured (40 query heads, 8 kv heads of 128; of the rate of a copy): 96 sequences of 5 to 16,384 tokens, q8_0 pool,
-// 84 us (4.8 TB/s, 0.71), f16 pool 0.91; one sequence of 58,300, q8_0, 30 us (4.2 TB/s, 0.62); eight of about 2,100,
-// f16, 19 us (3.6 TB/s, 0.54).  The last two pay about 8 us for the two launches, the list, the first loads and the
-// join; q8_0 pools are bound by the consumers' chains of loads, conversions and products.
+// 79 us (5.1 TB/s, 0.75), f16 pool 0.91; one sequence of 58,300, q8_0, 30 us (4.2 TB/s, 0.62); eight of about 2,100,
+// f16, 18.7 us (3.7 TB/s, 0.55).  The last two pay about 7 us (a sequence of 64 tokens) for the two launches, the list,
+// the first loads and the join; q8_0 pools are bound by the consumers' chains of loads, conversions and products.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -52,10 +52,13 @@ using namespace ptx;
 constexpr int KT = 64;              // keys per tile
 constexpr int CW = 4;               // consumer warps, 16 keys of a tile each
 constexpr int THREADS = 32 * (CW + 1);
-constexpr int CTAS_PER_SM = 2;
-constexpr int SMEM_BUDGET = 115712;  // 113 KB: two CTAs per SM
+// CTAs per SM: two, whose consumers keep up with the loads of an f16 pool; three for q8_0, where they do not (the 96
+// sequences above take 84 us with two).
+constexpr int ctas_per_sm(bool q8) { return q8 ? 3 : 2; }
+constexpr int smem_budget(bool q8) { return q8 ? 76800 : 115712; }   // 75 and 113 KB
 constexpr int COMBINE_THREADS = 256;
-// What starting and ending a pair costs, in tiles.  The 96 sequences above with 0, 1, 2 and 4: 90.7, 85.8, 84.0, 87.8 us.
+// What starting and ending a pair costs, in tiles.  The 96 sequences above with 0, 1, 2 and 4, and two
+// CTAs per SM: 90.7, 85.8, 84.0, 87.8 us.
 constexpr int PIECE_COST = 2;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994531f;
@@ -73,10 +76,10 @@ struct Cfg {
     static constexpr int ESZ = DT == KVC_IN_F32 ? 4 : 2;
     static constexpr int QB = 8 * NT * D * ESZ;             // the most that a group's queries take
     static constexpr int MISC = 1024;
-    static constexpr int FIT = (SMEM_BUDGET - 1024 - RED - QB - MISC) / STAGE;
+    static constexpr int FIT = (smem_budget(Q8) - 1024 - RED - QB - MISC) / STAGE;
     static constexpr int NS = FIT < 12 ? FIT : 12;
     static constexpr int OFF_RED = NS * STAGE, OFF_MISC = OFF_RED + RED, OFF_Q = OFF_MISC + MISC;
-    static constexpr int Q_ROOM = SMEM_BUDGET - 1024 - OFF_Q;
+    static constexpr int Q_ROOM = smem_budget(Q8) - 1024 - OFF_Q;
     static_assert(NS >= 2 && Q_ROOM >= QB, "shared memory plan");
 };
 constexpr int MAX_NQ = 4;           // slots for the queries of pieces to come: as many as fit
@@ -100,7 +103,7 @@ struct Args {
     float *lse;
     float *part_o;                       // [CTA][2][G][D]
     float2 *part_ml;                     // [CTA][2][G]
-    int4 *desc;                          // [CTA]: sequence, kv head, partials (0: none) of the pair this CTA begins
+    int4 *desc;                          // [join]: sequence, kv head, partials (0: none), CTA that begins the pair
     int H_q, H_kv, G, box, n_slots, n_q;
     float scale_log2;
 };
@@ -112,6 +115,12 @@ struct Piece {
 
 __device__ __forceinline__ int keys_of(const PagedView &pg, int i) {
     return min(max(__ldcg(pg.len + i), 0), pg.max_pages * pg.page_size);
+}
+// One join for each pair where there are no more pairs than CTAs, else one for each CTA: the pair that it begins and
+// others finish, if there is one.  (A join without work costs a block of each query head: one sequence of 58,300 tokens
+// takes 1.4 us less than with a join for each CTA.)
+__host__ __device__ __forceinline__ bool join_by_pair(int H_kv, int n_seq, int n_slots) {
+    return (int64_t)H_kv * n_seq <= n_slots;
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + KT - 1) / KT; }
 __device__ __forceinline__ int units_of(int keys) { return keys > 0 ? tiles_of(keys) + PIECE_COST : 0; }
@@ -194,7 +203,7 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
 }
 
 template <int D, bool Q8, int DT, int NT>
-__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
+__global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8))
     decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const PagedView pg, const Args a) {
     using C = Cfg<D, Q8, DT, NT>;
@@ -361,6 +370,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         const int kp = key_of(g);                               // my key (and kp + 8) in the first product
         const int v0 = key_of(2 * t4), v1 = key_of(2 * t4 + 1);   // my keys (and + 8) in the second
         uint32_t n = 0, nq = 0;
+        const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
         bool owner = false, ok = true;   // !ok: a wait gave up; the warp only keeps up with the others' barriers
         Piece p;
         // sequences without keys have no unit in the list
@@ -369,6 +379,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
             for (int e = threadIdx.x; e < a.H_q * D; e += 32 * CW) store_out<DT>(a.out, (int64_t)i * a.H_q * D + e, 0.f);
             if (a.lse)
                 for (int e = threadIdx.x; e < a.H_q; e += 32 * CW) a.lse[(int64_t)i * a.H_q + e] = -INFINITY;
+            if (by_pair)
+                for (int e = threadIdx.x; e < a.H_kv; e += 32 * CW) a.desc[e * pg.n_seq + i] = make_int4(0, 0, 0, 0);
         }
         while (walk.next(pg, a.H_kv, p)) {
             // the group's queries as the second operand of S^T: lane (g, t4) holds head g's eight values from
@@ -659,22 +671,23 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                                 L[nt][e] == 0.f ? -INFINITY : (M[nt][e] + log2f(L[nt][e])) * LN2;
                     }
             }
-            if (p.t0 == 0 && p.t1 < p.nt) {
+            if (p.t0 == 0 && (by_pair || !whole)) {
                 owner = true;
                 if (threadIdx.x == 0) {
                     const unsigned long long end = u1 + (p.nt - p.t1);   // the pair's last unit, plus one
                     const int last = (int)((end * runs_of(W) - 1) / W);    // the CTA whose run holds it
-                    a.desc[blockIdx.x] = make_int4(p.seq, p.h, last - (int)blockIdx.x + 1, 0);
+                    a.desc[by_pair ? p.h * pg.n_seq + p.seq : blockIdx.x] =
+                        make_int4(p.seq, p.h, whole ? 0 : last - (int)blockIdx.x + 1, blockIdx.x);
                 }
             }
         }
-        if (!owner && threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (!by_pair && !owner && threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
     __syncthreads();
     if (threadIdx.x == 0 && *s_abort) atomicExch(&g_paged_status, 1);
 }
 
-// Joins the partials of the pair that CTA blockIdx.x of the first kernel began, for one query head:
+// Joins the partials of one pair, for one query head:
 // out = sum_p w_p O_p / sum_p w_p l_p, w_p = 2^(m_p - max m), the runs in a fixed order.
 template <int D, int DT>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_paged_kernel(const Args a) {
@@ -686,7 +699,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_paged_kernel(const Ar
     const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, head = blockIdx.y;
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    // partial j lies with CTA blockIdx.x + j: its second slot for the first (the pair begins there), else the first
+    // partial j lies with CTA d.w + j: its second slot for the first (the pair begins there), else the first
     constexpr int B = 4;
     for (int j0 = grp; j0 < d.z; j0 += B * GROUPS) {
         float2 ml[B];
@@ -697,7 +710,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_paged_kernel(const Ar
             ml[b] = make_float2(-INFINITY, 0.f);
             o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (j < d.z) {
-                const int slot = ((blockIdx.x + j) * 2 + (j == 0)) * a.G + head;
+                const int slot = ((d.w + j) * 2 + (j == 0)) * a.G + head;
                 ml[b] = __ldcg(a.part_ml + slot);
                 o[b] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (int64_t)slot * D) + lane);
             }
@@ -748,19 +761,19 @@ template <int D, bool Q8, int DT, int NT>
 int launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const PagedView &pg, Args a, cudaStream_t s) {
     using C = Cfg<D, Q8, DT, NT>;
     a.n_q = min(MAX_NQ, C::Q_ROOM / (a.G * D * C::ESZ));
-    if (allow_dynamic_smem((const void *)decode_paged_kernel<D, Q8, DT, NT>, SMEM_BUDGET) != KVC_OK) return KVC_ECUDA;
+    if (allow_dynamic_smem((const void *)decode_paged_kernel<D, Q8, DT, NT>, smem_budget(Q8)) != KVC_OK) return KVC_ECUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.n_slots);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM_BUDGET;
+    cfg.dynamicSmemBytes = smem_budget(Q8);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, decode_paged_kernel<D, Q8, DT, NT>, tk, tv, pg, a) != cudaSuccess) return KVC_ECUDA;
-    cfg.gridDim = dim3(a.n_slots, a.G);
+    cfg.gridDim = dim3(join_by_pair(a.H_kv, pg.n_seq, a.n_slots) ? a.H_kv * pg.n_seq : a.n_slots, a.G);
     cfg.blockDim = dim3(COMBINE_THREADS);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, combine_paged_kernel<D, DT>, a) != cudaSuccess) return KVC_ECUDA;
@@ -781,13 +794,13 @@ int launch_d(int dtype, const CUtensorMap &tk, const CUtensorMap &tv, const Page
     }
 }
 
-int slots_of() { return CTAS_PER_SM * sm_count(); }
+int slots_of(bool q8) { return ctas_per_sm(q8) * sm_count(); }
 
 }  // namespace
 
 size_t paged_scratch_bytes(const kvc_desc &d, int, int n_head_q) {
     const size_t G = n_head_q / d.n_head_kv;
-    return (size_t)slots_of() * (2 * G * (d.head_dim + 2) * sizeof(float) + sizeof(int4));
+    return (size_t)slots_of(d.type == KVC_Q8_0) * (2 * G * (d.head_dim + 2) * sizeof(float) + sizeof(int4));
 }
 
 int launch_decode_paged(const kvc_cache &c, const kvc_pages &p, int layer, const void *q, int64_t ld_q, int dtype,
@@ -808,7 +821,7 @@ int launch_decode_paged(const kvc_cache &c, const kvc_pages &p, int layer, const
     a.H_q = n_head_q;
     a.H_kv = d.n_head_kv;
     a.G = n_head_q / d.n_head_kv;
-    a.n_slots = slots_of();
+    a.n_slots = slots_of(q8);
     a.desc = static_cast<int4 *>(scratch);
     a.part_o = reinterpret_cast<float *>(a.desc + a.n_slots);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)a.n_slots * 2 * a.G * D);
