@@ -411,14 +411,15 @@ class PageTable:
 
 
 # The calls below are made once a layer and step with a few rows, where the host's time counts: they look at each
-# attribute once and pass plain integers.
+# attribute once and pass plain integers.  A given stream is made the current one, so that what they allocate belongs
+# to it.
 
-def _on(device, stream):
-    """The raw stream to launch on: `stream`, or the current one of `device`, which has to be the current device."""
+def _on(device):
+    """The current stream of `device`, which has to be the current device."""
     index = device.index
     if torch._C._cuda_getDevice() != index:
         raise ValueError("the tensors are on %s, which is not the current device" % device)
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _packed_rows(t, what, heads, head_dim, dtype, device):
@@ -463,6 +464,9 @@ def _pool(cache, pages):
 def kv_paged_append(cache, layer, pages, row_start, k, v, stream=None):
     """Store packed rows k, v [n_rows][H_kv][D]: rows [row_start[i], row_start[i + 1]) are the last positions of
     sequence i (pages.lengths counts them), quantised or rounded as kv_cache_append does."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_paged_append(cache, layer, pages, row_start, k, v)
     dev, dtype, code = _pool(cache, pages), k.dtype, DTYPES.get(k.dtype)
     ld_k = _packed_rows(k, "k", cache.n_head_kv, cache.head_dim, dtype, dev)
     ld_v = _packed_rows(v, "v", cache.n_head_kv, cache.head_dim, dtype, dev)
@@ -470,13 +474,16 @@ def kv_paged_append(cache, layer, pages, row_start, k, v, stream=None):
     if v.shape[0] != n or code is None:
         raise ValueError("k and v must have the same rows and be f32, bf16 or f16")
     st = _lib().kv_paged_append(cache.addr, pages.addr, layer, _starts(row_start, "row_start", pages.n_seq, dev), n,
-                                k.data_ptr(), v.data_ptr(), ld_k, ld_v, code, _on(dev, stream))
+                                k.data_ptr(), v.data_ptr(), ld_k, ld_v, code, _on(dev))
     if st:
         raise KvcError(st, "kv_paged_append")
 
 
 def kv_paged_read(cache, layer, pages, row_start, n_rows, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """The values the pool holds for packed rows (as in kv_paged_append): k, v [n_rows][H_kv][D] in dtype."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_paged_read(cache, layer, pages, row_start, n_rows, dtype, k, v)
     dev, code = _pool(cache, pages), DTYPES.get(dtype)
     if code is None:
         raise ValueError("dtype must be f32, bf16 or f16")
@@ -484,7 +491,7 @@ def kv_paged_read(cache, layer, pages, row_start, n_rows, dtype=torch.bfloat16, 
     k = _output(k, "k", shape, dtype, dev)
     v = _output(v, "v", shape, dtype, dev, k)
     st = _lib().kv_paged_read(cache.addr, pages.addr, layer, _starts(row_start, "row_start", pages.n_seq, dev), n_rows,
-                              k.data_ptr(), v.data_ptr(), code, _on(dev, stream))
+                              k.data_ptr(), v.data_ptr(), code, _on(dev))
     if st:
         raise KvcError(st, "kv_paged_read")
     return k, v
@@ -501,6 +508,9 @@ def paged_scratch(cache, n_seq, n_head_q):
 def decode_attn_paged(cache, layer, pages, q, out=None, lse=None, scratch=None, stream=None):
     """Attention of one token q[i] [H_q][D] of each sequence over its pages.lengths[i] keys; returns out
     [n_seq][H_q][D] in q's type.  lse: None, or a float32 tensor [n_seq][H_q] to fill."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return decode_attn_paged(cache, layer, pages, q, out, lse, scratch)
     dev, n, dtype, shape = _pool(cache, pages), pages.n_seq, q.dtype, q.shape
     code = DTYPES.get(dtype)
     if len(shape) != 3 or shape[0] != n or code is None:
@@ -513,7 +523,7 @@ def decode_attn_paged(cache, layer, pages, q, out=None, lse=None, scratch=None, 
     if scratch is None:
         scratch = paged_scratch(cache, n, hq)
     st = _lib().decode_attn_paged(cache.addr, pages.addr, layer, q.data_ptr(), ld, code, hq, out.data_ptr(), lse,
-                                  scratch.data_ptr(), _bytes(scratch, dev), _on(dev, stream))
+                                  scratch.data_ptr(), _bytes(scratch, dev), _on(dev))
     if st:
         raise KvcError(st, "decode_attn_paged")
     return out
@@ -531,6 +541,9 @@ def attn_packed(q, k, v, q_start, k_start=None, out=None, lse=None, scratch=None
     """Causal attention of packed prompts: q [n_q][H_q][D], k and v [n_k][H_kv][D] (bf16 or f16); sequence s has
     query rows [q_start[s], q_start[s + 1]) and keys [k_start[s], k_start[s + 1]) (q_start when None), its queries
     being its last positions.  Returns out like q, contiguous.  lse: None, or a float32 [n_q][H_q] to fill."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attn_packed(q, k, v, q_start, k_start, out, lse, scratch)
     dev, dtype, qshape, kshape = q.device, q.dtype, q.shape, k.shape
     if len(qshape) != 3 or len(kshape) != 3 or dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("q, k and v must be bf16 or f16 tensors [rows][heads][D]")
@@ -550,7 +563,7 @@ def attn_packed(q, k, v, q_start, k_start=None, out=None, lse=None, scratch=None
         scratch = packed_scratch(n_q, n_seq, hq, hkv, d, dev)
     st = _lib().attn_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), ld_q, ld_k, ld_v, DTYPES[dtype], qs, ks, n_seq,
                             n_q, n_k, hq, hkv, d, out.data_ptr(), lse, scratch.data_ptr(), _bytes(scratch, dev),
-                            _on(dev, stream))
+                            _on(dev))
     if st:
         raise KvcError(st, "attn_packed")
     return out

@@ -451,8 +451,8 @@ int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_
  * never used, whatever they are.  Any number of sequences and lengths share the
  * GPU evenly: the keys of all of them are cut into equal shares.
  * Computed as decode_attn (fp16 products of q and the values, float32
- * accumulation and softmax), then rounded once to `dtype`.  head_dim 64 or 128, n_head_q /
- * n_head_kv <= 16.  Errors as kv_paged_append, KVC_ENOSPC (scratch too small). */
+ * accumulation and softmax), then rounded once to `dtype`.  out and lse overlap no
+ * input.  head_dim 64 or 128, n_head_q / n_head_kv <= 16.  Errors as kv_paged_append, KVC_ENOSPC (scratch too small). */
 int decode_attn_paged(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const void *q, int64_t ld_q,
                       int32_t dtype, int32_t n_head_q, void *out, float *lse, void *scratch, size_t scratch_bytes,
                       kvc_stream_t stream);
@@ -473,7 +473,9 @@ int kvc_packed_scratch_bytes(int32_t n_rows, int32_t n_seq, int32_t n_head_q, in
  * (`dtype`), ld_* elements between tokens; out: [n_q][n_head_q][head_dim]
  * contiguous in `dtype`; lse: null or [n_q][n_head_q] float32, the natural
  * logarithm of the sum of exponentials.  Values must be finite within a
- * sequence; what lies outside its rows is never used.  Tensor-core products in
+ * sequence, and scaled scores below 2^26 in magnitude (float32 tells greater ones
+ * apart too coarsely for an exponent); what lies outside its rows is never used.
+ * out overlaps no input.  Tensor-core products in
  * the inputs' type, float32 accumulation and softmax; the softmax numerators
  * enter the second product rounded to `dtype`.  head_dim 64 or 128, n_head_q /
  * n_head_kv <= 128.  Errors: KVC_EINVAL (null or unaligned pointers, dtype f32,

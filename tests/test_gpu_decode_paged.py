@@ -172,6 +172,26 @@ def test_two_streams_at_once(kvc):
             check(outs[i][0][j], o, b, "stream %d seq %d" % (i, j))
 
 
+def test_what_a_call_allocates_belongs_to_its_stream(kvc):
+    # the side stream is busy when memory is asked for on the current one
+    held = [9000, 200]
+    cache, pages, _ = make_pool(kvc, held, 16, 2, 128, "f16", "head_major", seed=9)
+    q = inputs((2, 10, 128), torch.bfloat16, 4)
+    x, xs = inputs((3000, 10, 128), torch.bfloat16, 5), i32([0, 3000])
+    want, want_x = kvc.decode_attn_paged(cache, 0, pages, q), kvc.attn_packed(x, x[:, :2], x[:, 2:4], xs)
+    sizes = [kvc.paged_scratch(cache, 2, 10).nbytes, kvc.packed_scratch(3000, 1, 10, 2, 128).nbytes, q.nbytes, x.nbytes]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = kvc.decode_attn_paged(cache, 0, pages, q, stream=side)
+    got_x = kvc.attn_packed(x, x[:, :2], x[:, 2:4], xs, stream=side)
+    for n in sizes:
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_x, want_x)
+
+
 def test_pool_past_32_bit_offsets(kvc):
     cache = kvc.KVCache(1, 1 << 20, 16, 128, "f16", "head_major")    # 2^31 values, 2^32 bytes
     n_pages = (1 << 20) // 64
