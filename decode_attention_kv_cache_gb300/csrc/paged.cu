@@ -7,8 +7,8 @@
 // find a row's page (row_start, len, the table, then the data).  What bounds the q8_0 append of many rows is neither:
 // the quantiser's own arithmetic, about 200 instructions for eight values.
 //
-// Measured (8 kv heads of 128, of the rate of a copy): 19,300 fp16 rows into an f16 cache 28.1 us (5.6 TB/s, 0.83);
-// 21,100 bf16 rows into a q8_0 cache 43.4 us (3.0 TB/s, 0.45; from float32 4.0 TB/s); 58,300 positions of a q8_0 cache
+// Measured (8 kv heads of 128, of the rate of a copy): 19,300 fp16 rows into an f16 cache 27.6 us (5.7 TB/s, 0.85);
+// 21,100 bf16 rows into a q8_0 cache 42.1 us (3.1 TB/s, 0.46; from float32 4.5 TB/s); 58,300 positions of a q8_0 cache
 // read into bf16 56.7 us (6.5 TB/s, 0.95) and of an f16 cache 71.6 us (6.7 TB/s, 0.98); eight rows appended 2.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -21,10 +21,12 @@
 namespace kvc {
 namespace {
 
-constexpr int THREADS = 256;
+// Threads of a CTA, which waits for its look-ups as one: 256, 128 and 64 take 43.4, 42.1 and 42.6 us for the q8_0 append
+// above (54, 49 and 49 from float32), 56.6, 56.8 and 63.7 for the q8_0 read.
+constexpr int THREADS = 128;
 // Units that a thread takes where there are many.  Measured at the sizes above, with 1, 2 and 4 of them: a q8_0 append
-// with the read of its rows behind it 81, 74 and 74 us, an f16 append 28.3, 28.1 and 29.4; a read of a q8_0 cache, whose
-// one load makes two stores' worth of values, 56.7, 57.2 and 62.7; of an f16 cache 76.8, 71.6 and 71.8.
+// 48.0, 42.1 and 42.6 us, an f16 append 27.7, 27.8 and 28.6; a read of a q8_0 cache, whose one load makes two stores'
+// worth of values, 56.7, 57.2 and 62.7; of an f16 cache 76.8, 71.6 and 71.8.
 constexpr int APPEND_PASSES = 2;
 template <bool Q8>
 constexpr int READ_PASSES = Q8 ? 1 : 2;
@@ -242,7 +244,7 @@ cudaLaunchConfig_t config(int64_t n_units, int units_per_cta, cudaLaunchAttribut
 
 // Several passes only where there are enough units to keep every SM busy with several CTAs of that many: eight rows
 // take 2.0 us with one and 2.25 with two.
-bool many(int64_t n_units, int passes) { return n_units >= (int64_t)THREADS * passes * 4 * sm_count(); }
+bool many(int64_t n_units, int passes) { return n_units >= (int64_t)THREADS * passes * 8 * sm_count(); }
 
 template <int DT, bool Q8, int PASSES>
 cudaError_t append_p(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int64_t n,
