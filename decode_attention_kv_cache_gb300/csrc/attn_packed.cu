@@ -13,7 +13,8 @@
 // and 4 heads of 64, 78 us (610 TF/s, 0.32).  The long prompt with parts of the work left out: neither loads, products nor
 // softmax (the barriers, tensor memory's loads and stores) 363 us, loads alone 509, products alone 590, both 640, all
 // but the products 718.  The softmax's arithmetic and the waits around it hardly overlap, since all of a CTA's softmax
-// warps are in the same phase.
+// warps are in the same phase; and the GPU is at its power limit (1400 W; the clock falls from 2.07 to 1.75-1.95 GHz),
+// so that eight softmax warps of 128 keys each, or sixteen, or two sets of eight all take 790 to 830 us.
 //
 // Work split.  The G query heads of a kv head see the same keys, so a block of 128 rows holds 128 / G tokens with all
 // their heads: a prompt of 25 tokens with five heads fills one block where a block for each head would leave four
