@@ -23,13 +23,14 @@
 //   - the order of dimensions in the first product and of keys in both is free as long as the operands agree,
 //     so each lane loads 8 or 16 consecutive bytes of a row, and codes need no shuffles between lanes;
 //   - q8_0 codes enter the first product as the integers they are; each block's products are scaled by d in
-//     float32.  In the second product the values are fp16(d * q) and the numerators p are rounded to fp16;
+//     float32.  In the second product the values are fp16(d * q) and the numerators p are rounded to fp16, in two parts
+//     where the output is finer than bf16;
 //   - S^T leaves the first product with a lane per key and enters the second with a lane per head: one 8x8
 //     transposition for each half of the subtile.
 // Keys past the length and pages outside the pool are never loaded, or are given zero weight and zeroed values.
 //
 // Measured (40 query heads, 8 kv heads of 128; of the rate of a copy): 96 sequences of 5 to 16,384 tokens, q8_0 pool,
-// 79 us (5.1 TB/s, 0.75), f16 pool 0.91; one sequence of 58,300, q8_0, 30 us (4.2 TB/s, 0.62); eight of about 2,100,
+// 82 us (4.9 TB/s, 0.73; 79 to a bf16 output), f16 pool 0.91; one sequence of 58,300, q8_0, 30 us (4.2 TB/s, 0.62); eight of about 2,100,
 // f16, 18.7 us (3.7 TB/s, 0.55).  The last two pay about 7 us (a sequence of 64 tokens) for the two launches, the list,
 // the first loads and the join; q8_0 pools are bound by the consumers' chains of loads, conversions and products.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
@@ -65,6 +66,10 @@ constexpr float LN2 = 0.69314718055994531f;
 
 template <int D, bool Q8, int DT, int NT>
 struct Cfg {
+    // Both operands of a q8_0 pool's second product are rounded to fp16, which an fp16 or float32 output shows (the 96
+    // sequences above: 1.53 times the error of the output's own rounding): there the numerators enter in two parts, for 4%
+    // of the time (1.41 times).  A bf16 output's rounding, eight times as coarse, hides it.
+    static constexpr bool FINE = Q8 && DT != KVC_IN_BF16;
     static constexpr int NB = D / 32;                       // q8_0 blocks per row
     static constexpr int ROW = D * (Q8 ? 1 : 2);            // bytes of a row
     static constexpr int TILE = KT * ROW;                   // a K or V tile
@@ -524,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8))
                             }
                         }
                     }
-                    uint32_t pb[NT][2];
+                    uint32_t pb[NT][2], pl[NT][2];   // the numerators in fp16, and what that leaves of them
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float e[4];
@@ -534,8 +539,14 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8))
                         for (int i = 0; i < 4; ++i) e[i] = ex2(fmaf(s[nt][i], a.scale_log2, -ref[i & 1]));
                         l[nt][0] += e[0] + e[2];
                         l[nt][1] += e[1] + e[3];
-                        pb[nt][0] = movmatrix_trans(pack_half2(e[0], e[1]));
-                        pb[nt][1] = movmatrix_trans(pack_half2(e[2], e[3]));
+                        const uint32_t p0 = pack_half2(e[0], e[1]), p1 = pack_half2(e[2], e[3]);
+                        pb[nt][0] = movmatrix_trans(p0);
+                        pb[nt][1] = movmatrix_trans(p1);
+                        if constexpr (C::FINE) {
+                            const float2 f0 = __half22float2(as_half2(p0)), f1 = __half22float2(as_half2(p1));
+                            pl[nt][0] = movmatrix_trans(pack_half2(e[0] - f0.x, e[1] - f0.y));
+                            pl[nt][1] = movmatrix_trans(pack_half2(e[2] - f1.x, e[3] - f1.y));
+                        }
                     }
                     if constexpr (Q8) {
                         constexpr int NW = D / 32;   // words of one key's part: 16 (8) dimensions from D / 8 * g
@@ -565,7 +576,10 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8))
                                 A[e] = as_u32(__hmul2(as_half2(unbias(u)), e & 2 ? d23 : d01));
                             }
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_16816(o[i][nt], A, pb[nt][0], pb[nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_16816(o[i][nt], A, pb[nt][0], pb[nt][1]);
+                                if constexpr (C::FINE) mma_16816(o[i][nt], A, pl[nt][0], pl[nt][1]);
+                            }
                         }
                     } else {
                         const int key = warp * 16 + key_of(lane & 7) + 8 * (lane >> 4);
