@@ -54,9 +54,10 @@ constexpr int KT = 64;              // keys per tile
 constexpr int CW = 4;               // consumer warps, 16 keys of a tile each
 constexpr int THREADS = 32 * (CW + 1);
 // CTAs per SM: two, whose consumers keep up with the loads of an f16 pool; three for q8_0, where they do not (the 96
-// sequences above take 84 us with two).
-constexpr int ctas_per_sm(bool q8) { return q8 ? 3 : 2; }
-constexpr int smem_budget(bool q8) { return q8 ? 76800 : 115712; }   // 75 and 113 KB
+// sequences above take 84 us with two), but for groups of more than 8 query heads (NT = 2), whose accumulators three leave
+// too few registers (16 heads: 133 us with three, 125 with two; one sequence of 58,300 49 and 42).
+constexpr int ctas_per_sm(bool q8, int NT) { return q8 && NT == 1 ? 3 : 2; }
+constexpr int smem_budget(bool q8, int NT) { return ctas_per_sm(q8, NT) == 3 ? 76800 : 115712; }   // 75 and 113 KB
 constexpr int COMBINE_THREADS = 256;
 // What starting and ending a pair costs, in tiles.  The 96 sequences above with 0, 1, 2 and 4, and two
 // CTAs per SM: 90.7, 85.8, 84.0, 87.8 us.
@@ -81,10 +82,10 @@ struct Cfg {
     static constexpr int ESZ = DT == KVC_IN_F32 ? 4 : 2;
     static constexpr int QB = 8 * NT * D * ESZ;             // the most that a group's queries take
     static constexpr int MISC = 1024;
-    static constexpr int FIT = (smem_budget(Q8) - 1024 - RED - QB - MISC) / STAGE;
+    static constexpr int FIT = (smem_budget(Q8, NT) - 1024 - RED - QB - MISC) / STAGE;
     static constexpr int NS = FIT < 12 ? FIT : 12;
     static constexpr int OFF_RED = NS * STAGE, OFF_MISC = OFF_RED + RED, OFF_Q = OFF_MISC + MISC;
-    static constexpr int Q_ROOM = smem_budget(Q8) - 1024 - OFF_Q;
+    static constexpr int Q_ROOM = smem_budget(Q8, NT) - 1024 - OFF_Q;
     static_assert(NS >= 2 && Q_ROOM >= QB, "shared memory plan");
 };
 constexpr int MAX_NQ = 4;           // slots for the queries of pieces to come: as many as fit
@@ -208,7 +209,7 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
 }
 
 template <int D, bool Q8, int DT, int NT>
-__global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8))
+__global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
     decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const PagedView pg, const Args a) {
     using C = Cfg<D, Q8, DT, NT>;
@@ -775,14 +776,14 @@ template <int D, bool Q8, int DT, int NT>
 int launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const PagedView &pg, Args a, cudaStream_t s) {
     using C = Cfg<D, Q8, DT, NT>;
     a.n_q = min(MAX_NQ, C::Q_ROOM / (a.G * D * C::ESZ));
-    if (allow_dynamic_smem((const void *)decode_paged_kernel<D, Q8, DT, NT>, smem_budget(Q8)) != KVC_OK) return KVC_ECUDA;
+    if (allow_dynamic_smem((const void *)decode_paged_kernel<D, Q8, DT, NT>, smem_budget(Q8, NT)) != KVC_OK) return KVC_ECUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.n_slots);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem_budget(Q8);
+    cfg.dynamicSmemBytes = smem_budget(Q8, NT);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -808,13 +809,13 @@ int launch_d(int dtype, const CUtensorMap &tk, const CUtensorMap &tv, const Page
     }
 }
 
-int slots_of(bool q8) { return ctas_per_sm(q8) * sm_count(); }
+int slots_of(bool q8, int G) { return ctas_per_sm(q8, G <= 8 ? 1 : 2) * sm_count(); }
 
 }  // namespace
 
 size_t paged_scratch_bytes(const kvc_desc &d, int, int n_head_q) {
     const size_t G = n_head_q / d.n_head_kv;
-    return (size_t)slots_of(d.type == KVC_Q8_0) * (2 * G * (d.head_dim + 2) * sizeof(float) + sizeof(int4));
+    return (size_t)slots_of(d.type == KVC_Q8_0, (int)G) * (2 * G * (d.head_dim + 2) * sizeof(float) + sizeof(int4));
 }
 
 int launch_decode_paged(const kvc_cache &c, const kvc_pages &p, int layer, const void *q, int64_t ld_q, int dtype,
@@ -835,7 +836,7 @@ int launch_decode_paged(const kvc_cache &c, const kvc_pages &p, int layer, const
     a.H_q = n_head_q;
     a.H_kv = d.n_head_kv;
     a.G = n_head_q / d.n_head_kv;
-    a.n_slots = slots_of(q8);
+    a.n_slots = slots_of(q8, a.G);
     a.desc = static_cast<int4 *>(scratch);
     a.part_o = reinterpret_cast<float *>(a.desc + a.n_slots);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)a.n_slots * 2 * a.G * D);
