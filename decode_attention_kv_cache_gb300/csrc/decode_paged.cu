@@ -702,74 +702,98 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
     if (threadIdx.x == 0 && *s_abort) atomicExch(&g_paged_status, 1);
 }
 
-// Joins the partials of one pair, for one query head:
-// out = sum_p w_p O_p / sum_p w_p l_p, w_p = 2^(m_p - max m), the runs in a fixed order.
-template <int D, int DT>
+// Joins the partials of one pair: for each query head
+// out = sum_p w_p O_p / sum_p w_p l_p, w_p = 2^(m_p - max m), the runs in a fixed order.  D / 4 threads, a group, take a
+// row.  Where there are few pairs a CTA joins one head (blockIdx.y), its groups sharing the partials; else (MANY) a CTA
+// joins all heads, a group each where there are few partials: 96 sequences of 64 tokens take 12.2 us, 13.5 with a CTA for
+// each head, which is mostly the starting of CTAs.
+constexpr int FEW_PARTS = 8;
+template <int D, int DT, bool MANY>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_paged_kernel(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int4 d = __ldcg(a.desc + blockIdx.x);
     if (d.z == 0) return;
     constexpr int LANES = D / 4, GROUPS = COMBINE_THREADS / LANES;
-    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, head = blockIdx.y;
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    // partial j lies with CTA d.w + j: its second slot for the first (the pair begins there), else the first
-    constexpr int B = 4;
-    for (int j0 = grp; j0 < d.z; j0 += B * GROUPS) {
-        float2 ml[B];
-        float4 o[B];
+    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+    // partials first, first + step, ... of a head
+    auto join = [&](int head, int first, int step, float &m, float &l, float4 &acc) {
+        m = -INFINITY;
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        // partial j lies with CTA d.w + j: its second slot for the first (the pair begins there), else the first
+        constexpr int B = 4;
+        for (int j0 = first; j0 < d.z; j0 += B * step) {
+            float2 ml[B];
+            float4 o[B];
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const int j = j0 + b * GROUPS;
-            ml[b] = make_float2(-INFINITY, 0.f);
-            o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j < d.z) {
-                const int slot = ((d.w + j) * 2 + (j == 0)) * a.G + head;
-                ml[b] = __ldcg(a.part_ml + slot);
-                o[b] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (int64_t)slot * D) + lane);
+            for (int b = 0; b < B; ++b) {
+                const int j = j0 + b * step;
+                ml[b] = make_float2(-INFINITY, 0.f);
+                o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j < d.z) {
+                    const int slot = ((d.w + j) * 2 + (j == 0)) * a.G + head;
+                    ml[b] = __ldcg(a.part_ml + slot);
+                    o[b] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (int64_t)slot * D) + lane);
+                }
+            }
+            float mx = m;
+#pragma unroll
+            for (int b = 0; b < B; ++b) mx = fmaxf(mx, ml[b].x);
+            if (mx == -INFINITY) continue;
+            const float f = m == -INFINITY ? 0.f : ex2(m - mx);
+            m = mx;
+            l *= f; acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const float w = ml[b].x == -INFINITY ? 0.f : ex2(ml[b].x - m);
+                l = fmaf(w, ml[b].y, l);
+                acc.x = fmaf(w, o[b].x, acc.x); acc.y = fmaf(w, o[b].y, acc.y);
+                acc.z = fmaf(w, o[b].z, acc.z); acc.w = fmaf(w, o[b].w, acc.w);
             }
         }
-        float mx = m;
-#pragma unroll
-        for (int b = 0; b < B; ++b) mx = fmaxf(mx, ml[b].x);
-        if (mx == -INFINITY) continue;
-        const float f = m == -INFINITY ? 0.f : ex2(m - mx);
-        m = mx;
-        l *= f; acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const float w = ml[b].x == -INFINITY ? 0.f : ex2(ml[b].x - m);
-            l = fmaf(w, ml[b].y, l);
-            acc.x = fmaf(w, o[b].x, acc.x); acc.y = fmaf(w, o[b].y, acc.y);
-            acc.z = fmaf(w, o[b].z, acc.z); acc.w = fmaf(w, o[b].w, acc.w);
+    };
+    auto store = [&](int head, float M, float L, const float4 &acc) {
+        const int64_t row = (int64_t)d.x * a.H_q + d.y * a.G + head;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        store_out<DT>(a.out, row * D + 4 * lane, acc.x * inv);
+        store_out<DT>(a.out, row * D + 4 * lane + 1, acc.y * inv);
+        store_out<DT>(a.out, row * D + 4 * lane + 2, acc.z * inv);
+        store_out<DT>(a.out, row * D + 4 * lane + 3, acc.w * inv);
+        if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+    };
+    float m, l;
+    float4 acc;
+    if (MANY && d.z <= FEW_PARTS) {
+        for (int head = grp; head < a.G; head += GROUPS) {
+            join(head, 0, 1, m, l, acc);
+            store(head, m, l, acc);
         }
+        return;
     }
     __shared__ float sm_m[GROUPS], sm_l[GROUPS];
     __shared__ float4 sm_o[GROUPS][LANES];
-    if (lane == 0) { sm_m[grp] = m; sm_l[grp] = l; }
-    sm_o[grp][lane] = acc;
-    __syncthreads();
-    if (grp != 0) return;
-    float M = -INFINITY, L = 0.f;
+    for (int head = MANY ? 0 : blockIdx.y, end = MANY ? a.G : head + 1; head < end; ++head) {
+        join(head, grp, GROUPS, m, l, acc);
+        if (MANY) __syncthreads();   // the groups' results of the head before have been read
+        if (lane == 0) { sm_m[grp] = m; sm_l[grp] = l; }
+        sm_o[grp][lane] = acc;
+        __syncthreads();
+        if (grp != 0) continue;
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i) M = fmaxf(M, sm_m[i]);
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < GROUPS; ++i) M = fmaxf(M, sm_m[i]);
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
-        const float w = sm_m[i] == -INFINITY ? 0.f : ex2(sm_m[i] - M);
-        const float4 o = sm_o[i][lane];
-        L = fmaf(w, sm_l[i], L);
-        acc.x = fmaf(w, o.x, acc.x); acc.y = fmaf(w, o.y, acc.y);
-        acc.z = fmaf(w, o.z, acc.z); acc.w = fmaf(w, o.w, acc.w);
+        for (int i = 0; i < GROUPS; ++i) {
+            const float w = sm_m[i] == -INFINITY ? 0.f : ex2(sm_m[i] - M);
+            const float4 o = sm_o[i][lane];
+            L = fmaf(w, sm_l[i], L);
+            acc.x = fmaf(w, o.x, acc.x); acc.y = fmaf(w, o.y, acc.y);
+            acc.z = fmaf(w, o.z, acc.z); acc.w = fmaf(w, o.w, acc.w);
+        }
+        store(head, M, L, acc);
     }
-    const int64_t row = (int64_t)d.x * a.H_q + d.y * a.G + head;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    store_out<DT>(a.out, row * D + 4 * lane, acc.x * inv);
-    store_out<DT>(a.out, row * D + 4 * lane + 1, acc.y * inv);
-    store_out<DT>(a.out, row * D + 4 * lane + 2, acc.z * inv);
-    store_out<DT>(a.out, row * D + 4 * lane + 3, acc.w * inv);
-    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
 }
 
 template <int D, bool Q8, int DT, int NT>
@@ -788,10 +812,12 @@ int launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const PagedView &pg, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, decode_paged_kernel<D, Q8, DT, NT>, tk, tv, pg, a) != cudaSuccess) return KVC_ECUDA;
-    cfg.gridDim = dim3(join_by_pair(a.H_kv, pg.n_seq, a.n_slots) ? a.H_kv * pg.n_seq : a.n_slots, a.G);
+    const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
+    cfg.gridDim = by_pair ? dim3(a.H_kv * pg.n_seq, a.G) : dim3(a.n_slots);
     cfg.blockDim = dim3(COMBINE_THREADS);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, combine_paged_kernel<D, DT>, a) != cudaSuccess) return KVC_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, by_pair ? combine_paged_kernel<D, DT, false> : combine_paged_kernel<D, DT, true>, a) != cudaSuccess)
+        return KVC_ECUDA;
     return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ECUDA;
 }
 
