@@ -30,9 +30,10 @@
 // Keys past the length and pages outside the pool are never loaded, or are given zero weight and zeroed values.
 //
 // Measured (40 query heads, 8 kv heads of 128; of the rate of a copy): 96 sequences of 5 to 16,384 tokens, q8_0 pool,
-// 82 us (4.9 TB/s, 0.73; 79 to a bf16 output), f16 pool 0.93; one sequence of 58,300, q8_0, 30 us (4.2 TB/s, 0.62); eight of about 2,100,
-// f16, 18.7 us (3.7 TB/s, 0.55).  The last two pay about 7 us (a sequence of 64 tokens) for the two launches, the list,
-// the first loads and the join; q8_0 pools are bound by the consumers' chains of loads, conversions and products.
+// 82 us (4.9 TB/s, 0.73; 79 to a bf16 output), f16 pool 0.93; one sequence of 58,300, q8_0, 30 us (4.2 TB/s,
+// 0.62); eight of about 2,100, f16, 18.7 us (3.7 TB/s, 0.55).  The last two pay about 7 us (a sequence of 64 tokens)
+// for the two launches, the list, the first loads and the join; q8_0 pools are bound by the consumers' chains of
+// loads, conversions and products.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
