@@ -576,7 +576,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             return __all_sync(0xffffffffu, here);
         };
         // The maximum of four values, as fp16 without the last bit: the values are exponents relative to the row's reference,
-        // which may be any number not far from their maximum.  -infinity travels as the lowest number.
+        // which may be any number not far from their maximum.  -infinity travels as the lowest number.  Up to 1,024 an
+        // fp16 step is 1/2, so that the rounding (half a step) and the flag in place of the last bit (one) miss a value by
+        // 3/4 at most; from 16,384 on it would be 24, more than the range of fp16 numerators allows.
         auto maximum4 = [&](float v, float &all) -> bool {
             uint32_t w0, w1;
             post(__half_as_ushort(__float2half_rn(fminf(fmaxf(v, -65000.f), 65000.f))));
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             all = ((join(h0, l0) + join(h0 >> 16, l0 >> 16)) + join(h1, l1)) + join(h1 >> 16, l1 >> 16);
             return k;
         };
-        constexpr float LOWEST = -60000.f, HIGHEST = 60000.f;   // what maximum4 tells apart lies between
+        constexpr float FAR = 1024.f;   // a reference is set from what maximum4 tells only between -FAR and FAR
         for (uint32_t n_item = 0; ok; ++n_item) {
             // the item stays in its slot until the block is done
             if (!warp_wait(&ms->item_full[n_item % NI], (n_item / NI) & 1, s_abort)) break;
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!(ok = maximum4(mx * sl2 - m_sub, up))) break;
                 if (__builtin_expect(__any_sync(0xffffffffu, fresh || up > RESCALE_LOG2), 0)) {
                     // the reference rises, or is set
-                    const bool told = up < HIGHEST && (!fresh || up > LOWEST);
+                    const bool told = up < FAR && (!fresh || up > -FAR);
                     if (!__all_sync(0xffffffffu, told)) {
                         float exact;
                         if (!(ok = maximum4_exact(mx * sl2 - m_sub, exact))) break;
