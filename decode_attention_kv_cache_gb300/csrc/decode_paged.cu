@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
                 const int box_slot = __shfl_sync(0xffffffffu, slot, 4 * i + ((lane * per_box) & 3));
                 const bool load = lane < boxes && box_slot >= 0;
                 const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+                __syncwarp();   // the counts before the arrival that publishes them (shuffles and ballots order no memory)
                 if (lane == 0) mbar_arrive_expect_tx(&ms->full[st], loads * 2 * a.box * C::ROW);
                 __syncwarp();
                 if (load) {
