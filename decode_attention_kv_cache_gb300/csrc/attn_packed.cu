@@ -39,8 +39,8 @@
 //              allocates tensor memory;
 //   warps 4-19  softmax, four threads for each row, 64 keys of each tile each, 32 of either half.  They exchange their
 //              maxima through shared memory, but go on with the reference that the row has: it is raised, and O rescaled,
-//              only where a score passes it by more than 2^8.  Where a sequence ends inside a piece of V these warps
-//              also set the rows behind it to zero.
+//              only where a score passes it by more than 2^8 (fp16: 2^15, a raised reference lying 2^7 below the maximum).
+//              Where a sequence ends inside a piece of V these warps also set the rows behind it to zero.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -70,7 +70,13 @@ constexpr int BLOCK_COST = 512;
 // 61.2 us, the chunks 77.4, 77.6 and 80.7.
 constexpr int SNAP = 2;
 constexpr int MAX_DYN_SMEM = 232448;
-constexpr float RESCALE_LOG2 = 8.0f;
+// A row's reference lies this far below its greatest score: with fp16 numerators 2^7, so that numerators (2^15 at most before
+// the reference is raised) are held down to 2^-31 of the greatest.  With the reference at the score itself those below 2^-25
+// vanished from O, but not from the sum.  bf16 has the range.
+template <bool BF16>
+constexpr float SHIFT_LOG2 = BF16 ? 0.0f : 7.0f;
+template <bool BF16>
+constexpr float RESCALE_LOG2 = SHIFT_LOG2<BF16> + 8.0f;
 constexpr float LN2 = 0.69314718055994531f;
 constexpr uint32_t TMEM_COLS = 512;
 
@@ -627,7 +633,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool valid;
             valid = token < it.tokens;
             last = valid ? first_last + token : -1;
-            // the row's reference: numerators are 2^(s sl2 - m), at most 2^8.  Rows that do not exist need none.
+            // the row's reference: numerators are 2^(s sl2 - m), at most 2^8 (fp16: 2^15).  Rows that do not exist need none.
             float m = valid ? -INFINITY : 0.f, l = 0.f;
             // keys that the row does not see get -infinity
             auto mask = [&](uint32_t (&s)[32], int key0) {
@@ -692,7 +698,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!valid) mx = -INFINITY;   // rows that do not exist hold anything
                 float up;
                 if (!(ok = maximum4(mx * sl2 - m_sub, up))) break;
-                if (__builtin_expect(__any_sync(0xffffffffu, fresh || up > RESCALE_LOG2), 0)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, fresh || up > RESCALE_LOG2<BF16>), 0)) {
                     // the reference rises, or is set
                     const bool told = up < FAR && (!fresh || up > -FAR);
                     if (!__all_sync(0xffffffffu, told)) {
@@ -700,7 +706,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (!(ok = maximum4_exact(mx * sl2 - m_sub, exact))) break;
                         if (!told) up = exact;
                     }
-                    if (fresh ? up > -INFINITY : up > RESCALE_LOG2) m = m_sub + up;   // a fresh row that sees nothing stays fresh
+                    // a fresh row that sees nothing stays fresh
+                    if (fresh ? up > -INFINITY : up > RESCALE_LOG2<BF16>) m = m_sub + (up - SHIFT_LOG2<BF16>);
                     const float alpha = fresh ? 1.f : ex2(m_sub - m);
                     l *= alpha;
                     if (t > t0 && __any_sync(0xffffffffu, alpha != 1.f)) {

@@ -16,8 +16,8 @@
 // One CTA: a producer warp looks up the pages and keeps a ring of tiles in flight by TMA (one box per page piece,
 // swizzled so that both products read them without bank conflicts, scales by 8-byte asynchronous copies); four
 // consumer warps take 16 keys of each tile, one subtile each, which always lies within one page.  A warp keeps its own
-// running maximum (raised only when a score passes it by 2^8, so that the accumulators are seldom rescaled) and
-// sum, and the four are joined when a pair ends.  Both products run on warp-level matrix instructions with
+// reference, 2^7 below the running maximum (raised only when a score passes that by 2^8, so that the accumulators are seldom
+// rescaled), and sum, and the four are joined when a pair ends.  Both products run on warp-level matrix instructions with
 // the keys (S^T = K Q^T) and the value dimensions (O^T = V^T P^T) as the 16-row side, so that a group of up
 // to 8 query heads wastes nothing but padding columns:
 //   - the order of dimensions in the first product and of keys in both is free as long as the operands agree,
@@ -63,7 +63,10 @@ constexpr int COMBINE_THREADS = 256;
 // What starting and ending a pair costs, in tiles.  The 96 sequences above with 0, 1, 2 and 4, and two
 // CTAs per SM: 90.7, 85.8, 84.0, 87.8 us.
 constexpr int PIECE_COST = 2;
-constexpr float RESCALE_LOG2 = 8.0f;
+// A row's reference lies SHIFT_LOG2 below its greatest score, so that the numerators are 2^7 there (2^15 at most before the
+// reference is raised) and fp16 holds them down to 2^-31 of it.  With the reference at the score itself those below 2^-25
+// vanished from O, but not from the sum: long contexts lost them.
+constexpr float SHIFT_LOG2 = 7.0f, RESCALE_LOG2 = SHIFT_LOG2 + 8.0f;
 constexpr float LN2 = 0.69314718055994531f;
 
 template <int D, bool Q8, int DT, int NT>
@@ -95,7 +98,7 @@ constexpr int MAX_NQ = 4;           // slots for the queries of pieces to come: 
 struct Misc {
     uint64_t full[12], empty[12], q_full[MAX_NQ], q_empty[MAX_NQ];
     int count[12][CW];                   // keys of each subtile that exist
-    float2 ml[CW][16];                   // running maximum and sum of each warp and head
+    float2 ml[CW][16];                   // reference and sum of each warp and head
     unsigned long long warp_units[CW + 1], total;
     int first_seq, rest, abort;
 };
@@ -521,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                                const float m_new = fmaxf(m[nt][e], x * a.scale_log2);
+                                const float m_new = fmaxf(m[nt][e], x * a.scale_log2 - SHIFT_LOG2);
                                 f[e] = m[nt][e] == m_new ? 1.f : ex2(m[nt][e] - m_new);
                                 m[nt][e] = m_new;
                                 l[nt][e] *= f[e];

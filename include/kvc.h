@@ -451,7 +451,9 @@ int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_
  * never used, whatever they are.  Any number of sequences and lengths share the
  * GPU evenly: the keys of all of them are cut into equal shares.
  * Computed as decode_attn (fp16 products of q and the values, float32
- * accumulation and softmax), then rounded once to `dtype`.  out and lse overlap no
+ * accumulation and softmax; |q| up to 65504), then rounded once to `dtype`.
+ * Softmax numerators enter the second product as fp16 and count down to 2^-31
+ * of the greatest.  out and lse overlap no
  * input.  head_dim 64 or 128, n_head_q / n_head_kv <= 16.  Errors as kv_paged_append, KVC_ENOSPC (scratch too small). */
 int decode_attn_paged(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const void *q, int64_t ld_q,
                       int32_t dtype, int32_t n_head_q, void *out, float *lse, void *scratch, size_t scratch_bytes,
@@ -477,7 +479,7 @@ int kvc_packed_scratch_bytes(int32_t n_rows, int32_t n_seq, int32_t n_head_q, in
  * apart too coarsely for an exponent); what lies outside its rows is never used.
  * out overlaps no input.  Tensor-core products in
  * the inputs' type, float32 accumulation and softmax; the softmax numerators
- * enter the second product rounded to `dtype`.  head_dim 64 or 128, n_head_q /
+ * enter the second product rounded to `dtype` (f16: down to 2^-31 of the greatest).  head_dim 64 or 128, n_head_q /
  * n_head_kv <= 128.  Errors: KVC_EINVAL (null or unaligned pointers, dtype f32,
  * shapes, ld), KVC_ENOSPC (scratch too small). */
 int attn_packed(const void *q, const void *k, const void *v, int64_t ld_q, int64_t ld_k, int64_t ld_v, int32_t dtype,
