@@ -396,18 +396,36 @@ class PageTable:
     """The pages of n_seq sequences in a pool (a KVCache whose positions are cut into pages).
 
     table: int32 [n_seq][max_pages], lengths: int32 [n_seq], contiguous tensors on the pool's device.  They are
-    read when a kernel runs, so both may be updated in place between calls (and between replays of a graph).
-    An entry outside the pool, such as -1, is a hole.
+    read when a kernel runs, so both may be updated in place between calls (and between replays of a graph, which
+    reads the tensors that it was captured with).  Either may also be replaced by assignment: the next call reads the
+    new tensor, which has to fit the other one.  An entry outside the pool, such as -1, is a hole.
     """
 
     def __init__(self, table, lengths, page_size):
+        self._check(table, lengths, table.shape[:1], table.device)
+        page_size = int(page_size)
+        c = kvc_pages(table.data_ptr(), lengths.data_ptr(), table.shape[0], table.shape[1], page_size)
+        self.__dict__.update(table=table, lengths=lengths, page_size=page_size, n_seq=table.shape[0],
+                             device=table.device, c=c, addr=ctypes.addressof(c))
+
+    @staticmethod
+    def _check(table, lengths, n_seq, device):
         _need(table, "table", torch.int32); _need(lengths, "lengths", torch.int32)
-        if table.dim() != 2 or lengths.shape != table.shape[:1] or lengths.device != table.device:
+        if (table.dim() != 2 or table.shape[:1] != n_seq or lengths.shape != n_seq or table.device != device or
+                lengths.device != device):
             raise ValueError("table must be [n_seq][max_pages] and lengths [n_seq], on one device")
-        self.table, self.lengths, self.page_size = table, lengths, int(page_size)
-        self.n_seq, self.device = table.shape[0], table.device
-        self.c = kvc_pages(table.data_ptr(), lengths.data_ptr(), table.shape[0], table.shape[1], self.page_size)
-        self.addr = ctypes.addressof(self.c)
+
+    # c holds the tensors' addresses: an assignment that left it alone would have the next call read freed memory
+    def __setattr__(self, name, value):
+        if name == "table":
+            self._check(value, self.lengths, (self.n_seq,), self.device)
+            self.c.table, self.c.max_pages = value.data_ptr(), value.shape[1]
+        elif name == "lengths":
+            self._check(self.table, value, (self.n_seq,), self.device)
+            self.c.len = value.data_ptr()
+        elif name in self.__dict__:
+            raise AttributeError("%s of a PageTable cannot be changed" % name)
+        self.__dict__[name] = value
 
 
 # The calls below are made once a layer and step with a few rows, where the host's time counts: they look at each
