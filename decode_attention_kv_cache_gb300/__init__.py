@@ -597,10 +597,10 @@ def kvc_device_status():
     return s.value
 
 
-TEST_PREFILL, TEST_DECODE = 0, 1
+TEST_PREFILL, TEST_DECODE, TEST_PAGED, TEST_PACKED = 0, 1, 2, 3
 
 
 def arm_test_wait_timeout(which, limit_ns):
-    """Test hook: the next launch of the prefill (TEST_PREFILL) or head_dim-128 decode (TEST_DECODE)
-    tensor-core kernel waits on a barrier nothing arrives at, gives up after limit_ns and unwinds."""
+    """Test hook: the next launch of the prefill (TEST_PREFILL), head_dim-128 decode (TEST_DECODE), paged decode
+    (TEST_PAGED) or packed (TEST_PACKED) kernel waits on a barrier nothing arrives at, gives up after limit_ns and unwinds."""
     _check(_lib().kvc_test_arm_wait_timeout(which, limit_ns), "kvc_test_arm_wait_timeout")

@@ -18,7 +18,7 @@ using namespace kvc;
 
 namespace kvc {
 namespace {
-std::atomic<uint64_t> g_test_stall[2];   // per kernel kind: wait limit of the armed stall, 0 = none
+std::atomic<uint64_t> g_test_stall[4];   // per kernel kind: wait limit of the armed stall, 0 = none
 }  // namespace
 void arm_test_stall(int which, uint64_t limit_ns) { g_test_stall[which].store(limit_ns); }
 uint64_t take_test_stall(int which) { return g_test_stall[which].exchange(0); }
@@ -466,7 +466,7 @@ int kvc_device_status(int32_t *status) {
 }
 
 int kvc_test_arm_wait_timeout(int32_t which, uint64_t limit_ns) {
-    if (which != KVC_TEST_PREFILL && which != KVC_TEST_DECODE) return KVC_EINVAL;
+    if (which < KVC_TEST_PREFILL || which > KVC_TEST_PACKED) return KVC_EINVAL;
     arm_test_stall(which, limit_ns);
     return KVC_OK;
 }

@@ -106,11 +106,11 @@ struct Item {
 __device__ __forceinline__ int halves(int seen, int t) { return seen - t * BN > HN ? 2 : 1; }
 
 struct Misc {
-    uint64_t q_full[2], q_empty[2], s_full, s_free, p_ready, o_done, k_full[6], k_empty[6], v_full[6], v_empty[6], item_full[NI], item_empty[NI], drain[2];
+    uint64_t q_full[2], q_empty[2], s_full, s_free, p_ready, o_done, k_full[6], k_empty[6], v_full[6], v_empty[6], item_full[NI], item_empty[NI], drain[2], stall;
     Item items[NI];
     unsigned long long warp_units[THREADS / 32], total, rest;
     int first_seq, abort;
-    uint32_t tmem;
+    uint32_t tmem, k_pieces, v_pieces, q_tiles;   // the last three: what the producer has asked for in all
 };
 static_assert(sizeof(Misc) <= 1024, "small area");
 
@@ -124,6 +124,7 @@ struct Args {
     float2 *part_ml;          // [CTA][2][128]
     int4 *desc;               // [CTA]: the block that this CTA begins and others finish (see combine)
     float scale_log2;
+    uint64_t stall_ns;        // test hook: > 0 makes the thread that issues the products with V wait for what never comes
 };
 
 // ---- the list --------------------------------------------------------------------------------------------
@@ -274,6 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         mbar_init(&ms->drain[0], 1);
         mbar_init(&ms->drain[1], 1);
+        mbar_init(&ms->stall, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -467,13 +469,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             it = nx;
         }
         if (!owner_first && lane == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-        if (*s_abort) {   // a wait gave up: let the copies in flight land before the CTA exits
-            volatile int never = 0;
-            for (uint32_t e = n_k > (uint32_t)C::KS ? n_k - C::KS : 0; e < n_k; ++e)
-                mbar_wait(&ms->k_full[e % C::KS], (e / C::KS) & 1, &never, 200000000ull);
-            for (uint32_t e = n_v > (uint32_t)C::VS ? n_v - C::VS : 0; e < n_v; ++e)
-                mbar_wait(&ms->v_full[e % C::VS], (e / C::VS) & 1, &never, 200000000ull);
-            for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(&ms->q_full[i & 1], (i >> 1) & 1, &never, 200000000ull);
+        if (lane == 0) {
+            ms->k_pieces = n_k;
+            ms->v_pieces = n_v;
+            ms->q_tiles = nq;
         }
     } else if (warp == 1 || warp == 2) {
         // ------------------------------------------------------------------ MMA issuers
@@ -518,6 +517,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 } else {
+                    if (a.stall_ns != 0) {   // gives up with S MMAs and copies in flight
+                        mbar_wait(&ms->stall, 0, s_abort, a.stall_ns);
+                        break;
+                    }
                     for (int t = t0; ok && t < t1; ++t, ++n) {
                         const int e = halves(seen, t);
 #pragma unroll 1
@@ -536,11 +539,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-            }
-            if (*s_abort) {   // let the MMAs in flight finish before tensor memory is freed
-                volatile int never = 0;
-                umma_commit(&ms->drain[warp - 1]);
-                mbar_wait(&ms->drain[warp - 1], 0, &never, 200000000ull);
             }
         }
         __syncwarp();
@@ -825,7 +823,26 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && *s_abort) atomicExch(&g_packed_status, 1);
+    if (*s_abort) {   // a wait gave up, whoever's: what is in flight ends before tensor memory is freed and the CTA exits
+        volatile int never = 0;
+        if (threadIdx.x == 0) atomicExch(&g_packed_status, 1);
+        if (warp == 0) {
+            const uint32_t n_k = ms->k_pieces, n_v = ms->v_pieces, nq = ms->q_tiles;
+            for (uint32_t e = n_k > (uint32_t)C::KS ? n_k - C::KS : 0; e < n_k; ++e)
+                mbar_wait(&ms->k_full[e % C::KS], (e / C::KS) & 1, &never, 200000000ull);
+            for (uint32_t e = n_v > (uint32_t)C::VS ? n_v - C::VS : 0; e < n_v; ++e)
+                mbar_wait(&ms->v_full[e % C::VS], (e / C::VS) & 1, &never, 200000000ull);
+            for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(&ms->q_full[i & 1], (i >> 1) & 1, &never, 200000000ull);
+        } else if (warp <= 2 && lane == 0) {
+            umma_commit(&ms->drain[warp - 1]);
+            mbar_wait(&ms->drain[warp - 1], 0, &never, 200000000ull);
+        } else if (warp >= 4) {
+            tmem_st_wait();
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
@@ -913,6 +930,7 @@ int launch_packed(const PackedArgs &p, void *scratch, cudaStream_t s) {
     a.part_o = reinterpret_cast<float *>(a.desc + ctas);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)ctas * 2 * BM * p.D);
     a.scale_log2 = 1.4426950408889634f / sqrtf((float)p.D);
+    a.stall_ns = take_test_stall(KVC_TEST_PACKED);
     const bool bf = p.dtype == KVC_IN_BF16;
     const CUtensorMapDataType dt = bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap tq, tk, tv;

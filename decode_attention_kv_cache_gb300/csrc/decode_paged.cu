@@ -96,10 +96,11 @@ constexpr int MAX_NQ = 4;           // slots for the queries of pieces to come: 
 
 // what the small area behind the ring holds
 struct Misc {
-    uint64_t full[12], empty[12], q_full[MAX_NQ], q_empty[MAX_NQ];
-    int count[12][CW];                   // keys of each subtile that exist
+    uint64_t full[12], empty[12], q_full[MAX_NQ], q_empty[MAX_NQ], stall;
+    int16_t count[12][CW];               // keys of each subtile that exist
     float2 ml[CW][16];                   // reference and sum of each warp and head
     unsigned long long warp_units[CW + 1], total;
+    uint32_t tiles, queries;             // what the producer has asked for in all
     int first_seq, rest, abort;
 };
 static_assert(sizeof(Misc) <= 1024, "small area");
@@ -116,6 +117,7 @@ struct Args {
     int4 *desc;                          // [join]: sequence, kv head, partials (0: none), CTA that begins the pair
     int H_q, H_kv, G, box, n_slots, n_q;
     float scale_log2;
+    uint64_t stall_ns;                   // test hook: > 0 makes the first consumer warp wait for what never comes
 };
 
 // A pair's keys, or the part of them that falls into one CTA's run.
@@ -172,8 +174,9 @@ __device__ __forceinline__ unsigned long long run_start(unsigned long long W, un
 }
 
 // A wait of a whole warp, with one answer for all its lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                          uint64_t limit_ns = 2000000000ull) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
 }
 
 template <int DT>
@@ -233,6 +236,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
             mbar_init(&ms->q_full[s], 1);
             mbar_init(&ms->q_empty[s], CW);
         }
+        mbar_init(&ms->stall, 1);
         fence_mbar_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
                 const int st = n % C::NS;
                 if (n >= (uint32_t)C::NS && !warp_wait(&ms->empty[st], ((n / C::NS) - 1) & 1, s_abort)) { ok = false; break; }
                 uint8_t *kt = sm + st * C::STAGE, *vt = kt + C::TILE;
-                if ((lane >> 2) == i) ms->count[st][lane & 3] = count;
+                if ((lane >> 2) == i) ms->count[st][lane & 3] = (int16_t)count;
                 const int box_slot = __shfl_sync(0xffffffffu, slot, 4 * i + ((lane * per_box) & 3));
                 const bool load = lane < boxes && box_slot >= 0;
                 const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
@@ -364,16 +368,9 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
                 ++n;
             }
         }
-        if (*s_abort) {   // a wait gave up: let the copies in flight land before the CTA exits
-            volatile int never = 0;
-            for (uint32_t st = 0; st < (uint32_t)C::NS && st < n; ++st) {
-                const uint32_t last = st + ((n - 1 - st) / C::NS) * C::NS;
-                mbar_wait(&ms->full[st], (last / C::NS) & 1, &never, 200000000ull);
-            }
-            for (uint32_t qs = 0; qs < (uint32_t)a.n_q && qs < nq; ++qs) {
-                const uint32_t last = qs + ((nq - 1 - qs) / a.n_q) * a.n_q;
-                mbar_wait(&ms->q_full[qs], (last / a.n_q) & 1, &never, 200000000ull);
-            }
+        if (lane == 0) {
+            ms->tiles = n;
+            ms->queries = nq;
         }
     } else {
         // ------------------------------------------------------------------ consumers
@@ -399,6 +396,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
             const int qs = nq % a.n_q;
             const uint32_t q_at = smem_u32(sm + C::OFF_Q) + qs * a.G * D * C::ESZ;
             ok = ok && warp_wait(&ms->q_full[qs], (nq / a.n_q) & 1, s_abort);
+            if (a.stall_ns != 0 && ok && warp == 0) ok = warp_wait(&ms->stall, 0, s_abort, a.stall_ns);
             uint32_t qf[D / 16][NT][2];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
@@ -704,7 +702,17 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
         if (!by_pair && !owner && threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
     __syncthreads();
-    if (threadIdx.x == 0 && *s_abort) atomicExch(&g_paged_status, 1);
+    if (*s_abort) {   // a wait gave up, whoever's: let the copies in flight land before the CTA exits
+        if (threadIdx.x == 0) atomicExch(&g_paged_status, 1);
+        if (warp == CW) {
+            volatile int never = 0;
+            const uint32_t n = ms->tiles, nq = ms->queries, n_q = a.n_q;
+            for (uint32_t e = n > (uint32_t)C::NS ? n - C::NS : 0; e < n; ++e)
+                mbar_wait(&ms->full[e % C::NS], (e / C::NS) & 1, &never, 200000000ull);
+            for (uint32_t e = nq > n_q ? nq - n_q : 0; e < nq; ++e)
+                mbar_wait(&ms->q_full[e % n_q], (e / n_q) & 1, &never, 200000000ull);
+        }
+    }
 }
 
 // Joins the partials of one pair: for each query head
@@ -872,6 +880,7 @@ int launch_decode_paged(const kvc_cache &c, const kvc_pages &p, int layer, const
     a.part_o = reinterpret_cast<float *>(a.desc + a.n_slots);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)a.n_slots * 2 * a.G * D);
     a.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+    a.stall_ns = take_test_stall(KVC_TEST_PAGED);
     // a TMA box covers the part of a tile that lies in one page
     a.box = p.page_size % 64 == 0 ? 64 : p.page_size % 32 == 0 ? 32 : 16;
     const CUtensorMapDataType dt = q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;

@@ -103,7 +103,7 @@ size_t packed_scratch_bytes(int n_rows, int n_seq, int n_head_q, int n_head_kv, 
 int launch_packed(const PackedArgs &a, void *scratch, cudaStream_t s);
 
 // Test hook of the failure path: the wait limit (ns) of a stall armed for the next launch of a kernel
-// kind (KVC_TEST_PREFILL / KVC_TEST_DECODE), 0 when none; take_ consumes it.
+// kind (KVC_TEST_PREFILL, KVC_TEST_DECODE, KVC_TEST_PAGED or KVC_TEST_PACKED), 0 when none; take_ consumes it.
 void arm_test_stall(int which, uint64_t limit_ns);
 uint64_t take_test_stall(int which);
 

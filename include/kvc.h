@@ -502,10 +502,12 @@ int kvc_device_status(int32_t *status);
 
 /* Test hook for the failure path.  Arms one bounded wait that nothing will
  * satisfy in the next launch of the chosen tensor-core kernel on any device:
- * which = KVC_TEST_PREFILL (the prefill attention pass, head_dim 64 or 128) or
- * KVC_TEST_DECODE (the decode split pass for head_dim 128).  In that launch the
+ * which = KVC_TEST_PREFILL (the prefill attention pass, head_dim 64 or 128),
+ * KVC_TEST_DECODE (the decode split pass for head_dim 128), KVC_TEST_PAGED
+ * (decode_attn_paged) or KVC_TEST_PACKED (attn_packed).  In that launch the
  * thread that issues the MMAs waits on a barrier nothing arrives at, in place
- * of its first wait for a softmax tile; after limit_ns the wait gives up, as
+ * of its first wait for a softmax tile (decode_attn_paged: a consumer warp, in
+ * front of its first tile); after limit_ns the wait gives up, as
  * any bounded wait does, and every CTA unwinds: the TMA copies and MMAs in
  * flight are let finish, tensor memory is freed, the kernel returns and
  * kvc_device_status reports KVC_EDEVICE.  limit_ns = 0 disarms.  One launch
@@ -513,6 +515,8 @@ int kvc_device_status(int32_t *status);
  * can show a wait that gives up leaves a usable context. */
 #define KVC_TEST_PREFILL 0
 #define KVC_TEST_DECODE 1
+#define KVC_TEST_PAGED 2
+#define KVC_TEST_PACKED 3
 int kvc_test_arm_wait_timeout(int32_t which, uint64_t limit_ns);
 
 #ifdef __cplusplus
