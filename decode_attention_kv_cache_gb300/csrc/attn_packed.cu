@@ -245,8 +245,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-    if (sm + C::USED > smem_raw + C::ALLOC) {  // the tiles need 1024-byte alignment
-        if (threadIdx.x == 0) atomicExch(&g_packed_status, 2);
+    if (sm + C::USED > smem_raw + C::ALLOC) {  // the tiles need 1024-byte alignment: nothing is computed, nothing joined
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // who waits for this kernel waits for those before it too
+        if (threadIdx.x == 0) {
+            a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+            atomicExch(&g_packed_status, 2);
+        }
         return;
     }
     Misc *ms = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
