@@ -138,8 +138,9 @@ __device__ __forceinline__ Seq make_seq(const Args &a, int q0, int q1, int k0, i
     s.q0 = q0;
     s.nq = q0 < 0 || q0 >= a.n_q || q1 <= q0 ? 0 : q1 - q0;
     k0 = max(k0, 0);
-    s.k0 = k0;
-    s.nk = max(min(k1, a.n_k) - k0, 0);
+    k1 = min(k1, a.n_k);
+    s.nk = k1 > k0 ? k1 - k0 : 0;   // (a difference of any two numbers could pass 32 bits)
+    s.k0 = s.nk ? k0 : 0;
     return s;
 }
 __device__ __forceinline__ Seq load_seq(const Args &a, int i) {
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int last;       // the last key that this row sees
             bool valid;
             valid = token < it.tokens;
-            last = valid ? first_last + token : -1;
+            last = valid ? max(first_last + token, -1) : -1;
             // the row's reference: numerators are 2^(s sl2 - m), at most 2^8 (fp16: 2^15).  Rows that do not exist need none.
             float m = valid ? -INFINITY : 0.f, l = 0.f;
             // keys that the row does not see get -infinity

@@ -470,7 +470,10 @@ int kvc_packed_scratch_bytes(int32_t n_rows, int32_t n_seq, int32_t n_head_q, in
  * array); the queries are its last positions, so with nq rows and nk keys row i
  * sees the keys j <= i + nk - nq:
  *   out[i][h] = sum_j softmax_j(q[i][h] . k[j][h/G] / sqrt(head_dim)) v[j][h/G].
- * A row that sees no key (nk < nq) gives out 0 and lse -infinity.  q: [n_q]
+ * A row that sees no key (nk < nq) gives out 0 and lse -infinity.  Starts cannot
+ * be checked on the host: keys before row 0 or at n_k and past it do not exist, rows
+ * past n_q are not computed (but count in nq), and a sequence has no keys, or no
+ * rows, where its starts decrease.  q: [n_q]
  * [n_head_q][head_dim], k and v: [n_k][n_head_kv][head_dim], all bf16 or all f16
  * (`dtype`), ld_* elements between tokens; out: [n_q][n_head_q][head_dim]
  * contiguous in `dtype`; lse: null or [n_q][n_head_q] float32, the natural
