@@ -66,6 +66,18 @@ __device__ __forceinline__ void load_inputs8(const void *base, int64_t idx, floa
     widen8<DT>(load_raw8<DT>(base, idx), x);
 }
 
+// The codes of a block whose d is 2^-128 or less, so that 1 / d would be infinite, and so coarse that x / d may pass 127.
+// Not inlined: its divisions would cost the ordinary blocks' code registers.
+static __device__ __noinline__ void q8_0_coarse32(const float *x, float d, uint32_t *packed) {
+#pragma unroll 1
+    for (int w = 0; w < 8; ++w) {
+        packed[w] = 0u;
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b)
+            packed[w] |= ((uint32_t)max(min((int)roundf(__fdiv_rn(x[4 * w + b], d)), 127), -127) & 0xFFu) << (8 * b);
+    }
+}
+
 // Quantise x[0..31]: the 32 codes packed four to a word (byte i of word w is code 4 w + i) and the
 // fp16 bits of the scale.
 __device__ __forceinline__ uint16_t q8_0_quantize32(const float (&x)[32], uint32_t (&packed)[8]) {
@@ -80,7 +92,15 @@ __device__ __forceinline__ uint16_t q8_0_quantize32(const float (&x)[32], uint32
 #pragma unroll
     for (int w = 0; w < 8; ++w) packed[w] = 0u;
     // codes are zero when amax/127 is zero (x/d undefined); |x * r| <= 127 (to an ulp) otherwise
-    if (d > 0.f && amax <= 3.402823466e38f) {
+    if (__builtin_expect(d > 0.f && d <= 0x1p-128f, 0)) {
+        float z[32];
+        uint32_t w8[8];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = x[i];
+        q8_0_coarse32(z, d, w8);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) packed[w] = w8[w];
+    } else if (d > 0.f && amax <= 3.402823466e38f) {
         const float r = __frcp_rn(d);
         const uint64_t r2 = ptx::f2_pack(r, r), mz = ptx::f2_pack(-0.f, -0.f), M2 = ptx::f2_pack(12582912.f, 12582912.f),
                        nM2 = ptx::f2_pack(-12582912.f, -12582912.f), n1 = ptx::f2_pack(-1.f, -1.f);
