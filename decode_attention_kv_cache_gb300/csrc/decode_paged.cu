@@ -54,14 +54,18 @@ using namespace ptx;
 constexpr int KT = 64;              // keys per tile
 constexpr int CW = 4;               // consumer warps, 16 keys of a tile each
 constexpr int THREADS = 32 * (CW + 1);
-// CTAs per SM: two, whose consumers keep up with the loads of an f16 pool; three for q8_0, where they do not (the 96
-// sequences above take 84 us with two), but for groups of more than 8 query heads (NT = 2), whose accumulators three leave
-// too few registers (16 heads: 133 us with three, 125 with two; one sequence of 58,300 49 and 42).
+// CTAs per SM: two, whose consumers keep up with the loads of an f16 pool; three for q8_0, where they do not, but for groups
+// of more than 8 query heads (NT = 2), whose accumulators three leave too few registers.  With three and two, in us (bf16, 8
+// kv heads, back to back): up to 8 heads to a group, D = 128 the 96 sequences above 82 and 84, one of 58,300 31.9 and 32.2, 96
+// of 700 42.9 and 38.6; D = 64 69 and 68, 21.8 and 25.1.  16 heads, D = 128 147 and 130, 50.6 and 45.5; D = 64 69 and 73: there
+// two are 6% slower.
 constexpr int ctas_per_sm(bool q8, int NT) { return q8 && NT == 1 ? 3 : 2; }
 constexpr int smem_budget(bool q8, int NT) { return ctas_per_sm(q8, NT) == 3 ? 76800 : 115712; }   // 75 and 113 KB
 constexpr int COMBINE_THREADS = 256;
-// What starting and ending a pair costs, in tiles.  The 96 sequences above with 0, 1, 2 and 4, and two
-// CTAs per SM: 90.7, 85.8, 84.0, 87.8 us.
+// What starting and ending a pair costs, in tiles.  With 0, 1, 2 and 4, in us: the 96 sequences above 94, 91, 83 and 91, in 16
+// heads to a group 144, 137, 130 and 117, with D = 64 65, 58, 69 and 73, f16 126, 122, 122 and 122; 170 sequences of 10 to 3,000,
+// 2 kv heads 25, 20, 19 and 21; one of 58,300 31.4, 31.5, 31.9 and 31.9.  (The cuts' places, and with them which CTAs pass the
+// same tokens together, move with it.)
 constexpr int PIECE_COST = 2;
 // A row's reference lies SHIFT_LOG2 below its greatest score, so that the numerators are 2^7 there (2^15 at most before the
 // reference is raised) and fp16 holds them down to 2^-31 of it.  With the reference at the score itself those below 2^-25
@@ -92,7 +96,7 @@ struct Cfg {
     static constexpr int Q_ROOM = smem_budget(Q8, NT) - 1024 - OFF_Q;
     static_assert(NS >= 2 && Q_ROOM >= QB, "shared memory plan");
 };
-constexpr int MAX_NQ = 4;           // slots for the queries of pieces to come: as many as fit
+constexpr int MAX_NQ = 4;           // slots for the queries of pieces to come: as many as fit (1, 2 and 4 take the same time)
 
 // what the small area behind the ring holds
 struct Misc {
@@ -719,7 +723,8 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
 // out = sum_p w_p O_p / sum_p w_p l_p, w_p = 2^(m_p - max m), the runs in a fixed order.  D / 4 threads, a group, take a
 // row.  Where there are few pairs a CTA joins one head (blockIdx.y), its groups sharing the partials; else (MANY) a CTA
 // joins all heads, a group each where there are few partials: 96 sequences of 64 tokens take 12.2 us, 13.5 with a CTA for
-// each head, which is mostly the starting of CTAs.
+// each head, which is mostly the starting of CTAs.  The 96 sequences of 5 to 16,384 with a group for a head up to 0, 2, 8 and 32
+// partials: 86, 86, 83 and 83 us, in 16 heads to a group 141, 140, 130 and 130.
 constexpr int FEW_PARTS = 8;
 template <int D, int DT, bool MANY>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_paged_kernel(const Args a) {

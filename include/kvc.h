@@ -393,7 +393,7 @@ int kv_cache_truncate(const kvc_cache *cache, int32_t n_tokens, kvc_stream_t str
  * is stored there, it reads as zero and attention gives it no weight (so the
  * pages a sequence has let go may be marked -1) - and a negative length is zero.
  * Several sequences may share pages that are only read.  Rows that one call
- * stores to the same pool position race: the position then holds either.
+ * stores to the same pool position race: the position then holds parts of each.
  *
  * Packed rows.  Rows of several sequences lie one after another in one tensor;
  * row_start (device, [n_seq + 1], not decreasing) gives each sequence's rows,
@@ -402,7 +402,7 @@ int kv_cache_truncate(const kvc_cache *cache, int32_t n_tokens, kvc_stream_t str
  * len[i] rows for a whole prompt, a chunk's rows otherwise.  A sequence may have
  * none.  Rows that would fall before position 0 belong to no position.  Rows
  * outside [row_start[0], row_start[n_seq]), such as padding behind the last
- * sequence, are neither read nor written.  n_rows is the number of rows of the
+ * sequence, are neither used nor written.  n_rows is the number of rows of the
  * tensors; no row at or past it is touched, whatever row_start says.
  * Packed tensors are token-major with contiguous heads; ld_* is the distance
  * between tokens in elements (at least heads * head_dim, a multiple of 16 bytes),
@@ -420,7 +420,7 @@ typedef struct {
 
 /* Store packed rows of k and v ([n_rows][n_head_kv][head_dim] in `dtype`) at
  * their positions in `layer` of the pool, quantised or rounded exactly as
- * kv_cache_append does (the same bytes).  Rows of holes are dropped.
+ * kv_cache_append does (the same bytes, of finite values).  Rows of holes are dropped.
  * Errors: KVC_EINVAL (null or unaligned pointers, dtype, ld, page_size, n_seq or
  * max_pages out of bounds), KVC_ERANGE (layer). */
 int kv_paged_append(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const int32_t *row_start,
