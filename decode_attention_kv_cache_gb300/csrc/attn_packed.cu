@@ -97,7 +97,7 @@ struct Item {
     int q_row, tokens;        // first query row and number of tokens of the block
     int h;                    // kv head; -1: no more items
     int k_row, keys;          // the sequence's first key and their number
-    int last;                 // the last key that the block's first token sees (may be negative)
+    int last;                 // the last key that the block's first token sees (may be negative, -BM at least)
     int seen;                 // keys that the block sees, at least 1
     int t0, t1;               // key tiles
     int whole;                // the run holds the whole block
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 it.k_row = s.k0;
                 it.keys = s.nk;
                 it.seen = seen;
-                it.last = block * a.tok + s.nk - s.nq;
+                it.last = max(block * a.tok + s.nk - s.nq, -BM);   // (no token of the block then sees anything either way)
                 it.whole = it.t0 == 0 && it.t1 == tiles;
                 left -= x1 - x;
                 if (it.t0 == 0 && it.t1 > 0 && it.t1 < tiles) {
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int last;       // the last key that this row sees
             bool valid;
             valid = token < it.tokens;
-            last = valid ? max(first_last + token, -1) : -1;
+            last = valid ? first_last + token : -1;
             // the row's reference: numerators are 2^(s sl2 - m), at most 2^8 (fp16: 2^15).  Rows that do not exist need none.
             float m = valid ? -INFINITY : 0.f, l = 0.f;
             // keys that the row does not see get -infinity
