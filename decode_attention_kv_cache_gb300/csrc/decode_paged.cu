@@ -62,6 +62,7 @@ constexpr int THREADS = 32 * (CW + 1);
 constexpr int ctas_per_sm(bool q8, int NT) { return q8 && NT == 1 ? 3 : 2; }
 constexpr int smem_budget(bool q8, int NT) { return ctas_per_sm(q8, NT) == 3 ? 76800 : 115712; }   // 75 and 113 KB
 constexpr int COMBINE_THREADS = 256;
+constexpr int MAX_NS = 10;          // tiles of the longest ring (16 heads of 64, q8_0)
 // What starting and ending a pair costs, in tiles.  With 0, 1, 2 and 4, in us: the 96 sequences above 94, 91, 83 and 91, in 16
 // heads to a group 144, 137, 130 and 117, with D = 64 65, 58, 69 and 73, f16 126, 122, 122 and 122; 170 sequences of 10 to 3,000,
 // 2 kv heads 25, 20, 19 and 21; one of 58,300 31.4, 31.5, 31.9 and 31.9.  (The cuts' places, and with them which CTAs pass the
@@ -91,7 +92,7 @@ struct Cfg {
     static constexpr int QB = 8 * NT * D * ESZ;             // the most that a group's queries take
     static constexpr int MISC = 1024;
     static constexpr int FIT = (smem_budget(Q8, NT) - 1024 - RED - QB - MISC) / STAGE;
-    static constexpr int NS = FIT < 12 ? FIT : 12;
+    static constexpr int NS = FIT < MAX_NS ? FIT : MAX_NS;
     static constexpr int OFF_RED = NS * STAGE, OFF_MISC = OFF_RED + RED, OFF_Q = OFF_MISC + MISC;
     static constexpr int Q_ROOM = smem_budget(Q8, NT) - 1024 - OFF_Q;
     static_assert(NS >= 2 && Q_ROOM >= QB, "shared memory plan");
@@ -100,8 +101,8 @@ constexpr int MAX_NQ = 4;           // slots for the queries of pieces to come: 
 
 // what the small area behind the ring holds
 struct Misc {
-    uint64_t full[12], empty[12], q_full[MAX_NQ], q_empty[MAX_NQ], stall;
-    int16_t count[12][CW];               // keys of each subtile that exist
+    uint64_t full[MAX_NS], empty[MAX_NS], q_full[MAX_NQ], q_empty[MAX_NQ], stall;
+    int count[MAX_NS][CW];               // keys of each subtile that exist
     float2 ml[CW][16];                   // reference and sum of each warp and head
     unsigned long long warp_units[CW + 1], total;
     uint32_t tiles, queries;             // what the producer has asked for in all
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
                 const int st = n % C::NS;
                 if (n >= (uint32_t)C::NS && !warp_wait(&ms->empty[st], ((n / C::NS) - 1) & 1, s_abort)) { ok = false; break; }
                 uint8_t *kt = sm + st * C::STAGE, *vt = kt + C::TILE;
-                if ((lane >> 2) == i) ms->count[st][lane & 3] = (int16_t)count;
+                if ((lane >> 2) == i) ms->count[st][lane & 3] = count;
                 const int box_slot = __shfl_sync(0xffffffffu, slot, 4 * i + ((lane * per_box) & 3));
                 const bool load = lane < boxes && box_slot >= 0;
                 const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
@@ -384,6 +385,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
         uint32_t n = 0, nq = 0;
         const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
         bool owner = false, ok = true;   // !ok: a wait gave up; the warp only keeps up with the others' barriers
+        if (a.stall_ns != 0 && warp == 0) ok = warp_wait(&ms->stall, 0, s_abort, a.stall_ns);
         Piece p;
         // sequences without keys have no unit in the list
         for (int i = blockIdx.x; i < pg.n_seq; i += gridDim.x) {
@@ -400,7 +402,6 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
             const int qs = nq % a.n_q;
             const uint32_t q_at = smem_u32(sm + C::OFF_Q) + qs * a.G * D * C::ESZ;
             ok = ok && warp_wait(&ms->q_full[qs], (nq / a.n_q) & 1, s_abort);
-            if (a.stall_ns != 0 && ok && warp == 0) ok = warp_wait(&ms->stall, 0, s_abort, a.stall_ns);
             uint32_t qf[D / 16][NT][2];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
