@@ -10,7 +10,7 @@
 //
 // Measured (of the rate of a large matrix product): one prompt of 10,041 tokens, 40 query and 8 kv heads of 128, 797 us
 // (1,295 TF/s, 0.67); 48 prompts of 1 to 513 tokens 60 us; 512-token chunks over prefixes of 2,500 to 9,000, 16
-// and 4 heads of 64, 78 us (610 TF/s, 0.32).  The long prompt with parts of the work left out: neither loads, products nor
+// and 4 heads of 64, 79 us (600 TF/s, 0.31).  The long prompt with parts of the work left out: neither loads, products nor
 // softmax (the barriers, tensor memory's loads and stores) 363 us, loads alone 509, products alone 590, both 640, all
 // but the products 718.  The softmax's arithmetic and the waits around it hardly overlap, since all of a CTA's softmax
 // warps are in the same phase; and the GPU is at its power limit (1400 W; the clock falls from 2.07 to 1.75-1.95 GHz),

@@ -29,11 +29,11 @@
 //     transposition for each half of the subtile.
 // Keys past the length and pages outside the pool are never loaded, or are given zero weight and zeroed values.
 //
-// Measured (40 query heads, 8 kv heads of 128; of the rate of a copy): 96 sequences of 5 to 16,384 tokens, q8_0 pool,
-// 82 us (4.9 TB/s, 0.73; 79 to a bf16 output), f16 pool 0.93; one sequence of 58,300, q8_0, 30 us (4.2 TB/s,
-// 0.62); eight of about 2,100, f16, 18.7 us (3.7 TB/s, 0.55).  The last two pay about 7 us (a sequence of 64 tokens)
-// for the two launches, the list, the first loads and the join; q8_0 pools are bound by the consumers' chains of
-// loads, conversions and products.
+// Measured (40 query heads, 8 kv heads of 128; of the rate of a copy): 96 sequences of 5 to 16,384 tokens, q8_0 pool, to an
+// fp16 output 82 us (4.9 TB/s, 0.73), to bf16 79 to 81, in 16 heads to a group 124; f16 pool 120 to 122 us (6.3 TB/s, 0.92);
+// one sequence of 58,300, q8_0, 30 us (4.2 TB/s, 0.62); eight of about 2,100, f16, 18.7 us (3.7 TB/s, 0.55).  The last two
+// pay about 7 us (a sequence of 64 tokens) for the two launches, the list, the first loads and the join; q8_0 pools are
+// bound by the consumers' chains of loads, conversions and products.
 // Every mbarrier wait is bounded (2 s); a wait that gives up sets the device status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,17 +56,17 @@ constexpr int CW = 4;               // consumer warps, 16 keys of a tile each
 constexpr int THREADS = 32 * (CW + 1);
 // CTAs per SM: two, whose consumers keep up with the loads of an f16 pool; three for q8_0, where they do not, but for groups
 // of more than 8 query heads (NT = 2), whose accumulators three leave too few registers.  With three and two, in us (bf16, 8
-// kv heads, back to back): up to 8 heads to a group, D = 128 the 96 sequences above 82 and 84, one of 58,300 31.9 and 32.2, 96
-// of 700 42.9 and 38.6; D = 64 69 and 68, 21.8 and 25.1.  16 heads, D = 128 147 and 130, 50.6 and 45.5; D = 64 69 and 73: there
-// two are 6% slower.
+// kv heads, back to back): up to 8 heads to a group, D = 128 the 96 sequences below 79 and 83, one of 58,300 31.7 and 32.2, 96
+// of 700 40.9 and 38.1; D = 64 68 and 69, 21.6 and 25.5.  16 heads, D = 128 144 and 125, 50 and 43; D = 64 70 and 73: there
+// two are 5% slower.
 constexpr int ctas_per_sm(bool q8, int NT) { return q8 && NT == 1 ? 3 : 2; }
 constexpr int smem_budget(bool q8, int NT) { return ctas_per_sm(q8, NT) == 3 ? 76800 : 115712; }   // 75 and 113 KB
 constexpr int COMBINE_THREADS = 256;
 constexpr int MAX_NS = 10;          // tiles of the longest ring (16 heads of 64, q8_0)
-// What starting and ending a pair costs, in tiles.  With 0, 1, 2 and 4, in us: the 96 sequences above 94, 91, 83 and 91, in 16
-// heads to a group 144, 137, 130 and 117, with D = 64 65, 58, 69 and 73, f16 126, 122, 122 and 122; 170 sequences of 10 to 3,000,
-// 2 kv heads 25, 20, 19 and 21; one of 58,300 31.4, 31.5, 31.9 and 31.9.  (The cuts' places, and with them which CTAs pass the
-// same tokens together, move with it.)
+// What starting and ending a pair costs, in tiles.  With 0, 1, 2 and 4, in us (q8_0, bf16): 96 sequences of 5 to 16,384 91, 85,
+// 79 and 87, in 16 heads to a group 136, 131, 125 and 112, with D = 64 61, 57, 68 and 72, f16 123, 119, 120 and 120; 170 sequences
+// of 10 to 3,000, 2 kv heads 25, 20, 19 and 21; one of 58,300 31.4, 31.4, 31.7 and 31.6.  (The cuts' places, and with them
+// which CTAs pass the same tokens together, move with it.)
 constexpr int PIECE_COST = 2;
 // A row's reference lies SHIFT_LOG2 below its greatest score, so that the numerators are 2^7 there (2^15 at most before the
 // reference is raised) and fp16 holds them down to 2^-31 of it.  With the reference at the score itself those below 2^-25
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
 // row.  Where there are few pairs a CTA joins one head (blockIdx.y), its groups sharing the partials; else (MANY) a CTA
 // joins all heads, a group each where there are few partials: 96 sequences of 64 tokens take 12.2 us, 13.5 with a CTA for
 // each head, which is mostly the starting of CTAs.  The 96 sequences of 5 to 16,384 with a group for a head up to 0, 2, 8 and 32
-// partials: 86, 86, 83 and 83 us, in 16 heads to a group 141, 140, 130 and 130.
+// partials: 82, 82, 79 and 79 us, in 16 heads to a group 136, 135, 125 and 125.
 constexpr int FEW_PARTS = 8;
 template <int D, int DT, bool MANY>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_paged_kernel(const Args a) {
