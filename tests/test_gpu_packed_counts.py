@@ -2,8 +2,9 @@
 place changes an output by a quarter or more, where the bound is the roundings of one number.
 
 V is one in the dimension that belongs to the key's piece of 128 (piece mod D) and zero elsewhere.
-  Equal weights (q = 0): out is count / keys.  All numerators are equal powers of two, so sums below 2^22 are exact and
-    what errs is 1 / l, the product (2^-24 each) and the output's rounding.
+  Equal weights (q = 0): out is count / keys.  All numerators are the same number, one that both types hold exactly but
+    for the exponential's 2^-22, so that what errs beside it is 1 / l and the product (2^-24 each), the sum l of n numbers
+    ((n / 8 + 32) 2^-23; the products' sums are whole multiples of one number and exact) and the output's rounding.
   Weights e^0 to e^3 by piece (whole-number scores in one dimension): with V >= 0 the numerators' rounding, half a step
     of the type, bounds the relative error; exponents 2^-17, sums (n / 8 + 32) 2^-23 twice, the output's rounding.
 """
@@ -32,11 +33,11 @@ def test_every_piece_counts_once(kvc, qn, kn, dtype, d, weights):
     k = torch.zeros(sum(kn), hkv, d, dtype=t, device="cuda")
     piece = torch.cat([torch.arange(n, device="cuda") // 128 for n in kn])
     v = torch.nn.functional.one_hot(piece % d, d)[:, None].expand(-1, hkv, -1).to(t).contiguous()
-    step = 0.0
+    step = 2.0 ** -21
     if weights != "equal":
         q[..., 0] = 8
         k[..., 0] = (piece % 7 % 4)[:, None].to(t)
-        step = half_step(t) + 2.0 ** -17
+        step = half_step(t) + 2.0 ** -17 + 2.0 ** -21
     out = kvc.attn_packed(q, k, v, starts(qn), starts(kn))
     a = b = 0
     for nq, nk in zip(qn, kn):
@@ -45,7 +46,7 @@ def test_every_piece_counts_once(kvc, qn, kn, dtype, d, weights):
         seen = torch.arange(nk, device="cuda")[None, :] <= (r + nk - nq)[:, None]
         p = torch.exp(s) * seen
         want = ((p @ v[b:b + nk, 0].double()) / p.sum(-1, keepdim=True))[:, None]
-        bound = want * (step + half_step(t) + 2.0 ** -21 + (2 * (nk / 8 + 32) * 2.0 ** -23 if step else 0.0))
+        bound = want * (step + half_step(t) + 2 * (nk / 8 + 32) * 2.0 ** -23)
         got = out[a:a + nq][r].double()
         assert ((got - want).abs() <= bound * 1.01 + 2.0 ** -25).all(), (nq, nk)
         a, b = a + nq, b + nk
