@@ -1,4 +1,4 @@
-"""Python binding of libkvc: attention over a device-resident q8_0/f16 KV cache on GB300.
+"""Python binding of libkvc: attention over a device-resident q8_0/f16 KV cache (pools of pages: also q4_0) on GB300.
 
 Argument marshalling only.  Every step of the path (quantise-and-append,
 chunked prefill attention, split-K decode attention, state pack/unpack) runs in
@@ -20,7 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvc.so")
 
 KVC_OK, KVC_EINVAL, KVC_ERANGE, KVC_ENOSPC, KVC_EFORMAT, KVC_ECUDA, KVC_EDEVICE = 0, -1, -2, -3, -4, -5, -6
-CACHE_TYPES = {"f16": 0, "q8_0": 1}
+CACHE_TYPES = {"f16": 0, "q8_0": 1, "q4_0": 2}
 LAYOUTS = {"head_major": 0, "layer_major": 1}
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
@@ -140,8 +140,9 @@ def cache_bytes(desc):
 class KVCache:
     """A cache whose four buffers are torch allocations on `device`.
 
-    Codes/values: k_q, v_q; scales (q8_0 only): k_s, v_s.  The buffers are
-    exposed as typed views in the layout of the descriptor.
+    Codes/values: k_q, v_q; scales (q8_0 and q4_0): k_s, v_s.  The buffers are
+    exposed as typed views in the layout of the descriptor.  "q4_0" is a type
+    of pools: the calls with a PageTable take it.
     """
 
     def __init__(self, n_layer, n_ctx, n_head_kv, head_dim, cache_type="q8_0", layout="head_major",
@@ -154,7 +155,7 @@ class KVCache:
         self._bufs = [torch.empty(max(n, 16), dtype=torch.uint8, device=self.device) for n in (kq, ks, vq, vs)]
         self._sizes = (kq, ks, vq, vs)
         self.c = kvc_cache()
-        scales = cache_type == "q8_0"
+        scales = cache_type != "f16"
         _check(_lib().kvc_cache_init(ctypes.byref(self.c), ctypes.byref(self.desc), _ptr(self._bufs[0]),
                                   _ptr(self._bufs[1]) if scales else ctypes.c_void_p(0), _ptr(self._bufs[2]),
                                   _ptr(self._bufs[3]) if scales else ctypes.c_void_p(0)), "kvc_cache_init")
@@ -166,13 +167,15 @@ class KVCache:
         return (self.n_layer, self.n_ctx, self.n_head_kv, last)
 
     def codes(self, kv):
-        """K (kv=0) or V (kv=1) codes (int8) or values (float16), in layout order."""
+        """K (kv=0) or V (kv=1) codes (int8; q4_0: uint8, two to a byte) or values (float16), in layout order."""
         b = self._bufs[2 * kv][: self._sizes[2 * kv]]
+        if self.cache_type == "q4_0":
+            return b.view(self._shape(self.head_dim // 2))
         dt = torch.int8 if self.cache_type == "q8_0" else torch.float16
         return b.view(dt).view(self._shape(self.head_dim))
 
     def scales(self, kv):
-        if self.cache_type != "q8_0":
+        if self.cache_type == "f16":
             return None
         b = self._bufs[2 * kv + 1][: self._sizes[2 * kv + 1]]
         return b.view(torch.float16).view(self._shape(self.head_dim // 32))

@@ -30,14 +30,18 @@ constexpr uint32_t STATE_MAGIC = 0x3143564Bu;  // 'K' 'V' 'C' '1' little-endian
 constexpr uint32_t STATE_VERSION = 1u;
 constexpr size_t STATE_HEADER = 32;
 
-bool desc_ok(const kvc_desc *d) {
+// any cache: what the calls on pools of pages take
+bool pool_desc_ok(const kvc_desc *d) {
     if (!d) return false;
     if (d->n_layer <= 0 || d->n_ctx <= 0 || d->n_head_kv <= 0 || d->head_dim <= 0) return false;
     if (d->head_dim % 32 != 0 || d->head_dim > 1024) return false;
-    if (d->type != KVC_F16 && d->type != KVC_Q8_0) return false;
+    if (d->type != KVC_F16 && d->type != KVC_Q8_0 && d->type != KVC_Q4_0) return false;
     if (d->layout != KVC_HEAD_MAJOR && d->layout != KVC_LAYER_MAJOR) return false;
     return true;
 }
+
+// one that every call takes: q4_0 is a type of pools
+bool desc_ok(const kvc_desc *d) { return pool_desc_ok(d) && d->type != KVC_Q4_0; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -52,13 +56,15 @@ bool on_current_device(const void *p) {
     return (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged) && at.device == dev;
 }
 
-bool cache_ok(const kvc_cache *c) {
-    if (!c || !desc_ok(&c->d)) return false;
+bool pool_ok(const kvc_cache *c) {
+    if (!c || !pool_desc_ok(&c->d)) return false;
     if (!c->k_q || !c->v_q || !aligned16(c->k_q) || !aligned16(c->v_q)) return false;
-    if (c->d.type == KVC_Q8_0 && (!c->k_s || !c->v_s || !aligned16(c->k_s) || !aligned16(c->v_s)))
+    if (has_scales(c->d.type) && (!c->k_s || !c->v_s || !aligned16(c->k_s) || !aligned16(c->v_s)))
         return false;
     return true;
 }
+
+bool cache_ok(const kvc_cache *c) { return pool_ok(c) && desc_ok(&c->d); }
 
 size_t elems(const kvc_desc &d) { return (size_t)d.n_layer * d.n_ctx * d.n_head_kv * d.head_dim; }
 
@@ -84,15 +90,10 @@ bool dtype_ok(int dtype) { return dtype == KVC_IN_F32 || dtype == KVC_IN_BF16 ||
 extern "C" {
 
 int kvc_cache_bytes(const kvc_desc *desc, size_t *k_q, size_t *k_s, size_t *v_q, size_t *v_s) {
-    if (!desc_ok(desc) || !k_q || !k_s || !v_q || !v_s) return KVC_EINVAL;
+    if (!pool_desc_ok(desc) || !k_q || !k_s || !v_q || !v_s) return KVC_EINVAL;
     const size_t n = elems(*desc);
-    if (desc->type == KVC_Q8_0) {
-        *k_q = *v_q = n;
-        *k_s = *v_s = n / 32 * 2;
-    } else {
-        *k_q = *v_q = n * 2;
-        *k_s = *v_s = 0;
-    }
+    *k_q = *v_q = (size_t)code_bytes(desc->type, (int64_t)n);
+    *k_s = *v_s = has_scales(desc->type) ? n / 32 * 2 : 0;
     return KVC_OK;
 }
 
@@ -108,14 +109,14 @@ size_t kv_state_size(const kvc_desc *desc, int32_t n_tokens) {
 }
 
 int kvc_cache_init(kvc_cache *out, const kvc_desc *desc, void *k_q, void *k_s, void *v_q, void *v_s) {
-    if (!out || !desc_ok(desc)) return KVC_EINVAL;
+    if (!out || !pool_desc_ok(desc)) return KVC_EINVAL;
     kvc_cache c;
     c.d = *desc;
     c.k_q = k_q;
-    c.k_s = desc->type == KVC_Q8_0 ? k_s : nullptr;
+    c.k_s = has_scales(desc->type) ? k_s : nullptr;
     c.v_q = v_q;
-    c.v_s = desc->type == KVC_Q8_0 ? v_s : nullptr;
-    if (!cache_ok(&c)) return KVC_EINVAL;
+    c.v_s = has_scales(desc->type) ? v_s : nullptr;
+    if (!pool_ok(&c)) return KVC_EINVAL;
     *out = c;
     return KVC_OK;
 }
@@ -349,7 +350,7 @@ int kv_state_set_heads(kvc_cache *cache, int32_t head0, const void *src, size_t 
 int kv_paged_append(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const int32_t *row_start,
                     int32_t n_rows, const void *k, const void *v, int64_t ld_k, int64_t ld_v, int32_t dtype,
                     kvc_stream_t stream) {
-    if (!cache_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype) || n_rows < 0) return KVC_EINVAL;
+    if (!pool_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype) || n_rows < 0) return KVC_EINVAL;
     if (!ld_ok(ld_k, pool->d.n_head_kv, pool->d.head_dim, dtype) ||
         !ld_ok(ld_v, pool->d.n_head_kv, pool->d.head_dim, dtype))
         return KVC_EINVAL;
@@ -361,7 +362,7 @@ int kv_paged_append(const kvc_cache *pool, const kvc_pages *pages, int32_t layer
 
 int kv_paged_read(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const int32_t *row_start,
                   int32_t n_rows, void *k, void *v, int32_t dtype, kvc_stream_t stream) {
-    if (!cache_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype) || n_rows < 0) return KVC_EINVAL;
+    if (!pool_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype) || n_rows < 0) return KVC_EINVAL;
     if (layer < 0 || layer >= pool->d.n_layer) return KVC_ERANGE;
     if (n_rows == 0 || pages->n_seq == 0) return KVC_OK;
     if (!pages->table || !pages->len || !row_start || !k || !v || !aligned16(k) || !aligned16(v)) return KVC_EINVAL;
@@ -369,7 +370,7 @@ int kv_paged_read(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, 
 }
 
 int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_q, size_t *bytes) {
-    if (!desc_ok(desc) || !bytes || n_seq < 0 || n_seq > 65535) return KVC_EINVAL;
+    if (!pool_desc_ok(desc) || !bytes || n_seq < 0 || n_seq > 65535) return KVC_EINVAL;
     if (desc->head_dim != 64 && desc->head_dim != 128) return KVC_EINVAL;
     if (n_head_q <= 0 || n_head_q % desc->n_head_kv || n_head_q / desc->n_head_kv > 16) return KVC_EINVAL;
     *bytes = paged_scratch_bytes(*desc, n_seq, n_head_q);
@@ -379,7 +380,7 @@ int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_
 int decode_attn_paged(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const void *q, int64_t ld_q,
                       int32_t dtype, int32_t n_head_q, void *out, float *lse, void *scratch, size_t scratch_bytes,
                       kvc_stream_t stream) {
-    if (!cache_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype)) return KVC_EINVAL;
+    if (!pool_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype)) return KVC_EINVAL;
     size_t need = 0;
     if (kvc_paged_scratch_bytes(&pool->d, pages->n_seq, n_head_q, &need) != KVC_OK) return KVC_EINVAL;
     if (!ld_ok(ld_q, n_head_q, pool->d.head_dim, dtype)) return KVC_EINVAL;
@@ -422,7 +423,7 @@ int attn_packed(const void *q, const void *k, const void *v, int64_t ld_q, int64
 }
 
 int kv_cache_truncate(const kvc_cache *cache, int32_t n_tokens, kvc_stream_t stream) {
-    if (!cache_ok(cache)) return KVC_EINVAL;
+    if (!pool_ok(cache)) return KVC_EINVAL;
     const kvc_desc &d = cache->d;
     if (n_tokens < 0 || n_tokens > d.n_ctx) return KVC_ERANGE;
     if (n_tokens == d.n_ctx) return KVC_OK;
@@ -436,9 +437,9 @@ int kv_cache_truncate(const kvc_cache *cache, int32_t n_tokens, kvc_stream_t str
         return cudaMemset2DAsync(static_cast<uint8_t *>(buf) + n * per_pos, T * per_pos, 0, (T - n) * per_pos, rows,
                                  s) == cudaSuccess;
     };
-    const size_t code_bytes = (size_t)d.head_dim * (d.type == KVC_Q8_0 ? 1 : 2);
-    if (!clear(cache->k_q, code_bytes) || !clear(cache->v_q, code_bytes)) return KVC_ECUDA;
-    if (d.type == KVC_Q8_0) {
+    const size_t row_bytes = (size_t)code_bytes(d.type, d.head_dim);
+    if (!clear(cache->k_q, row_bytes) || !clear(cache->v_q, row_bytes)) return KVC_ECUDA;
+    if (has_scales(d.type)) {
         const size_t scale_bytes = (size_t)(d.head_dim / 32) * 2;
         if (!clear(cache->k_s, scale_bytes) || !clear(cache->v_s, scale_bytes)) return KVC_ECUDA;
     }

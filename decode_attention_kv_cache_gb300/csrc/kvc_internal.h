@@ -30,6 +30,10 @@ inline Geom geom_of(const kvc_desc &d) {
     return g;
 }
 
+// Bytes of n consecutive values (whole blocks of 32 for the quantised types) in a code buffer.
+inline int64_t code_bytes(int type, int64_t n) { return type == KVC_F16 ? 2 * n : type == KVC_Q8_0 ? n : n / 2; }
+inline bool has_scales(int type) { return type != KVC_F16; }
+
 inline int dtype_bytes(int dtype) { return dtype == KVC_IN_F32 ? 4 : 2; }
 
 

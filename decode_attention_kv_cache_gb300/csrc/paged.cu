@@ -1,7 +1,8 @@
 // Storing packed rows on a pool's pages, and reading them back.
 //
 // append: a row's values are quantised to q8_0 (blocks of 32 along head_dim: d = fp16(amax/127), codes
-// round(x / (amax/127)); the arithmetic is quant.cuh's, so the bytes are kv_cache_append's) or rounded to
+// round(x / (amax/127)); the arithmetic is quant.cuh's, so the bytes are kv_cache_append's) or q4_0 (4-bit codes of
+// x / d, d = fp16(-m/8), m the value of greatest magnitude), or rounded to
 // fp16.  read: x = d * q in float32 (exact: 11 and 8 significant bits), rounded once to the output type.
 // Both only move bytes: what bounds them is HBM, and for a few rows the latency of the dependent loads that
 // find a row's page (row_start, len, the table, then the data).  What bounds the q8_0 append of many rows is neither:
@@ -28,8 +29,8 @@ constexpr int THREADS = 128;
 // 48.0, 42.1 and 42.6 us, an f16 append 27.7, 27.8 and 28.6; a read of a q8_0 cache, whose one load makes two stores'
 // worth of values, 56.7, 57.2 and 62.7; of an f16 cache 76.8, 71.6 and 71.8.
 constexpr int APPEND_PASSES = 2;
-template <bool Q8>
-constexpr int READ_PASSES = Q8 ? 1 : 2;
+template <int CT>
+constexpr int READ_PASSES = CT == KVC_Q8_0 ? 1 : 2;
 
 // n / d for 32-bit n by a multiplication: floor(n (2^64 / d + 1) / 2^64), where the part that is too much,
 // n / 2^64, is below the 1/d that would be needed to reach the next integer.
@@ -49,8 +50,8 @@ struct Pool {
 
 Pool pool_of(const kvc_cache &c, int layer, int values_per_unit) {
     const Geom g = geom_of(c.d);
-    const int esz = c.d.type == KVC_Q8_0 ? 1 : 2, per_head = c.d.head_dim / values_per_unit, per_row = c.d.n_head_kv * per_head;
-    const int64_t at = layer * g.c_layer * esz, sat = c.d.type == KVC_Q8_0 ? layer * g.s_layer : 0;
+    const int per_head = c.d.head_dim / values_per_unit, per_row = c.d.n_head_kv * per_head;
+    const int64_t at = code_bytes(c.d.type, layer * g.c_layer), sat = has_scales(c.d.type) ? layer * g.s_layer : 0;
     return {static_cast<uint8_t *>(c.k_q) + at, static_cast<uint8_t *>(c.v_q) + at, static_cast<uint16_t *>(c.k_s) + sat,
             static_cast<uint16_t *>(c.v_s) + sat, g.c_tok, g.c_head, g.s_tok, g.s_head, div_of(per_row),
             div_of(per_head), per_row, per_head};
@@ -98,7 +99,7 @@ __device__ __forceinline__ void store8(void *dst, const uint32_t (&w)[8]) {
 // One thread takes eight consecutive values of a row, of K and of V, PASSES times; all of its loads are in flight
 // before the first value is used, and the look-ups overlap them.  The four lanes of a q8_0 block find its amax by
 // two shuffles, so input, codes and scales are all read and written in consecutive lanes' order.
-template <int DT, bool Q8, int PASSES>
+template <int DT, int CT, int PASSES>
 __global__ void __launch_bounds__(THREADS)
     paged_append_kernel(const void *__restrict__ k, const void *__restrict__ v, int64_t ld_k, int64_t ld_v,
                         int64_t n_units, const int32_t *row_start, const PagedView pg, const Pool p) {
@@ -133,7 +134,15 @@ __global__ void __launch_bounds__(THREADS)
         for (int kv = 0; kv < 2; ++kv) {
             float x[8];
             widen8<DT>(raw[i][kv], x);
-            if constexpr (Q8) {
+            if constexpr (CT == KVC_Q4_0) {
+                uint32_t w;
+                const uint16_t scale = q4_0_quantize_quad(x, w);
+                if (slot >= 0) {
+                    *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(kv ? p.vq : p.kq) + (at >> 1)) = w;
+                    if ((c & 31) == 0)
+                        (kv ? p.vs : p.ks)[slot * p.s_tok + head * p.s_head + (c >> 5)] = scale;
+                }
+            } else if constexpr (CT == KVC_Q8_0) {
                 uint32_t w[2];
                 const uint16_t scale = q8_0_quantize_quad(x, w);
                 if (slot >= 0) {
@@ -152,14 +161,15 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
-// One thread takes the values of one 16-byte load of the pool (16 codes of one block, or 8 fp16 values), of K
+// One thread takes 16 codes of one block (a 16-byte load, 8 bytes of q4_0) or 8 fp16 values, of K
 // and of V, PASSES times, all loads in flight together.  32-byte stores where the outputs allow them.
-template <int DT, bool Q8, int PASSES, bool WIDE>
+template <int DT, int CT, int PASSES, bool WIDE>
 __global__ void __launch_bounds__(THREADS)
     paged_read_kernel(void *__restrict__ k, void *__restrict__ v, int64_t n_units, const int32_t *row_start,
                       const PagedView pg, const Pool p) {
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int N = Q8 ? 16 : 8;
+    constexpr int N = CT == KVC_F16 ? 8 : 16;
+    constexpr bool Q8 = CT == KVC_Q8_0, Q4 = CT == KVC_Q4_0;
     __shared__ int slots[THREADS * PASSES / 2 + 1];   // a row has two units or more
     const Span sp = span_of(n_units, p.units_per_row, THREADS * PASSES);
     const int64_t u0 = (int64_t)blockIdx.x * (THREADS * PASSES), left = n_units - u0;
@@ -181,9 +191,14 @@ __global__ void __launch_bounds__(THREADS)
         const int64_t sat = slot[i] * p.s_tok + head * p.s_head + (c >> 5);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-            raw[i][kv] = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(kv ? p.vq : p.kq) +
-                                                                at * (Q8 ? 1 : 2)));
-            if (Q8) d[i][kv] = __ldcg((kv ? p.vs : p.ks) + sat);
+            const uint8_t *src = static_cast<const uint8_t *>(kv ? p.vq : p.kq) + (Q4 ? at >> 1 : at * (Q8 ? 1 : 2));
+            if constexpr (Q4) {
+                const uint2 w = __ldcg(reinterpret_cast<const uint2 *>(src));
+                raw[i][kv] = make_uint4(w.x, w.y, 0u, 0u);
+            } else {
+                raw[i][kv] = __ldcg(reinterpret_cast<const uint4 *>(src));
+            }
+            if (Q8 || Q4) d[i][kv] = __ldcg((kv ? p.vs : p.ks) + sat);
         }
     }
 #pragma unroll
@@ -193,10 +208,19 @@ __global__ void __launch_bounds__(THREADS)
         for (int kv = 0; kv < 2; ++kv) {
             float x[N];
             const uint32_t w[4] = {raw[i][kv].x, raw[i][kv].y, raw[i][kv].z, raw[i][kv].w};
-            const float s = Q8 ? __half2float(__ushort_as_half(d[i][kv])) : 0.f;
+            const float s = Q8 || Q4 ? __half2float(__ushort_as_half(d[i][kv])) : 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if constexpr (Q8) {
+                if constexpr (Q4) {
+                    // a code plus 8 in the low bits of the fp16 1024 is 1032 + code: two neighbours at a time
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t u = ((w[j >> 1] >> (8 * (j & 1) + 4 * b)) & 0x000F000Fu) | 0x64006400u;
+                        const float2 f = __half22float2(__hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1032.f)));
+                        x[4 * j + 2 * b] = f.x * s;
+                        x[4 * j + 2 * b + 1] = f.y * s;
+                    }
+                } else if constexpr (Q8) {
                     // a code plus 128 in the low bits of 2^23 is the float 2^23 + 128 + code, exactly
                     const uint32_t u = w[j] ^ 0x80808080u;
 #pragma unroll
@@ -217,7 +241,7 @@ __global__ void __launch_bounds__(THREADS)
                     for (int b = 0; b < 8; ++b) o[b] = __float_as_uint(x[j + b]);
                     store8<WIDE>(dst + 4 * j, o);
                 }
-            } else if constexpr (Q8) {
+            } else if constexpr (Q8 || Q4) {
                 uint32_t o[8];
 #pragma unroll
                 for (int b = 0; b < 8; ++b) o[b] = pack2<DT>(x[2 * b], x[2 * b + 1]);
@@ -246,76 +270,75 @@ cudaLaunchConfig_t config(int64_t n_units, int units_per_cta, cudaLaunchAttribut
 // take 2.0 us with one and 2.25 with two.
 bool many(int64_t n_units, int passes) { return n_units >= (int64_t)THREADS * passes * 8 * sm_count(); }
 
-template <int DT, bool Q8, int PASSES>
+template <int DT, int CT, int PASSES>
 cudaError_t append_p(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int64_t n,
                      const void *k, const void *v, int64_t ld_k, int64_t ld_v, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = config(n, THREADS * PASSES, attr, s);
-    return cudaLaunchKernelEx(&cfg, paged_append_kernel<DT, Q8, PASSES>, k, v, ld_k, ld_v, n, row_start,
+    return cudaLaunchKernelEx(&cfg, paged_append_kernel<DT, CT, PASSES>, k, v, ld_k, ld_v, n, row_start,
                               paged_view(c, pg), pool_of(c, layer, 8));
 }
-template <int DT, bool Q8>
+template <int DT, int CT>
 cudaError_t append_t(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int n_rows,
                      const void *k, const void *v, int64_t ld_k, int64_t ld_v, cudaStream_t s) {
     const int per_row = c.d.n_head_kv * (c.d.head_dim / 8);
     const int64_t n = (int64_t)n_rows * per_row;
     return many(n, APPEND_PASSES)
-               ? append_p<DT, Q8, APPEND_PASSES>(c, pg, layer, row_start, n, k, v, ld_k, ld_v, s)
-               : append_p<DT, Q8, 1>(c, pg, layer, row_start, n, k, v, ld_k, ld_v, s);
+               ? append_p<DT, CT, APPEND_PASSES>(c, pg, layer, row_start, n, k, v, ld_k, ld_v, s)
+               : append_p<DT, CT, 1>(c, pg, layer, row_start, n, k, v, ld_k, ld_v, s);
 }
 
-template <int DT, bool Q8, int PASSES, bool WIDE>
+template <int DT, int CT, int PASSES, bool WIDE>
 cudaError_t read_p(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int64_t n,
                    void *k, void *v, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = config(n, THREADS * PASSES, attr, s);
-    return cudaLaunchKernelEx(&cfg, paged_read_kernel<DT, Q8, PASSES, WIDE>, k, v, n, row_start,
-                              paged_view(c, pg), pool_of(c, layer, Q8 ? 16 : 8));
+    return cudaLaunchKernelEx(&cfg, paged_read_kernel<DT, CT, PASSES, WIDE>, k, v, n, row_start,
+                              paged_view(c, pg), pool_of(c, layer, CT == KVC_F16 ? 8 : 16));
 }
-template <int DT, bool Q8>
+template <int DT, int CT>
 cudaError_t read_t(const kvc_cache &c, const kvc_pages &pg, int layer, const int32_t *row_start, int n_rows, void *k,
                    void *v, cudaStream_t s) {
-    const int per_row = c.d.n_head_kv * (c.d.head_dim / (Q8 ? 16 : 8));
+    const int per_row = c.d.n_head_kv * (c.d.head_dim / (CT == KVC_F16 ? 8 : 16));
     const int64_t n = (int64_t)n_rows * per_row;
     const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31) == 0;
     // 16-byte stores elsewhere: 69 us instead of 57 for the q8_0 read above
-    if (!wide) return read_p<DT, Q8, 1, false>(c, pg, layer, row_start, n, k, v, s);
-    return many(n, READ_PASSES<Q8>) ? read_p<DT, Q8, READ_PASSES<Q8>, true>(c, pg, layer, row_start, n, k, v, s)
-                                    : read_p<DT, Q8, 1, true>(c, pg, layer, row_start, n, k, v, s);
+    if (!wide) return read_p<DT, CT, 1, false>(c, pg, layer, row_start, n, k, v, s);
+    return many(n, READ_PASSES<CT>) ? read_p<DT, CT, READ_PASSES<CT>, true>(c, pg, layer, row_start, n, k, v, s)
+                                    : read_p<DT, CT, 1, true>(c, pg, layer, row_start, n, k, v, s);
 }
 
 int done(cudaError_t e) { return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? KVC_OK : KVC_ECUDA; }
 
 }  // namespace
 
+#define KVC_TYPES(DT, CALL)                                              \
+    case DT:                                                             \
+        switch (c.d.type) {                                              \
+            case KVC_F16: return done(CALL(DT, KVC_F16));                \
+            case KVC_Q8_0: return done(CALL(DT, KVC_Q8_0));              \
+            default: return done(CALL(DT, KVC_Q4_0));                    \
+        }
 int launch_paged_append(const kvc_cache &c, const kvc_pages &p, int layer, const int32_t *row_start, int n_rows,
                         const void *k, const void *v, int64_t ld_k, int64_t ld_v, int dtype, cudaStream_t s) {
-    const bool q8 = c.d.type == KVC_Q8_0;
     switch (dtype) {
-#define KVC_CASE(DT)                                                                                       \
-    case DT:                                                                                               \
-        return done(q8 ? append_t<DT, true>(c, p, layer, row_start, n_rows, k, v, ld_k, ld_v, s)            \
-                       : append_t<DT, false>(c, p, layer, row_start, n_rows, k, v, ld_k, ld_v, s));
-        KVC_CASE(KVC_IN_F32)
-        KVC_CASE(KVC_IN_BF16)
-        KVC_CASE(KVC_IN_F16)
-#undef KVC_CASE
+#define KVC_CALL(DT, CT) append_t<DT, CT>(c, p, layer, row_start, n_rows, k, v, ld_k, ld_v, s)
+        KVC_TYPES(KVC_IN_F32, KVC_CALL)
+        KVC_TYPES(KVC_IN_BF16, KVC_CALL)
+        KVC_TYPES(KVC_IN_F16, KVC_CALL)
+#undef KVC_CALL
         default: return KVC_EINVAL;
     }
 }
 
 int launch_paged_read(const kvc_cache &c, const kvc_pages &p, int layer, const int32_t *row_start, int n_rows, void *k,
                       void *v, int dtype, cudaStream_t s) {
-    const bool q8 = c.d.type == KVC_Q8_0;
     switch (dtype) {
-#define KVC_CASE(DT)                                                                        \
-    case DT:                                                                                \
-        return done(q8 ? read_t<DT, true>(c, p, layer, row_start, n_rows, k, v, s)            \
-                       : read_t<DT, false>(c, p, layer, row_start, n_rows, k, v, s));
-        KVC_CASE(KVC_IN_F32)
-        KVC_CASE(KVC_IN_BF16)
-        KVC_CASE(KVC_IN_F16)
-#undef KVC_CASE
+#define KVC_CALL(DT, CT) read_t<DT, CT>(c, p, layer, row_start, n_rows, k, v, s)
+        KVC_TYPES(KVC_IN_F32, KVC_CALL)
+        KVC_TYPES(KVC_IN_BF16, KVC_CALL)
+        KVC_TYPES(KVC_IN_F16, KVC_CALL)
+#undef KVC_CALL
         default: return KVC_EINVAL;
     }
 }

@@ -1,4 +1,4 @@
-// The q8_0 block quantiser and the input loader, shared by the append kernel and the fused decode and
+// The q8_0 and q4_0 block quantisers and the input loader, shared by the append kernel and the fused decode and
 // prefill steps so that all of them store the same bytes.
 //
 // One block is 32 values along head_dim: fp16 scale d = amax / 127, int8 codes q = round(x / d)
@@ -211,6 +211,54 @@ __device__ __forceinline__ uint16_t q8_0_quantize_quad(const float (&x)[8], uint
                                     __byte_perm(q[4 * w + 2], q[4 * w + 3], 0x0040), 0x5410);
     }
     return __half_as_ushort(__float2half_rn(d));
+}
+
+// q4_0: a block spread over four neighbouring lanes, eight values each; all four lanes take part.  This lane's word of
+// codes and the block's scale.
+//
+//   m = the block's value of greatest magnitude (of +m and -m the negative one), d = fp16(-m / 8),
+//   code = min(round(-8 x / m), 7), ties away from zero; a block of zeros has d = +0 and codes of zero.
+// The quotient is meant exactly: with a = |x|, D = |m| / 8 and k <= a / D <= k + 1 but for an error that does not
+// matter, the sign of the residue a - (k + 1/2) D, which a fused multiply-add gives exactly, decides between k and k + 1.
+// No branch: bf16 and fp16 inputs, whose quotients have few bits, meet ties in most warps.
+// A word holds eight codes, value i of them, as code + 8, in the four bits from bit 16 (i % 2) + 4 (i / 2): one AND
+// with 0x000F000F << 4 (i / 2) then gives the neighbours 2 j, 2 j + 1 as the halves of a register.
+// A non-finite block (outside the method's domain) has codes of zero under a scale of infinity or NaN.
+__device__ __forceinline__ uint16_t q4_0_quantize_quad(const float (&x)[8], uint32_t &word) {
+    uint32_t key = 0u;   // magnitude, then sign: the greatest is m, by integers, which also keeps a NaN
+#pragma unroll
+    for (int i = 0; i < 8; ++i) key = max(key, __funnelshift_l(__float_as_uint(x[i]), __float_as_uint(x[i]), 1));
+    key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
+    key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
+    const uint32_t mbits = __funnelshift_r(key, key, 1);
+    const float m = __uint_as_float(mbits), am = fabsf(m);
+    word = 0x88888888u;
+    if (am > 0.f && am <= 3.402823466e38f) {
+        const float up = am < 0x1p-100f ? 0x1p100f : 1.f;   // 1 / D and the residues stay in the normal range
+        const float D = am * up * 0.125f;
+        float r;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(D));
+        const uint64_t r2 = ptx::f2_pack(r, r), D2 = ptx::f2_pack(D, D), M2 = ptx::f2_pack(12582912.f, 12582912.f),
+                       nM2 = ptx::f2_pack(-12582912.f, -12582912.f), n1 = ptx::f2_pack(-1.f, -1.f),
+                       nh = ptx::f2_pack(-0.5f, -0.5f);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const uint64_t a = ptx::f2_pack(fabsf(x[i]) * up, fabsf(x[i + 1]) * up);
+            const uint64_t t = ptx::f2_add(ptx::f2_fma(a, r2, nh), M2);                          // k + M
+            const uint64_t c = ptx::f2_fma(ptx::f2_fma(ptx::f2_add(t, nM2), n1, nh), D2, a);     // a - (k + 1/2) D
+            float t0, t1, c0, c1;
+            ptx::f2_unpack(t, t0, t1);
+            ptx::f2_unpack(c, c0, c1);
+            // -8 x / m is negative where x and m have the same sign
+            const int s0 = (int)~(__float_as_uint(x[i]) ^ mbits) >> 31, s1 = (int)~(__float_as_uint(x[i + 1]) ^ mbits) >> 31;
+            const int q0 = __float_as_int(t0) - 0x4B400000 + 1 + (__float_as_int(c0) >> 31);
+            const int q1 = __float_as_int(t1) - 0x4B400000 + 1 + (__float_as_int(c1) >> 31);
+            // adding a signed code to the 8 of its four bits gives code + 8 there and carries nowhere
+            word += (uint32_t)min((q0 ^ s0) - s0, 7) << (2 * i);
+            word += (uint32_t)min((q1 ^ s1) - s1, 7) << (16 + 2 * i);
+        }
+    }
+    return am > 0.f || am != am ? __half_as_ushort(__float2half_rn(m * -0.125f)) : (uint16_t)0;
 }
 
 }  // namespace kvc

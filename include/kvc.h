@@ -52,7 +52,18 @@
  *             all codes and d zero for an all-zero block.  The stored value is
  *             d * q.  Codes and scales live in separate arrays.
  *   KVC_F16:  fp16(x), round to nearest even.  The scale arrays are unused.
- * Layouts (element offsets; nb = head_dim/32; codes use head_dim, scales nb):
+ *   KVC_Q4_0: a type of pools of pages: blocks of 32 as for q8_0, each with one fp16
+ *             scale d = fp16(-m/8), m the block's value of greatest magnitude (of
+ *             +m and -m the negative one), and 32 codes of four bits
+ *             q = min(round(-8 x / m), 7) in [-8, 7] (the exact quotient, ties away
+ *             from zero), all codes and d zero for an all-zero block.  The stored
+ *             value is d * q.  A block's 16 bytes are four little-endian 32-bit
+ *             words; value i of a word's eight lies, as q + 8, in the four bits from
+ *             bit 16 (i % 2) + 4 (i / 2).  The calls on pages take this type
+ *             (kv_paged_*, decode_attn_paged, qk_norm_rope_append), and
+ *             kvc_cache_bytes, kvc_cache_init and kv_cache_truncate; every other
+ *             call refuses it (KVC_EINVAL).
+ * Layouts (element offsets, two q4_0 codes to a byte; nb = head_dim/32; codes use head_dim, scales nb):
  *   KVC_HEAD_MAJOR  [n_head_kv][n_layer][n_ctx][head_dim]   (split by head)
  *   KVC_LAYER_MAJOR [n_layer][n_ctx][n_head_kv][head_dim]   (split by layer)
  *
@@ -81,7 +92,7 @@ typedef struct CUstream_st *kvc_stream_t; /* a cudaStream_t */
 #define KVC_ECUDA   -5 /* a CUDA call or launch failed */
 #define KVC_EDEVICE -6 /* a kernel gave up a bounded wait (see kvc_device_status) */
 
-typedef enum { KVC_F16 = 0, KVC_Q8_0 = 1 } kvc_cache_type;
+typedef enum { KVC_F16 = 0, KVC_Q8_0 = 1, KVC_Q4_0 = 2 } kvc_cache_type;
 typedef enum { KVC_IN_F32 = 0, KVC_IN_BF16 = 1, KVC_IN_F16 = 2 } kvc_dtype;
 typedef enum { KVC_HEAD_MAJOR = 0, KVC_LAYER_MAJOR = 1 } kvc_layout;
 
@@ -95,8 +106,8 @@ typedef struct {
     int32_t layout;  /* kvc_layout */
 } kvc_desc;
 
-/* A cache: its descriptor and four caller-owned device buffers.  For q8_0,
- * k_q/v_q hold int8 codes and k_s/v_s fp16 scales; for f16, k_q/v_q hold the
+/* A cache: its descriptor and four caller-owned device buffers.  For q8_0 (q4_0),
+ * k_q/v_q hold int8 (4-bit) codes and k_s/v_s fp16 scales; for f16, k_q/v_q hold the
  * fp16 values and k_s/v_s are NULL.  Buffers must be 16-byte aligned and at
  * least as large as kvc_cache_bytes reports.  Plain data, copied by value. */
 typedef struct {

@@ -9,6 +9,7 @@ holds none of the method's arithmetic).
 Modules:
   q8_0       block quantisation to 32-value int8 blocks with an fp16 scale, and
              the f16 cache rounding
+  q4_0       block quantisation to 32 four-bit codes with an fp16 scale, and its bytes
   attention  causal grouped-query softmax attention in float64 over the
              dequantised cache
   cache      a logical KV cache (append, chunk prefill, decode) and the byte
