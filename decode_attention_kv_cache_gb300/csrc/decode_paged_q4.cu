@@ -1,13 +1,728 @@
-// decode_attn_paged: the kernels of q4_0 pools (decode_paged.cuh), compiled beside the others.
+// decode_attn_paged over a pool of 4 bits (q4_0).
+//
+// Every code is read once and used for the G query heads of its group: 72 bytes for 128 values, and so little of them that
+// what bounds it is turning nibbles into operands.  Two things keep that short.
+//   - An fp16 number is linear in its bits as long as the exponent's are zero, and matrix products take such numbers exactly:
+//     a nibble n (code + 8) in the low byte of a half is the subnormal n 2^-24 or n 2^-20 where it lies.  An AND with
+//     0x000F000F or 0x00F000F0 makes two operands, and no subtraction or conversion is left to do for each value.  In the first
+//     product the queries of the lower nibbles are 16 times as large.  The second takes the whole bytes, n + 16 n',
+//     beside the high nibbles (one operation less), and the two sums are told apart at the end.
+//   - The 8 in each nibble is taken care of outside of the loops over values: the scores begin at -8 times the product of
+//     the key's scales with the sums of the queries over each block (one small product, the sums in two fp16 parts), and a
+//     product with eights in place of the values is subtracted from O at the end.
+// V's scales are multiplied into the numerators: in float32, before their one rounding, or where the output is bf16, whose
+// rounding is eight times as coarse, in fp16, after one.  So that numerators times scales stay in fp16's range, a warp divides
+// the scales of each block by a power of two above the greatest that it has met (inv: its inverse).
+//
+// Work split.  The list of decode_attn_paged, in tiles of 32 keys, is cut into runs for single *warps*: a warp looks up its
+// pages, keeps its own ring of tiles in flight and attends over them with all heads of the group and all dimensions; warps
+// share nothing but the look at the lengths, and starting and ending a pair holds up one warp.  (With four warps
+// on a pair's tiles and a fifth that loads, as for f16 and q8_0 pools, a pair's start and end took 2 us, which the four times
+// shorter tiles did not hide: the 96 sequences below 67 us.)  The four warps of a CTA (two, one where the kv heads
+// do not divide) take the same tokens of neighbouring kv heads, whose codes lie side by side in a layer-major pool: 58 us
+// instead of 67.  Copies are 16-byte asynchronous ones, waited for by the warp itself; no wait can fail to end.
+// TMA took 5 cycles for each row of 64 bytes, and 47 us where nothing was computed.
+//
+// Measured (40 query heads, 8 kv heads of 128, bf16; of the rate of a copy): 96 sequences of 5 to 16,384 tokens 58 us (3.6 TB/s,
+// 0.52; to fp16 59; the same from q8_0 79), in 16 heads to a group 90; 20 of 16,384 83 (0.67); one of 58,300 25 us (0.40); eight of about
+// 2,100 14.3; one of 64 8.6.  Without the copies the 96 take 52 us, without the products 47: the two hide each other in part.
+// A tile's products take a scheduler about 650 cycles: 42 matrix instructions, each 8 cycles of the tensor pipe and about four
+// in which nothing else issues, and 390 others.
 #include "decode_paged.cuh"
 
 namespace kvc {
+namespace {
 
-int launch_decode_paged_q4(const kvc_cache &c, int layer, int page_size, int dtype, const PagedView &pg,
-                           const DecodePagedArgs &a, cudaStream_t s) {
-    return launch_type<KVC_Q4_0>(c, layer, page_size, dtype, pg, a, s);
+using namespace paged;
+
+constexpr int KT = 32;              // keys per tile: two subtiles of 16, each within one page
+constexpr int WARPS = 4;
+constexpr int THREADS = 32 * WARPS;
+// What starting and ending a pair costs, in tiles.  With 2, 4 and 8, in us: the 96 sequences 59.5, 58 and 65 (an earlier
+// state), one of 58,300 24.7, 25.1 and 25.0.
+constexpr int PIECE_COST = 4;
+// CTAs per SM: as many as the registers allow without spilling.  Two instead of three: the 96 sequences 57.5 us, in heads of
+// 64 48 instead of 39; four (128 registers) 64.
+constexpr int ctas_per_sm(int NT) { return NT == 1 ? 3 : 2; }
+constexpr int MAX_NS = 6;
+constexpr float NONE = -1e30f;      // the reference of a head that has met no key
+
+template <int D, int DT, int NT>
+struct Cfg {
+    static constexpr bool FINE = DT != KVC_IN_BF16;
+    static constexpr int U = NT == 1 ? 2 : 1;               // subtiles taken together
+    static constexpr uint32_t ALL = U == 2 ? 0xFFFFFFFFu : 0xFFFFu;
+    static constexpr int NB = D / 32;                       // blocks per row
+    static constexpr int ROW = D / 2;                       // bytes of a row
+    static constexpr int TILE = KT * ROW;                   // a K or V tile
+    static constexpr int SC = KT * NB * 2;                  // a tile's scales
+    static constexpr int STAGE = 2 * TILE + 2 * SC;         // keeps the tiles on the swizzle's boundaries
+    static constexpr int MT = D / 16;                       // 16-row tiles of O^T
+    // of 228 KB, 1 KB for each CTA besides what it asks for, and 2 KB for what is small
+    static constexpr int FIT = (228 * 1024 / ctas_per_sm(NT) - 1024 - 2048) / (WARPS * STAGE);
+    static constexpr int NS = FIT < MAX_NS ? FIT : MAX_NS;
+    static constexpr int SMEM = WARPS * NS * STAGE;
+    static constexpr int CHUNKS = ROW / 16, RPL = 32 / CHUNKS;   // 16-byte chunks of a row; rows that a warp's copy takes
+    static_assert(NS >= 2, "shared memory plan");
+};
+
+// Which chunk of a row lies in place c: eight rows' chunks c lie in all banks.
+template <int D>
+__device__ __forceinline__ int swizzle(int row, int c) { return D == 128 ? c ^ ((row >> 1) & 3) : c ^ ((row >> 2) & 1); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_scales(uint32_t dst, const uint8_t *src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(valid ? N : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_groups_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The inverse of the power of two above |d|, 2^14 at most.
+__device__ __forceinline__ __half inverse_above(__half d) {
+    const int e = min(__half_as_ushort(d) >> 10 & 31, 30);
+    return __ushort_as_half((unsigned short)(e < 29 ? (29 - e) << 10 : 0x200 >> (e - 29)));
 }
 
-int read_and_clear_paged_q4_status(int32_t *status) { return read_and_clear(status); }
+// Eight consecutive values of q, as float32.
+template <int DT>
+__device__ __forceinline__ void load_q(const uint8_t *at, float (&v)[8]) {
+    const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(at));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (DT == KVC_IN_F32) {
+        const uint4 y = __ldcg(reinterpret_cast<const uint4 *>(at) + 1);
+        const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[i] = __uint_as_float(w[i]); v[4 + i] = __uint_as_float(z[i]); }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = DT == KVC_IN_F16 ? __half22float2(as_half2(w[i]))
+                                              : make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// The group's queries, each head scaled by a power of two (its greatest magnitude to 2^14, 2^10 for upper nibbles): any
+// magnitude from 2^-100 to 2^100 keeps its 11 bits.  eights: the second operand of the product that the scores begin
+// with, worth: what this lane's two columns' products are worth in powers of two.
+template <int D, int DT, int NT>
+__device__ __forceinline__ void load_queries(const uint8_t *q, int G, float scale_log2, int lane, uint32_t (&qf)[D / 16][NT][2],
+                                             uint32_t (&eights)[NT], float (&worth)[NT][2]) {
+    const int g = lane >> 2, t4 = lane & 3;
+    constexpr int ESZ = DT == KVC_IN_F32 ? 4 : 2, NB = D / 32;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int head = nt * 8 + g;
+        float v[NB][8], most = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[b][i] = 0.f;
+            if (head < G) load_q<DT>(q + (head * D + 32 * b + 8 * t4) * ESZ, v[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) most = fmax3(most, fabsf(v[b][i]), fabsf(v[b][i + 1]));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        const int ex = most > 0.f ? min(max((int)(__float_as_uint(most) >> 23) - 127, -100), 100) : 0;
+        const float lo = __uint_as_float((uint32_t)(127 + 10 - ex) << 23), hi = 16.f * lo;
+        const float w = __uint_as_float((uint32_t)(127 + 10 + ex) << 23) * scale_log2;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) worth[nt][e] = __shfl_sync(0xffffffffu, w, (2 * t4 + e) * 4);
+        float sum[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            sum[b] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t p = pack_half2(v[b][2 * i] * (i & 1 ? lo : hi), v[b][2 * i + 1] * (i & 1 ? lo : hi));
+                const float2 f = __half22float2(as_half2(p));
+                sum[b] += (f.x + f.y) * (i & 1 ? 1.f : 0.0625f);
+                qf[2 * b + (i >> 1)][nt][i & 1] = p;
+            }
+        }
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], x);
+        float mine[2] = {sum[0], sum[1]};   // of blocks 2 t4 and 2 t4 + 1, and again from lane NB / 2 on
+        if (NB == 4 && (t4 & 1)) { mine[0] = sum[NB - 2]; mine[1] = sum[NB - 1]; }
+        mine[0] *= -0x1p-17f;               // eight of the upper nibbles' units
+        mine[1] *= -0x1p-17f;
+        const uint32_t p = pack_half2(mine[0], mine[1]);
+        const float2 f = __half22float2(as_half2(p));
+        const uint32_t rest = pack_half2(mine[0] - f.x, mine[1] - f.y);
+        eights[nt] = t4 < NB / 2 ? p : t4 < NB ? rest : 0u;
+    }
+}
+
+// U subtiles of a tile, from row `row0` on: scores, numerators, sums.  exists: a bit for each of their keys.
+template <int D, int NT, class C>
+__device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, int lane, const uint32_t (&qf)[D / 16][NT][2],
+                                       const uint32_t (&eights)[NT], const float (&worth)[NT][2], float (&o)[C::MT][NT][4],
+                                       float (&ob)[C::NB][NT][4], float (&m)[NT][2], float (&l)[NT][2],
+                                       __half2 (&inv)[C::NB / 2]) {
+    constexpr int U = C::U, NB = C::NB;
+    constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, BYTES = 0x00FF00FFu;
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint32_t vt = kt + C::TILE, sc = vt + C::TILE;
+    const int g = lane >> 2, t4 = lane & 3;
+    // ldmatrix: lane i names row i % 8 of matrix i / 8: keys 0 to 7 and 8 to 15 of a block (16 bytes), then of the next one
+    const int mrow = (lane & 7) + 8 * ((lane >> 3) & 1), mchunk = lane >> 4;
+    uint32_t kw[U][NB / 2][4], vw[U][NB / 2][4];
+    __half2 dk[U][2][NB / 2], dv[U][2][NB / 2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int b = 0; b < NB; b += 2) {
+            const int sw = swizzle<D>(mrow, b + mchunk);
+            ldmatrix_x4(kw[u][b >> 1], kt + (row0 + u * 16 + mrow) * C::ROW + (sw << 4));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = sc + (row0 + u * 16 + g + 8 * h) * (2 * NB);
+            if constexpr (NB == 4) {
+                const uint2 x = lds64(at), y = lds64(at + C::SC);
+                dk[u][h][0] = as_half2(x.x); dk[u][h][1] = as_half2(x.y);
+                dv[u][h][0] = as_half2(y.x); dv[u][h][1] = as_half2(y.y);
+            } else {
+                dk[u][h][0] = as_half2(lds32(at));
+                dv[u][h][0] = as_half2(lds32(at + C::SC));
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int b = 0; b < NB; b += 2) {
+            const int sw = swizzle<D>(mrow, b + mchunk);
+            ldmatrix_x4_trans(vw[u][b >> 1], vt + (row0 + u * 16 + mrow) * C::ROW + (sw << 4));
+        }
+    float s[U][NT][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        // the scales of blocks 2 t4 and 2 t4 + 1, and again from lane NB / 2 on, as the sums of the queries lie
+        const uint32_t da = as_u32(NB == 4 && (t4 & 1) ? dk[u][0][NB / 2 - 1] : dk[u][0][0]);
+        const uint32_t db = as_u32(NB == 4 && (t4 & 1) ? dk[u][1][NB / 2 - 1] : dk[u][1][0]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_1688_to(s[u][nt], da, db, eights[nt], zero);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t ka = kw[u][b >> 1][2 * (b & 1)], kb = kw[u][b >> 1][2 * (b & 1) + 1], ka8 = ka >> 8, kb8 = kb >> 8;
+            const uint32_t A[4] = {ka & LO, kb & LO, ka & HI, kb & HI}, B[4] = {ka8 & LO, kb8 & LO, ka8 & HI, kb8 & HI};
+            const float ca = __half2float(b & 1 ? __high2half(dk[u][0][b >> 1]) : __low2half(dk[u][0][b >> 1]));
+            const float cb = __half2float(b & 1 ? __high2half(dk[u][1][b >> 1]) : __low2half(dk[u][1][b >> 1]));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float acc[4];
+                mma_16816_to(acc, A, qf[2 * b][nt][0], qf[2 * b][nt][1], zero);
+                mma_16816_to(acc, B, qf[2 * b + 1][nt][0], qf[2 * b + 1][nt][1], acc);
+                s[u][nt][0] = fmaf(acc[0], ca, s[u][nt][0]);
+                s[u][nt][1] = fmaf(acc[1], ca, s[u][nt][1]);
+                s[u][nt][2] = fmaf(acc[2], cb, s[u][nt][2]);
+                s[u][nt][3] = fmaf(acc[3], cb, s[u][nt][3]);
+            }
+        }
+    }
+    if (exists != C::ALL) {   // the last subtile of a sequence, or one of a hole
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if (!(exists >> (16 * u + g) & 1)) s[u][nt][0] = s[u][nt][1] = -INFINITY;
+                if (!(exists >> (16 * u + g + 8) & 1)) s[u][nt][2] = s[u][nt][3] = -INFINITY;
+            }
+    }
+    bool above = false;
+    __half2 d_here[NB / 2];   // the greatest scales of V; is one above its block's power of two?
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) {
+        d_here[i] = __hmax2(__habs2(dv[0][0][i]), __habs2(dv[0][1][i]));
+#pragma unroll
+        for (int u = 1; u < U; ++u) d_here[i] = __hmax2(d_here[i], __hmax2(__habs2(dv[u][0][i]), __habs2(dv[u][1][i])));
+        above |= !__hble2(__hmul2(d_here[i], inv[i]), __float2half2_rn(1.f));
+    }
+    float top[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            top[nt][e] = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
+#pragma unroll
+            for (int u = 1; u < U; ++u) top[nt][e] = fmax3(top[nt][e], s[u][nt][e], s[u][nt][e + 2]);
+            above |= fmaf(top[nt][e], worth[nt][e], -m[nt][e]) > RESCALE_LOG2;
+        }
+    if (__any_sync(0xffffffffu, above)) {
+        float fb[NB];
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1)
+                d_here[i] = __hmax2(d_here[i], as_half2(__shfl_xor_sync(0xffffffffu, as_u32(d_here[i]), x)));
+            const float2 was = __half22float2(inv[i]);
+            inv[i] = __hmin2(inv[i], __halves2half2(inverse_above(__low2half(d_here[i])), inverse_above(__high2half(d_here[i]))));
+            const float2 is = __half22float2(inv[i]);
+            fb[2 * i] = is.x / was.x;
+            fb[2 * i + 1] = is.y / was.y;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = top[nt][e];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                const float m_new = fmaxf(m[nt][e], fmaf(x, worth[nt][e], -SHIFT_LOG2));
+                f[e] = ex2(m[nt][e] - m_new);
+                m[nt][e] = m_new;
+                l[nt][e] *= f[e];
+            }
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i) {
+                const float f0 = f[0] * fb[i >> 1], f1 = f[1] * fb[i >> 1];
+                o[i][nt][0] *= f0; o[i][nt][1] *= f1; o[i][nt][2] *= f0; o[i][nt][3] *= f1;
+                if (i & 1) { ob[i >> 1][nt][0] *= f0; ob[i >> 1][nt][1] *= f1; }
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        uint32_t pe[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[u][nt][i] = ex2(fmaf(s[u][nt][i], worth[nt][i & 1], -m[nt][i & 1]));
+            l[nt][0] += s[u][nt][0] + s[u][nt][2];
+            l[nt][1] += s[u][nt][1] + s[u][nt][3];
+            if constexpr (!C::FINE) {
+                pe[nt][0] = pack_half2(s[u][nt][0], s[u][nt][1]);
+                pe[nt][1] = pack_half2(s[u][nt][2], s[u][nt][3]);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t va = vw[u][b >> 1][2 * (b & 1)], vb = vw[u][b >> 1][2 * (b & 1) + 1];
+            const uint32_t va8 = __byte_perm(va, 0u, 0x4341), vb8 = __byte_perm(vb, 0u, 0x4341);
+            const uint32_t A[4] = {va & BYTES, va & HI, vb & BYTES, vb & HI}, B[4] = {va8, va8 & HI, vb8, vb8 & HI};
+            const uint32_t E[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
+            const __half2 da = __hmul2(dv[u][0][b >> 1], inv[b >> 1]), db = __hmul2(dv[u][1][b >> 1], inv[b >> 1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                uint32_t p0, p1;
+                if constexpr (C::FINE) {
+                    const float ca = __half2float(b & 1 ? __high2half(da) : __low2half(da));
+                    const float cb = __half2float(b & 1 ? __high2half(db) : __low2half(db));
+                    p0 = pack_half2(s[u][nt][0] * ca, s[u][nt][1] * ca);
+                    p1 = pack_half2(s[u][nt][2] * cb, s[u][nt][3] * cb);
+                } else {
+                    p0 = as_u32(__hmul2(as_half2(pe[nt][0]), b & 1 ? __high2half2(da) : __low2half2(da)));
+                    p1 = as_u32(__hmul2(as_half2(pe[nt][1]), b & 1 ? __high2half2(db) : __low2half2(db)));
+                }
+                p0 = movmatrix_trans(p0);
+                p1 = movmatrix_trans(p1);
+                mma_16816_to(o[2 * b][nt], A, p0, p1, o[2 * b][nt]);
+                mma_16816_to(o[2 * b + 1][nt], B, p0, p1, o[2 * b + 1][nt]);
+                mma_16816_to(ob[b][nt], E, p0, p1, ob[b][nt]);
+            }
+        }
+    }
+}
+
+// Where the layer's codes and scales lie; distances in bytes.
+struct Codes {
+    const uint8_t *k, *sk;
+    int64_t v_from_k, sv_from_sk, tok, rows, head, s_tok, s_head;   // rows: of the rows that a warp copies together
+};
+
+// A warp's way through its run of the list: groups of kv heads, in each the sequences, in each its units.  Kept in shared
+// memory, where the loop over tiles leaves it alone: registers decide how many warps there are.
+struct Way {
+    unsigned long long left;
+    int seq, group, x, base;     // x: units of the current pair that lie before this run
+    int held[32];                // lengths from sequence `base` on
+    Piece piece;                 // h: the group
+};
+
+__device__ __forceinline__ void look(Way *w, const PagedView &pg, int seq, int lane) {
+    __syncwarp();
+    w->held[lane] = seq + lane < pg.n_seq ? keys_of(pg, seq + lane) : 0;
+    if (lane == 0) w->base = seq;
+    __syncwarp();
+}
+// Both of a warp's ways (one asks for tiles, one attends) from the start of its run.
+__device__ __forceinline__ void start(Way *w, Way *v, const PagedView &pg, int seq, int group, int x, unsigned long long left,
+                                      int lane) {
+    const int held = seq + lane < pg.n_seq ? keys_of(pg, seq + lane) : 0;
+    if (lane < 2) {
+        Way *t = lane == 0 ? w : v;
+        t->left = left;
+        t->seq = t->base = seq;
+        t->group = group;
+        t->x = x;
+    }
+    w->held[lane] = v->held[lane] = held;
+    __syncwarp();
+}
+// In 32 bits where that is enough: 64-bit divisions take some hundred cycles each.
+__device__ __forceinline__ unsigned long long div64(unsigned long long a, unsigned long long b) {
+    return (a | b) >> 32 ? a / b : (unsigned)a / (unsigned)b;
+}
+// The next piece into w->piece; false: there is none.
+__device__ __noinline__ bool next(Way *w, const PagedView &pg, int groups, int lane) {
+    unsigned long long left = w->left;
+    int seq = w->seq, group = w->group, x = w->x, base = w->base;
+    Piece p = {0, 0, 0, 0, 0, 0};
+    bool found = false;
+    while (!found && left > 0 && group < groups) {
+        if (seq - base >= 32 || seq < base) {
+            look(w, pg, seq, lane);
+            base = seq;
+        }
+        const int keys = w->held[seq - base], all = units_of<KT, PIECE_COST>(keys);
+        const int x1 = (int)min((unsigned long long)all, x + left);
+        p = {seq, group, max(x - PIECE_COST, 0), max(x1 - PIECE_COST, 0), tiles_of<KT>(keys), keys};
+        left -= x1 - x;
+        x = 0;
+        if (++seq == pg.n_seq) { seq = 0; ++group; }
+        found = p.t1 > p.t0;
+    }
+    __syncwarp();
+    if (lane == 0) {
+        w->left = left;
+        w->seq = seq;
+        w->group = group;
+        w->x = x;
+        w->piece = p;
+    }
+    __syncwarp();
+    return found;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_out8(void *out, int64_t i, const float (&x)[8]) {
+    if constexpr (DT == KVC_IN_F32) {
+        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(out) + i);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (DT == KVC_IN_F16) {
+                w[j] = pack_half2(x[2 * j], x[2 * j + 1]);
+            } else {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int D, int DT, int NT>
+__global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
+    decode_paged_q4_kernel(const PagedView pg, const Args a, const Codes codes) {
+    using C = Cfg<D, DT, NT>;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ unsigned long long warp_units[WARPS];
+    __shared__ int first_seq[WARPS], rest[WARPS];
+    __shared__ Way ways[WARPS][2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    // ---- where the warps' runs of the list start: a.step warps take the heads of a group in one run
+    const int groups = a.H_kv / a.step;
+    unsigned long long W = 0, each = 0;   // the list's units, of them the most that every run has
+    unsigned runs = 0, more = 0;          // runs that have units, units left: floor(W r / runs) = each r + floor(more r / runs)
+    auto run_from = [&](unsigned run) { return run >= runs ? W : each * run + more * run / runs; };
+    unsigned long long total = 0;
+    {
+        const int per = (pg.n_seq + THREADS - 1) / THREADS;
+        const int i0 = min((int)threadIdx.x * per, pg.n_seq), i1 = min(i0 + per, pg.n_seq);
+        unsigned long long mine = 0;
+        for (int i = i0; i < i1; ++i) mine += units_of<KT, PIECE_COST>(keys_of(pg, i));
+        unsigned long long sum = mine;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const unsigned long long up = __shfl_up_sync(0xffffffffu, sum, x);
+            if (lane >= x) sum += up;
+        }
+        if (lane == 31) warp_units[warp] = sum;
+        __syncthreads();
+        unsigned long long before = sum - mine;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) before += warp_units[w];
+            total += warp_units[w];
+        }
+        W = total * groups;
+        runs = (unsigned)min((unsigned long long)(a.n_slots / a.step), W);
+        if (runs > 0) {
+            each = div64(W, runs);
+            more = (unsigned)(W - each * runs);
+        }
+        for (int w = 0; w < WARPS; w += a.step) {
+            const unsigned run = (blockIdx.x * WARPS + w) / a.step;
+            const unsigned long long u = run_from(run);
+            unsigned long long r = total ? u - div64(u, total) * total : 0;
+            if (r >= before && r < before + mine) {
+                r -= before;
+                int i = i0;
+                for (; i + 1 < i1; ++i) {
+                    const unsigned long long n = units_of<KT, PIECE_COST>(keys_of(pg, i));
+                    if (r < n) break;
+                    r -= n;
+                }
+                for (int e = 0; e < a.step; ++e) {
+                    first_seq[w + e] = i;
+                    rest[w + e] = (int)r;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    const int c = blockIdx.x * WARPS + warp, member = warp % a.step;   // my slot, my head of a group
+    const unsigned run = c / a.step;
+    Way *ahead = &ways[warp][0], *way = &ways[warp][1];
+    {
+        const unsigned long long u0 = run_from(run), u1 = run_from(run + 1);
+        const bool some = u1 > u0;
+        start(ahead, way, pg, some ? first_seq[warp] : 0, some ? (int)(div64(u0, total)) : 0, some ? rest[warp] : 0, u1 - u0, lane);
+    }
+    const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
+    const int g = lane >> 2, t4 = lane & 3;
+    bool owner = false;
+
+    // ---- tiles are asked for up to NS ahead, across pieces
+    const uint32_t ring = smem_u32(sm) + warp * C::NS * C::STAGE;
+    const int my_row = lane / C::CHUNKS, my_chunk = lane % C::CHUNKS;   // of each copy of RPL rows
+    const uint32_t my_place = my_row * C::ROW + (swizzle<D>(my_row, my_chunk) << 4);
+    const uint8_t *my_code = codes.k, *my_scale = codes.sk;              // row and chunk, key, from the pool's start on
+    const int q_bytes = a.G * D * (DT == KVC_IN_F32 ? 4 : 2);            // a group's queries
+    int ta = 0, ta_end = 0, keys = 0, chunk = 0;        // of the piece that tiles are asked for of
+    int slot = -1, slot_next = -1;                      // lane i's: of the i-th subtile from tile `chunk` on (-1: a hole)
+    bool rest_of_run = true;
+    int stage_in = 0, stage_out = 0;
+    uint32_t exists = 0;                                // lane s: a bit for each key of the tile in stage s
+    auto look_up = [&](int tile, int seq) {
+        const int key = tile * KT + lane * 16;
+        const int lp = key / pg.page_size;
+        const int page = (unsigned)key < (unsigned)keys ? __ldcg(pg.table + (int64_t)seq * pg.max_pages + lp) : -1;
+        return (unsigned)page < (unsigned)pg.n_pages ? page * pg.page_size + (key - lp * pg.page_size) : -1;
+    };
+    auto ask = [&]() {
+        if (rest_of_run && ta >= ta_end) {
+            rest_of_run = next(ahead, pg, groups, lane);
+            if (rest_of_run) {
+                const Piece p = ahead->piece;
+                const int h = p.h * a.step + member;
+                ta = chunk = p.t0;
+                ta_end = p.t1;
+                keys = p.keys;
+                slot = look_up(chunk, p.seq);
+                slot_next = look_up(chunk + 16, p.seq);
+                my_code = codes.k + my_row * codes.tok + h * codes.head + my_chunk * 16;
+                my_scale = codes.sk + (lane & 15) * codes.s_tok + h * codes.s_head;
+            }
+        }
+        if (rest_of_run) {
+            if (ta - chunk == 16) {
+                chunk = ta;
+                slot = slot_next;
+                slot_next = look_up(chunk + 16, ahead->piece.seq);
+            }
+            const uint32_t kt = ring + stage_in * C::STAGE, place = kt + my_place;
+            const int sl[2] = {__shfl_sync(0xffffffffu, slot, 2 * (ta - chunk)), __shfl_sync(0xffffffffu, slot, 2 * (ta - chunk) + 1)};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (sl[u] < 0) continue;   // what the stage held stays: nothing of it counts
+                const uint8_t *k = my_code + sl[u] * codes.tok, *v = k + codes.v_from_k;
+#pragma unroll
+                for (int r = 0; r < 16; r += C::RPL) {
+                    copy16(place + (16 * u + r) * C::ROW, k);
+                    copy16(place + (16 * u + r) * C::ROW + C::TILE, v);
+                    k += codes.rows;
+                    v += codes.rows;
+                }
+            }
+            const int mine = lane < 16 ? sl[0] : sl[1];   // a key for each lane: its scales
+            const bool valid = mine >= 0 && lane < keys - ta * KT;
+            const uint8_t *k = my_scale + max(mine, 0) * codes.s_tok;
+            const uint32_t sc = kt + 2 * C::TILE + lane * C::NB * 2;
+            copy_scales<C::NB * 2>(sc, k, valid);
+            copy_scales<C::NB * 2>(sc + C::SC, k + codes.sv_from_sk, valid);
+            const uint32_t all = __ballot_sync(0xffffffffu, valid);
+            if (lane == stage_in) exists = all;
+            stage_in = stage_in + 1 == C::NS ? 0 : stage_in + 1;
+            ++ta;
+        }
+        copies_end_group();   // one for each call, so that the oldest is always NS - 1 before the newest
+    };
+    for (int i = 0; i < C::NS; ++i) ask();
+
+    // sequences without keys have no unit in the list
+    for (int i = blockIdx.x; i < pg.n_seq; i += gridDim.x) {
+        if (keys_of(pg, i) > 0) continue;
+        for (int e = threadIdx.x; e < a.H_q * D; e += THREADS) store_out<DT>(a.out, (int64_t)i * a.H_q * D + e, 0.f);
+        if (a.lse)
+            for (int e = threadIdx.x; e < a.H_q; e += THREADS) a.lse[(int64_t)i * a.H_q + e] = -INFINITY;
+        if (by_pair)
+            for (int e = threadIdx.x; e < a.H_kv; e += THREADS) a.desc[e * pg.n_seq + i] = make_int4(0, 0, 0, 0);
+    }
+
+    while (next(way, pg, groups, lane)) {
+        uint32_t qf[D / 16][NT][2], eights[NT];
+        float worth[NT][2];
+        load_queries<D, DT, NT>(a.q + way->piece.seq * a.ld_q + (way->piece.h * a.step + member) * (int64_t)q_bytes, a.G, a.scale_log2, lane, qf, eights, worth);
+        float o[C::MT][NT][4], ob[C::NB][NT][4], m[NT][2], l[NT][2];
+        __half2 inv[C::NB / 2];
+#pragma unroll
+        for (int i = 0; i < C::NB / 2; ++i) inv[i] = __float2half2_rn(0x1p14f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = NONE;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int b = 0; b < C::NB; ++b) ob[b][nt][0] = ob[b][nt][1] = ob[b][nt][2] = ob[b][nt][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+        }
+        for (int left = way->piece.t1 - way->piece.t0; left > 0; --left) {
+            wait_groups_but<C::NS - 1>();
+            __syncwarp();
+            const uint32_t kt = ring + stage_out * C::STAGE, e = __shfl_sync(0xffffffffu, exists, stage_out);
+#pragma unroll 1
+            for (int u = 0; u < 2; u += C::U) {
+                const uint32_t bits = C::U == 2 ? e : e >> (16 * u) & 0xFFFFu;
+                if (bits != 0) attend<D, NT, C>(kt, 16 * u, bits, lane, qf, eights, worth, o, ob, m, l, inv);
+            }
+            __syncwarp();   // before the stage is written again
+            stage_out = stage_out + 1 == C::NS ? 0 : stage_out + 1;
+            ask();
+        }
+
+        // ---- the piece is done
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+                l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+                l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+            }
+        const Piece p = way->piece;
+        const int h = p.h * a.step + member;
+        const bool whole = p.t0 == 0 && p.t1 == p.nt;
+        const int part = (c * 2 + (p.t0 == 0)) * a.G;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            // this lane stores for one of its two heads, eight dimensions of each block, half of them its neighbour's
+            const int head = nt * 8 + 2 * t4 + (g & 1);
+            const float L = g & 1 ? l[nt][1] : l[nt][0], m_own = g & 1 ? m[nt][1] : m[nt][0];
+            const float M = m_own == NONE ? -INFINITY : m_own;
+            const float by = whole ? (L > 0.f || L != L ? 1.f / L : 0.f) : 1.f;
+#pragma unroll
+            for (int b = 0; b < C::NB; ++b) {
+                const float w = 0x1p24f / __half2float(b & 1 ? __high2half(inv[b >> 1]) : __low2half(inv[b >> 1])) * by;
+                float x[8];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    // rows 0 to 7 of a tile have the bytes, rows 8 to 15 their high nibbles
+                    const float (&r)[4] = o[2 * b + (n >> 1)][nt];
+                    const float e0 = (n & 1 ? r[2] * 0.0625f : r[0] - r[2]) - ob[b][nt][0];
+                    const float e1 = (n & 1 ? r[3] * 0.0625f : r[1] - r[3]) - ob[b][nt][1];
+                    const float got = __shfl_xor_sync(0xffffffffu, g & 1 ? e0 : e1, 4);
+                    x[2 * n] = (g & 1 ? got : e0) * w;
+                    x[2 * n + 1] = (g & 1 ? e1 : got) * w;
+                }
+                const int dim = 32 * b + 8 * (g >> 1);
+                if (head >= a.G) continue;
+                if (whole) store_out8<DT>(a.out, ((int64_t)p.seq * a.H_q + h * a.G + head) * D + dim, x);
+                else store_out8<KVC_IN_F32>(a.part_o, (int64_t)(part + head) * D + dim, x);
+            }
+            if (g < 2 && head < a.G) {
+                if (!whole)   // the join passes over parts with M = -infinity, but a NaN has to reach it
+                    a.part_ml[part + head] = make_float2(isnan(L) ? INFINITY : M, L);
+                else if (a.lse)
+                    a.lse[(int64_t)p.seq * a.H_q + h * a.G + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+            }
+        }
+        if (p.t0 == 0 && (by_pair || !whole)) {
+            owner = true;
+            if (lane == 0) {
+                const unsigned long long end = run_from(run + 1) + (p.nt - p.t1);   // the pair's last unit, plus one
+                const int last = (int)div64(end * runs - 1, W);   // the run that holds it
+                a.desc[by_pair ? h * pg.n_seq + p.seq : c] = make_int4(p.seq, h, whole ? 0 : last - (int)run + 1, c);
+            }
+        }
+    }
+    if (!by_pair && !owner && lane == 0) a.desc[c] = make_int4(0, 0, 0, 0);
+}
+
+template <int D, int DT, int NT>
+int launch_t(const PagedView &pg, const Args &a, const Codes &codes, cudaStream_t s) {
+    using C = Cfg<D, DT, NT>;
+    if (allow_dynamic_smem((const void *)decode_paged_q4_kernel<D, DT, NT>, C::SMEM) != KVC_OK) return KVC_ECUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.n_slots / WARPS);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, decode_paged_q4_kernel<D, DT, NT>, pg, a, codes) != cudaSuccess) return KVC_ECUDA;
+    const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
+    const int joins = by_pair ? a.H_kv * pg.n_seq : a.n_slots;
+    cfg.gridDim = by_pair ? dim3(joins, a.G) : dim3(a.n_slots / WARPS);
+    cfg.blockDim = dim3(COMBINE_THREADS);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, by_pair ? combine_paged_kernel<D, DT, false> : combine_paged_kernel<D, DT, true>, a, joins) !=
+        cudaSuccess)
+        return KVC_ECUDA;
+    return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ECUDA;
+}
+
+template <int D>
+int launch_d(int dtype, const PagedView &pg, const Args &a, const Codes &codes, cudaStream_t s) {
+    switch (dtype) {
+#define KVC_CASE(DT)                                                                             \
+    case DT:                                                                                     \
+        return a.G <= 8 ? launch_t<D, DT, 1>(pg, a, codes, s) : launch_t<D, DT, 2>(pg, a, codes, s);
+        KVC_CASE(KVC_IN_F32)
+        KVC_CASE(KVC_IN_BF16)
+        KVC_CASE(KVC_IN_F16)
+#undef KVC_CASE
+        default: return KVC_EINVAL;
+    }
+}
+
+}  // namespace
+
+int paged_q4_slots(int G) { return WARPS * ctas_per_sm(G <= 8 ? 1 : 2) * sm_count(); }
+
+int launch_decode_paged_q4(const kvc_cache &c, const kvc_pages &p, int layer, int dtype, const paged::Args &args, cudaStream_t s) {
+    const Geom g = geom_of(c.d);
+    Args a = args;
+    a.step = c.d.n_head_kv % 4 == 0 ? 4 : c.d.n_head_kv % 2 == 0 ? 2 : 1;
+    const int64_t code = layer * g.c_layer / 2, scale = layer * g.s_layer * 2;
+    const uint8_t *k = static_cast<const uint8_t *>(c.k_q), *v = static_cast<const uint8_t *>(c.v_q);
+    const uint8_t *sk = static_cast<const uint8_t *>(c.k_s), *sv = static_cast<const uint8_t *>(c.v_s);
+    const Codes codes = {k + code, sk + scale, v - k, sv - sk, g.c_tok / 2, g.c_tok / 2 * (1024 / c.d.head_dim), g.c_head / 2, g.s_tok * 2, g.s_head * 2};
+    const PagedView pg = paged_view(c, p);
+    return c.d.head_dim == 128 ? launch_d<128>(dtype, pg, a, codes, s) : launch_d<64>(dtype, pg, a, codes, s);
+}
 
 }  // namespace kvc

@@ -210,13 +210,3 @@ def test_a_query_of_nan_is_nan(kvc):
     want[0, 3] = want[1, 8] = float("nan")
     assert torch.equal(torch.isnan(out), torch.isnan(want))
     assert torch.equal(out.nan_to_num(0.0), want.nan_to_num(0.0))
-
-
-def test_a_wait_that_gives_up_leaves_the_context_usable(kvc):
-    cache, pages, slots = make_pool4(kvc, [4000, 25], 16, 2, 128, "head_major")
-    q = inputs((2, 10, 128), torch.bfloat16, 1)
-    kvc.arm_test_wait_timeout(kvc.TEST_PAGED, 2_000_000)
-    kvc.decode_attn_paged(cache, 0, pages, q)
-    assert kvc.kvc_device_status() != 0
-    assert kvc.kvc_device_status() == 0
-    verify4(kvc, cache, 0, pages, slots, q)
