@@ -12,7 +12,9 @@ library reports an error.
 """
 
 import ctypes
+import math
 import os
+from fractions import Fraction
 
 import torch
 
@@ -22,6 +24,8 @@ LIB_PATH = os.path.join(_HERE, "libkvc.so")
 KVC_OK, KVC_EINVAL, KVC_ERANGE, KVC_ENOSPC, KVC_EFORMAT, KVC_ECUDA, KVC_EDEVICE = 0, -1, -2, -3, -4, -5, -6
 CACHE_TYPES = {"f16": 0, "q8_0": 1, "q4_0": 2}
 LAYOUTS = {"head_major": 0, "layer_major": 1}
+# 2^64 / (2 pi), to 2^-128 of itself
+_TURN = Fraction(1 << 64) / (2 * Fraction(3141592653589793238462643383279502884197, 10 ** 39))
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -44,6 +48,10 @@ class kvc_cache(ctypes.Structure):
 class kvc_pages(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("n_seq", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class kvc_rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("n_pairs", ctypes.c_int32), ("style", ctypes.c_int32)]
 
 
 def _load():
@@ -81,6 +89,10 @@ def _load():
         "kvc_packed_scratch_bytes": (ctypes.c_int, [I32, I32, I32, I32, I32, P(SZ)]),
         "attn_packed": (ctypes.c_int, [VP, VP, VP, I64, I64, I64, I32, VP, VP, I32, I32, I32, I32, I32, I32, VP, VP,
                                        VP, SZ, VP]),
+        "qk_norm_rope": (ctypes.c_int, [VP, VP, VP, I64, I64, I32, I32, I32, I32, I32, VP, VP, VP, ctypes.c_float, VP, VP,
+                                        I64, I64, VP]),
+        "qk_norm_rope_append": (ctypes.c_int, [VP, VP, I32, VP, I32, VP, VP, VP, VP, I64, I64, I64, I32, I32, VP, VP,
+                                               ctypes.c_float, VP, I64, VP]),
         "kvc_test_arm_wait_timeout": (ctypes.c_int, [I32, ctypes.c_uint64]),
     }
     for name, (res, args) in sig.items():
@@ -588,6 +600,107 @@ def attn_packed(q, k, v, q_start, k_start=None, out=None, lse=None, scratch=None
     if st:
         raise KvcError(st, "attn_packed")
     return out
+
+
+ROPE_STYLES = {"half": 0, "pairs": 1}
+
+
+class RopeTable:
+    """A rotation by position of the first `rot` values of each head: pairs (i, i + rot / 2) ("half") or (2 i, 2 i + 1)
+    ("pairs"), pair i by position * base ** (-2 i / rot), or by position * inv_freq[i] where inv_freq (a sequence or
+    tensor of rot / 2 frequencies in radians) is given.  The frequencies are kept as 64-bit fractions of a turn on
+    `device`: angles are exact to about 2^-32 of a turn at any position.  rot = 0: no rotation."""
+
+    def __init__(self, rot, base=10000.0, style="half", inv_freq=None, device="cuda"):
+        if rot < 0 or rot % 2 or style not in ROPE_STYLES:
+            raise ValueError('rot must be even and style "half" or "pairs"')
+        n = rot // 2
+        if inv_freq is None:
+            freq = [float(base) ** (-2.0 * i / rot) for i in range(n)]
+        else:
+            freq = [float(f) for f in inv_freq]
+        if len(freq) != n or not all(math.isfinite(f) for f in freq):
+            raise ValueError("inv_freq must be rot / 2 finite frequencies")
+        # 2^64 / (2 pi) times the frequency, in integers: a float's product would lose the last bits
+        turns = [round(Fraction(f) * _TURN) % (1 << 64) for f in freq]
+        turns = [t - (1 << 64) if t >= 1 << 63 else t for t in turns]
+        self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
+        self.rot, self.style, self.device = rot, style, self.turns.device
+        self.c = kvc_rope(self.turns.data_ptr() if n else None, n, ROPE_STYLES[style])
+        self.addr = ctypes.addressof(self.c)
+
+
+def _weight(w, what, head_dim, dtype, device):
+    if w is None:
+        return None
+    if w.shape != (head_dim,) or w.dtype != dtype or w.device != device or not w.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor [%d] on %s" % (what, dtype, head_dim, device))
+    return w.data_ptr()
+
+
+def _rows_out(t, what, like, heads, head_dim, dtype, device):
+    """An output of packed rows, which may have a distance of its own between rows: (tensor, ld)."""
+    if t is None:
+        t = torch.empty(like.shape, dtype=dtype, device=device)
+        return t, heads * head_dim
+    ld = _packed_rows(t, what, heads, head_dim, dtype, device)
+    if t.shape[0] != like.shape[0]:
+        raise ValueError("%s must have the rows of its input" % what)
+    return t, ld
+
+
+def qk_norm_rope(q, k, positions, rope, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Norms and rotation of packed rows in one pass: q [rows][H_q][D], k [rows][H_kv][D] divided by their root mean
+    square for each head (where a weight [D] of their type is given) times the weight, then rotated by positions
+    (int32 [rows]) as rope (a RopeTable) says.  Returns (q_out, k_out); outputs may be the inputs themselves."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out)
+    dev, dtype, code = q.device, q.dtype, DTYPES.get(q.dtype)
+    if q.dim() != 3 or k.dim() != 3 or code is None or dev.type != "cuda" or rope.device != dev:
+        raise ValueError("q and k must be f32, bf16 or f16 tensors [rows][heads][D] on the rope's CUDA device")
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    ld_q, ld_k = _packed_rows(q, "q", hq, d, dtype, dev), _packed_rows(k, "k", hkv, d, dtype, dev)
+    if k.shape[0] != n:
+        raise ValueError("q and k must have the same rows")
+    if positions.shape != (n,) or positions.dtype != torch.int32 or positions.device != dev or \
+            not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 tensor [rows] on %s" % dev)
+    qw, kw = _weight(q_weight, "q_weight", d, dtype, dev), _weight(k_weight, "k_weight", d, dtype, dev)
+    q_out, ld_qo = _rows_out(q_out, "q_out", q, hq, d, dtype, dev)
+    k_out, ld_ko = _rows_out(k_out, "k_out", k, hkv, d, dtype, dev)
+    st = _lib().qk_norm_rope(rope.addr, q.data_ptr(), k.data_ptr(), ld_q, ld_k, code, n, hq, hkv, d,
+                             positions.data_ptr(), qw, kw, eps, q_out.data_ptr(), k_out.data_ptr(), ld_qo, ld_ko, _on(dev))
+    if st:
+        raise KvcError(st, "qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_append(cache, layer, pages, row_start, q, k, v, rope, q_weight=None, k_weight=None, eps=1e-6, q_out=None,
+                        stream=None):
+    """qk_norm_rope of packed rows at the positions that pages and row_start give them, and kv_paged_append of the
+    resulting keys and of v, in one pass.  Returns the queries."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_norm_rope_append(cache, layer, pages, row_start, q, k, v, rope, q_weight, k_weight, eps, q_out)
+    dev, dtype, code = _pool(cache, pages), q.dtype, DTYPES.get(q.dtype)
+    if q.dim() != 3 or code is None or rope.device != dev:
+        raise ValueError("q must be an f32, bf16 or f16 tensor [rows][H_q][D], the rope on its device")
+    n, hq, d = q.shape[0], q.shape[1], cache.head_dim
+    ld_q = _packed_rows(q, "q", hq, d, dtype, dev)
+    ld_k = _packed_rows(k, "k", cache.n_head_kv, d, dtype, dev)
+    ld_v = _packed_rows(v, "v", cache.n_head_kv, d, dtype, dev)
+    if k.shape[0] != n or v.shape[0] != n:
+        raise ValueError("q, k and v must have the same rows")
+    qw, kw = _weight(q_weight, "q_weight", d, dtype, dev), _weight(k_weight, "k_weight", d, dtype, dev)
+    q_out, ld_qo = _rows_out(q_out, "q_out", q, hq, d, dtype, dev)
+    st = _lib().qk_norm_rope_append(cache.addr, pages.addr, layer, _starts(row_start, "row_start", pages.n_seq, dev), n,
+                                    rope.addr, q.data_ptr(), k.data_ptr(), v.data_ptr(), ld_q, ld_k, ld_v, code, hq, qw, kw,
+                                    eps, q_out.data_ptr(), ld_qo, _on(dev))
+    if st:
+        raise KvcError(st, "qk_norm_rope_append")
+    return q_out
 
 
 def kvc_device_status():

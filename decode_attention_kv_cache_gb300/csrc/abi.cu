@@ -422,6 +422,58 @@ int attn_packed(const void *q, const void *k, const void *v, int64_t ld_q, int64
     return launch_packed(a, scratch, (cudaStream_t)stream);
 }
 
+static bool rope_ok(const kvc_rope *r, int32_t head_dim, float eps) {
+    if (!r || r->n_pairs < 0 || r->n_pairs > head_dim / 2) return false;
+    if (r->style != KVC_ROPE_HALF && r->style != KVC_ROPE_PAIRS) return false;
+    if (r->style == KVC_ROPE_HALF && r->n_pairs % 8 != 0) return false;
+    if (r->n_pairs > 0 && (!r->turns || (reinterpret_cast<uintptr_t>(r->turns) & 7u))) return false;
+    return eps >= 0.f && eps <= 3.402823466e38f && head_dim > 0 && head_dim % 32 == 0 && head_dim <= 256;
+}
+
+// a weight's address has its type's alignment
+static bool weight_ok(const void *w, int dtype) {
+    return (reinterpret_cast<uintptr_t>(w) & (uintptr_t)(dtype_bytes(dtype) - 1)) == 0;
+}
+
+int qk_norm_rope(const kvc_rope *rope, const void *q, const void *k, int64_t ld_q, int64_t ld_k, int32_t dtype,
+                 int32_t n_rows, int32_t n_head_q, int32_t n_head_kv, int32_t head_dim, const int32_t *pos,
+                 const void *q_weight, const void *k_weight, float eps, void *q_out, void *k_out, int64_t ld_qo,
+                 int64_t ld_ko, kvc_stream_t stream) {
+    if (!dtype_ok(dtype) || !rope_ok(rope, head_dim, eps) || n_rows < 0) return KVC_EINVAL;
+    if (n_head_q <= 0 || n_head_kv < 0 || (int64_t)n_head_q + n_head_kv > 65535) return KVC_EINVAL;
+    if (!ld_ok(ld_q, n_head_q, head_dim, dtype) || !ld_ok(ld_qo, n_head_q, head_dim, dtype)) return KVC_EINVAL;
+    if (n_head_kv > 0 && (!ld_ok(ld_k, n_head_kv, head_dim, dtype) || !ld_ok(ld_ko, n_head_kv, head_dim, dtype)))
+        return KVC_EINVAL;
+    if (!weight_ok(q_weight, dtype) || !weight_ok(k_weight, dtype)) return KVC_EINVAL;
+    if (n_rows == 0) return KVC_OK;
+    if (!q || !q_out || !pos || !aligned16(q) || !aligned16(q_out)) return KVC_EINVAL;
+    if (n_head_kv > 0 && (!k || !k_out || !aligned16(k) || !aligned16(k_out))) return KVC_EINVAL;
+    const RopeArgs a = {q, k, nullptr, ld_q, ld_k, 0, dtype, n_rows, n_head_q, n_head_kv, head_dim, pos, rope->turns,
+                        rope->n_pairs, rope->style, q_weight, k_weight, eps, q_out, k_out, ld_qo, ld_ko};
+    return launch_rope(a, (cudaStream_t)stream);
+}
+
+int qk_norm_rope_append(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const int32_t *row_start,
+                        int32_t n_rows, const kvc_rope *rope, const void *q, const void *k, const void *v, int64_t ld_q,
+                        int64_t ld_k, int64_t ld_v, int32_t dtype, int32_t n_head_q, const void *q_weight,
+                        const void *k_weight, float eps, void *q_out, int64_t ld_qo, kvc_stream_t stream) {
+    if (!pool_ok(pool) || !pages_ok(pool, pages) || !dtype_ok(dtype) || n_rows < 0) return KVC_EINVAL;
+    const int H = pool->d.n_head_kv, D = pool->d.head_dim;
+    if (!rope_ok(rope, D, eps)) return KVC_EINVAL;
+    if (n_head_q <= 0 || (int64_t)n_head_q + 2 * (int64_t)H > 65535) return KVC_EINVAL;
+    if (!ld_ok(ld_q, n_head_q, D, dtype) || !ld_ok(ld_qo, n_head_q, D, dtype) || !ld_ok(ld_k, H, D, dtype) ||
+        !ld_ok(ld_v, H, D, dtype))
+        return KVC_EINVAL;
+    if (!weight_ok(q_weight, dtype) || !weight_ok(k_weight, dtype)) return KVC_EINVAL;
+    if (layer < 0 || layer >= pool->d.n_layer) return KVC_ERANGE;
+    if (n_rows == 0 || pages->n_seq == 0) return KVC_OK;
+    if (!pages->table || !pages->len || !row_start || !q || !k || !v || !q_out) return KVC_EINVAL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return KVC_EINVAL;
+    const RopeArgs a = {q, k, v, ld_q, ld_k, ld_v, dtype, n_rows, n_head_q, H, D, nullptr, rope->turns,
+                        rope->n_pairs, rope->style, q_weight, k_weight, eps, q_out, nullptr, ld_qo, 0};
+    return launch_rope_append(a, *pool, *pages, layer, row_start, (cudaStream_t)stream);
+}
+
 int kv_cache_truncate(const kvc_cache *cache, int32_t n_tokens, kvc_stream_t stream) {
     if (!pool_ok(cache)) return KVC_EINVAL;
     const kvc_desc &d = cache->d;

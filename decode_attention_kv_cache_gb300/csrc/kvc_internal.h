@@ -106,6 +106,23 @@ struct PackedArgs {
 size_t packed_scratch_bytes(int n_rows, int n_seq, int n_head_q, int n_head_kv, int head_dim);
 int launch_packed(const PackedArgs &a, void *scratch, cudaStream_t s);
 
+// Norms and rotation; STORE variants take keys and values to a pool.
+struct RopeArgs {
+    const void *q, *k, *v;
+    int64_t ld_q, ld_k, ld_v;
+    int dtype, n_rows, H_q, H_kv, D;
+    const int32_t *pos;
+    const uint64_t *turns;
+    int n_pairs, style;
+    const void *q_weight, *k_weight;
+    float eps;
+    void *q_out, *k_out;
+    int64_t ld_qo, ld_ko;
+};
+int launch_rope(const RopeArgs &a, cudaStream_t s);
+int launch_rope_append(const RopeArgs &a, const kvc_cache &c, const kvc_pages &p, int layer, const int32_t *row_start,
+                       cudaStream_t s);
+
 // Test hook of the failure path: the wait limit (ns) of a stall armed for the next launch of a kernel
 // kind (KVC_TEST_PREFILL, KVC_TEST_DECODE, KVC_TEST_PAGED or KVC_TEST_PACKED), 0 when none; take_ consumes it.
 void arm_test_stall(int which, uint64_t limit_ns);

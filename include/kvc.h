@@ -501,6 +501,49 @@ int attn_packed(const void *q, const void *k, const void *v, int64_t ld_q, int64
                 int32_t n_head_q, int32_t n_head_kv, int32_t head_dim, void *out, float *lse, void *scratch,
                 size_t scratch_bytes, kvc_stream_t stream);
 
+/* A rotation by position of the first 2 * n_pairs values of each head:
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = position * frequency of the pair.
+ * Pair i is values (i, i + n_pairs) (KVC_ROPE_HALF; n_pairs a multiple of 8) or
+ * (2 i, 2 i + 1) (KVC_ROPE_PAIRS).  turns (device): each pair's frequency in turns,
+ * frequency / (2 pi) modulo 1, as a fraction of 2^64 rounded to an integer, so that
+ * angles are exact to about 2^-32 of a turn at any position.  n_pairs 0: no
+ * rotation (turns may be null). */
+typedef struct {
+    const uint64_t *turns; /* device [n_pairs], 8-byte aligned */
+    int32_t n_pairs;       /* 0 .. head_dim / 2 */
+    int32_t style;         /* kvc_rope_style */
+} kvc_rope;
+typedef enum { KVC_ROPE_HALF = 0, KVC_ROPE_PAIRS = 1 } kvc_rope_style;
+
+/* Norms and rotation of queries and keys in one pass, for each row and head:
+ *   y = x / sqrt(mean(x^2) + eps) * weight, then the rotation by pos[row].
+ * q: [n_rows][n_head_q][head_dim], k: [n_rows][n_head_kv][head_dim] in `dtype`, ld_*
+ * elements between rows (packed rows as for kv_paged_append); q_out and k_out: the
+ * same shapes and type.  An output may be its input (the same pointer and ld); else
+ * outputs overlap nothing.  q_weight, k_weight: [head_dim] in `dtype`, or null: that
+ * tensor is rotated only.  pos: device int32 [n_rows], any values.  Sums, norms and
+ * products in float32, one rounding to `dtype`.  Values finite, their squares' sums
+ * within float32.  head_dim a multiple of 32 up to 256; n_head_q + n_head_kv <= 65535;
+ * n_head_kv may be 0 (k, k_out null).  n_rows == 0 is a no-op.
+ * Errors: KVC_EINVAL (null or unaligned pointers, dtype, shapes, ld, rope, an eps
+ * that is negative or not finite). */
+int qk_norm_rope(const kvc_rope *rope, const void *q, const void *k, int64_t ld_q, int64_t ld_k, int32_t dtype,
+                 int32_t n_rows, int32_t n_head_q, int32_t n_head_kv, int32_t head_dim, const int32_t *pos,
+                 const void *q_weight, const void *k_weight, float eps, void *q_out, void *k_out, int64_t ld_qo,
+                 int64_t ld_ko, kvc_stream_t stream);
+
+/* qk_norm_rope of packed rows and kv_paged_append of its keys and of v in one pass: the
+ * rows' positions are those that pages and row_start give them, q_out receives the
+ * queries, and the pool (of any type) the bytes that kv_paged_append stores of k_out
+ * and v.  Rows of holes are dropped from the pool, but have queries; rows that
+ * belong to no sequence are neither used nor written.  Two calls in one: nothing of
+ * k goes through memory in between.  head_dim up to 256.  Errors as qk_norm_rope and
+ * kv_paged_append. */
+int qk_norm_rope_append(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const int32_t *row_start,
+                        int32_t n_rows, const kvc_rope *rope, const void *q, const void *k, const void *v, int64_t ld_q,
+                        int64_t ld_k, int64_t ld_v, int32_t dtype, int32_t n_head_q, const void *q_weight,
+                        const void *k_weight, float eps, void *q_out, int64_t ld_qo, kvc_stream_t stream);
+
 /* ---- diagnostics ------------------------------------------------------------- */
 
 /* A short static description of a status code. */
