@@ -50,6 +50,10 @@ class kvc_pages(ctypes.Structure):
                 ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
 
+class kvc_free_pages(ctypes.Structure):
+    _fields_ = [("ring", ctypes.c_void_p), ("state", ctypes.c_void_p), ("n_pages", ctypes.c_int32)]
+
+
 class kvc_rope(ctypes.Structure):
     _fields_ = [("turns", ctypes.c_void_p), ("n_pairs", ctypes.c_int32), ("style", ctypes.c_int32)]
 
@@ -89,6 +93,7 @@ def _load():
         "kvc_packed_scratch_bytes": (ctypes.c_int, [I32, I32, I32, I32, I32, P(SZ)]),
         "attn_packed": (ctypes.c_int, [VP, VP, VP, I64, I64, I64, I32, VP, VP, I32, I32, I32, I32, I32, I32, VP, VP,
                                        VP, SZ, VP]),
+        "kv_pages_advance": (ctypes.c_int, [VP, VP, VP, VP, I32, VP, VP, VP]),
         "qk_norm_rope": (ctypes.c_int, [VP, VP, VP, I64, I64, I32, I32, I32, I32, I32, VP, VP, VP, ctypes.c_float, VP, VP,
                                         I64, I64, VP]),
         "qk_norm_rope_append": (ctypes.c_int, [VP, VP, I32, VP, I32, VP, VP, VP, VP, I64, I64, I64, I32, I32, VP, VP,
@@ -443,6 +448,33 @@ class PageTable:
         self.__dict__[name] = value
 
 
+class FreePages:
+    """The free pages of a pool of n_pages pages, for kv_pages_advance: ring (int32 [n_pages]), and state (int32 [3]: where
+    the ring begins, how many pages it holds, how many were asked for and not there), on the device.  pages: those
+    that are free at first (a sequence or int32 tensor of page numbers, each once); None: all of them, in order."""
+
+    def __init__(self, n_pages, pages=None, device="cuda"):
+        if n_pages < 1:
+            raise ValueError("a pool has a page or more")
+        if pages is None:
+            pages = torch.arange(n_pages, dtype=torch.int32)
+        elif not isinstance(pages, torch.Tensor):
+            pages = torch.tensor(list(pages), dtype=torch.int32)
+        if pages.dim() != 1 or pages.dtype != torch.int32 or pages.numel() > n_pages:
+            raise ValueError("pages must be at most n_pages int32 page numbers")
+        self.n_pages = int(n_pages)
+        self.ring = torch.full((self.n_pages,), -1, dtype=torch.int32, device=device)
+        self.ring[:pages.numel()] = pages.to(self.ring.device)
+        self.state = torch.tensor([0, pages.numel(), 0], dtype=torch.int32).to(self.ring.device)
+        self.device = self.ring.device
+        self.c = kvc_free_pages(self.ring.data_ptr(), self.state.data_ptr(), self.n_pages)
+        self.addr = ctypes.addressof(self.c)
+
+    def free(self):
+        """How many pages are free, and how many were asked for and not there (waits for the device)."""
+        return tuple(self.state.tolist()[1:])
+
+
 # The calls below are made once a layer and step with a few rows, where the host's time counts: they look at each
 # attribute once and pass plain integers.  A given stream is made the current one, so that what they allocate belongs
 # to it.
@@ -492,6 +524,31 @@ def _pool(cache, pages):
     if cache.cuda != pages.device:
         raise ValueError("the pool is on %s, its pages on %s" % (cache.cuda, pages.device))
     return pages.device
+
+
+def kv_pages_advance(pages, free, rows, n_rows, row_start=None, positions=None, slots=None, stream=None):
+    """Change the lengths of pages (a PageTable) by rows (int32 [n_seq]; negative: rewound or ended), take the pages that
+    they need from free (a FreePages) and give back those that they do not: table, lengths and free are updated in
+    place.  Returns (row_start [n_seq + 1], positions [n_rows], slots [n_rows]) of the packed rows that are added."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_pages_advance(pages, free, rows, n_rows, row_start, positions, slots)
+    dev, n = pages.device, pages.n_seq
+    if free.device != dev or rows.shape != (n,) or rows.dtype != torch.int32 or rows.device != dev or \
+            not rows.is_contiguous():
+        raise ValueError("rows must be a contiguous int32 tensor [n_seq], and the free pages be, on %s" % dev)
+    row_start = _output(row_start, "row_start", (n + 1,), torch.int32, dev)
+    positions = _output(positions, "positions", (n_rows,), torch.int32, dev)
+    slots = _output(slots, "slots", (n_rows,), torch.int32, dev, positions)
+    st = _lib().kv_pages_advance(pages.addr, free.addr, rows.data_ptr(), row_start.data_ptr(), n_rows,
+                                 positions.data_ptr() or None, slots.data_ptr() or None, _on(dev))
+    if st:
+        raise KvcError(st, "kv_pages_advance")
+    if n == 0:
+        row_start.zero_()
+        positions.fill_(-1)
+        slots.fill_(-1)
+    return row_start, positions, slots
 
 
 def kv_paged_append(cache, layer, pages, row_start, k, v, stream=None):

@@ -422,6 +422,24 @@ int attn_packed(const void *q, const void *k, const void *v, int64_t ld_q, int64
     return launch_packed(a, scratch, (cudaStream_t)stream);
 }
 
+int kv_pages_advance(const kvc_pages *pages, const kvc_free_pages *free_pages, const int32_t *rows, int32_t *row_start,
+                     int32_t n_rows, int32_t *positions, int32_t *slots, kvc_stream_t stream) {
+    if (!pages || !free_pages || n_rows < 0) return KVC_EINVAL;
+    if (pages->n_seq < 0 || pages->n_seq > 65535 || pages->max_pages <= 0 || pages->page_size <= 0 ||
+        pages->page_size % 16 != 0 || (int64_t)pages->max_pages * pages->page_size > INT32_MAX)
+        return KVC_EINVAL;
+    if (free_pages->n_pages <= 0 || (int64_t)free_pages->n_pages * pages->page_size > INT32_MAX) return KVC_EINVAL;
+    if (pages->n_seq == 0) return KVC_OK;
+    if (!pages->table || !pages->len || !free_pages->ring || !free_pages->state || !rows || !row_start) return KVC_EINVAL;
+    const void *all[] = {pages->table, pages->len, free_pages->ring, free_pages->state, rows, row_start, positions, slots};
+    for (const void *p : all)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return KVC_EINVAL;
+    const AdvanceArgs a = {const_cast<int32_t *>(pages->table), const_cast<int32_t *>(pages->len), pages->n_seq,
+                           pages->max_pages, pages->page_size, free_pages->ring, free_pages->state, free_pages->n_pages,
+                           rows, row_start, n_rows, positions, slots};
+    return launch_pages_advance(a, (cudaStream_t)stream);
+}
+
 static bool rope_ok(const kvc_rope *r, int32_t head_dim, float eps) {
     if (!r || r->n_pairs < 0 || r->n_pairs > head_dim / 2) return false;
     if (r->style != KVC_ROPE_HALF && r->style != KVC_ROPE_PAIRS) return false;

@@ -106,6 +106,19 @@ struct PackedArgs {
 size_t packed_scratch_bytes(int n_rows, int n_seq, int n_head_q, int n_head_kv, int head_dim);
 int launch_packed(const PackedArgs &a, void *scratch, cudaStream_t s);
 
+// Page tables that follow the sequences' lengths.
+struct AdvanceArgs {
+    int32_t *table, *len;
+    int n_seq, max_pages, page_size;
+    int32_t *ring, *state;
+    int n_pages;
+    const int32_t *rows;
+    int32_t *starts;
+    int n_rows;
+    int32_t *pos, *slots;
+};
+int launch_pages_advance(const AdvanceArgs &a, cudaStream_t s);
+
 // Norms and rotation; STORE variants take keys and values to a pool.
 struct RopeArgs {
     const void *q, *k, *v;

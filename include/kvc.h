@@ -501,6 +501,41 @@ int attn_packed(const void *q, const void *k, const void *v, int64_t ld_q, int64
                 int32_t n_head_q, int32_t n_head_kv, int32_t head_dim, void *out, float *lse, void *scratch,
                 size_t scratch_bytes, kvc_stream_t stream);
 
+/* The free pages of a pool: a ring of n_pages cells.  state (device, three values):
+ * the cell that the ring begins with, how many pages it holds from there on, and how
+ * many pages have been asked for that were not there.  Initially the ring holds the
+ * pages that no sequence has, once each, from cell 0 on, and state is {0, their
+ * number, 0}; unused cells may hold anything. */
+typedef struct {
+    int32_t *ring;   /* device [n_pages] */
+    int32_t *state;  /* device [3] */
+    int32_t n_pages; /* of the pool: its n_ctx / page_size, at least 1 */
+} kvc_free_pages;
+
+/* Advance the sequences of a page table, on the device: sequence i's length changes by
+ * rows[i] (device [n_seq]).  rows[i] > 0: that many packed rows are to be stored (a
+ * token, a chunk, a prompt); < 0: it is rewound, or ended (a length does not fall
+ * below 0, so any number down to -2^31 ends it).
+ *   - len[i] becomes clamp(len[i] + rows[i], 0, 2^31 - 1);
+ *   - table entries that the new length needs and the old one did not take pages from the
+ *     front of the ring, in the order of sequences, in each of positions; where the ring
+ *     has none left they become -1 (a hole) and state[2] counts them;
+ *   - entries that it does not need any more give their pages back at the ring's end, in the
+ *     same order (holes give none), and become -1.  These pages can be taken by the next
+ *     call, not by this one;
+ *   - row_start (device [n_seq + 1]) receives the running sum of the rows that are added:
+ *     the row_start of kv_paged_append and the other calls on packed rows;
+ *   - positions and slots (device [n_rows], each may be null) receive each packed row's
+ *     position in its sequence and its pool position (-1 for a hole); both are -1 for rows
+ *     at or past row_start[n_seq].  No row at or past n_rows is touched.
+ * A page belongs to one sequence: a table that shares pages between sequences is not
+ * one for this call.  The call writes pages->table and pages->len.  max_pages limits a
+ * sequence's table as for the other calls (positions behind it are holes).  n_rows == 0
+ * still advances; n_seq == 0 is a no-op.  Results do not depend on timing.
+ * Errors: KVC_EINVAL (null or 4-byte-unaligned pointers, shapes). */
+int kv_pages_advance(const kvc_pages *pages, const kvc_free_pages *free_pages, const int32_t *rows, int32_t *row_start,
+                     int32_t n_rows, int32_t *positions, int32_t *slots, kvc_stream_t stream);
+
 /* A rotation by position of the first 2 * n_pairs values of each head:
  *   (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = position * frequency of the pair.
  * Pair i is values (i, i + n_pairs) (KVC_ROPE_HALF; n_pairs a multiple of 8) or
