@@ -14,7 +14,6 @@ library reports an error.
 import ctypes
 import math
 import os
-from fractions import Fraction
 
 import torch
 
@@ -24,8 +23,19 @@ LIB_PATH = os.path.join(_HERE, "libkvc.so")
 KVC_OK, KVC_EINVAL, KVC_ERANGE, KVC_ENOSPC, KVC_EFORMAT, KVC_ECUDA, KVC_EDEVICE = 0, -1, -2, -3, -4, -5, -6
 CACHE_TYPES = {"f16": 0, "q8_0": 1, "q4_0": 2}
 LAYOUTS = {"head_major": 0, "layer_major": 1}
-# 2^64 / (2 pi), to 2^-128 of itself
-_TURN = Fraction(1 << 64) / (2 * Fraction(3141592653589793238462643383279502884197, 10 ** 39))
+# 2^128 / (2 pi)
+_TURN = (10 ** 39 << 128) // (2 * 3141592653589793238462643383279502884197)
+
+
+def _turns(freq):
+    """The frequency in turns, modulo 1, as a fraction of 2^64: a signed 64-bit integer.  In integers, as a float's
+    product with 1 / (2 pi) would lose the last bits."""
+    n, d = freq.as_integer_ratio()          # d is a power of two
+    shift = 64 + d.bit_length() - 1
+    t = ((n * _TURN >> shift - 1) + 1 >> 1) & (1 << 64) - 1
+    return t - (1 << 64) if t >> 63 else t
+
+
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -678,10 +688,7 @@ class RopeTable:
             freq = [float(f) for f in inv_freq]
         if len(freq) != n or not all(math.isfinite(f) for f in freq):
             raise ValueError("inv_freq must be rot / 2 finite frequencies")
-        # 2^64 / (2 pi) times the frequency, in integers: a float's product would lose the last bits
-        turns = [round(Fraction(f) * _TURN) % (1 << 64) for f in freq]
-        turns = [t - (1 << 64) if t >= 1 << 63 else t for t in turns]
-        self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
+        self.turns = torch.tensor([_turns(f) for f in freq], dtype=torch.int64).to(device)
         self.rot, self.style, self.device = rot, style, self.turns.device
         self.c = kvc_rope(self.turns.data_ptr() if n else None, n, ROPE_STYLES[style])
         self.addr = ctypes.addressof(self.c)

@@ -27,10 +27,11 @@ namespace {
 constexpr int THREADS = 128;
 // Units that a thread takes where there are many.  Measured at the sizes above, with 1, 2 and 4 of them: a q8_0 append
 // 48.0, 42.1 and 42.6 us, an f16 append 27.7, 27.8 and 28.6; a read of a q8_0 cache, whose one load makes two stores'
-// worth of values, 56.7, 57.2 and 62.7; of an f16 cache 76.8, 71.6 and 71.8.
+// worth of values, 56.7, 57.2 and 62.7; of an f16 cache 76.8, 71.6 and 71.8.  20,500 bf16 rows into a q4_0 cache 32.5, 32.1 and 33.4; read
+// back into fp16 26.1, 29.5 and 22.8.
 constexpr int APPEND_PASSES = 2;
 template <int CT>
-constexpr int READ_PASSES = CT == KVC_Q8_0 ? 1 : 2;
+constexpr int READ_PASSES = CT == KVC_Q8_0 ? 1 : CT == KVC_Q4_0 ? 4 : 2;
 
 // n / d for 32-bit n by a multiplication: floor(n (2^64 / d + 1) / 2^64), where the part that is too much,
 // n / 2^64, is below the 1/d that would be needed to reach the next integer.
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(THREADS)
             widen8<DT>(raw[i][kv], x);
             if constexpr (CT == KVC_Q4_0) {
                 uint32_t w;
-                const uint16_t scale = q4_0_quantize_quad(x, w);
+                const uint16_t scale = q4_0_quantize_quad<DT>(x, w);
                 if (slot >= 0) {
                     *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(kv ? p.vq : p.kq) + (at >> 1)) = w;
                     if ((c & 31) == 0)

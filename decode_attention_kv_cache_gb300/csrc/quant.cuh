@@ -213,50 +213,88 @@ __device__ __forceinline__ uint16_t q8_0_quantize_quad(const float (&x)[8], uint
     return __half_as_ushort(__float2half_rn(d));
 }
 
+// The codes of eight values of a block whose greatest is m (finite, not zero): the quotient is meant exactly.  With a = |x|,
+// D = |m| / 8 and k <= a / D <= k + 1 but for an error that does not matter, the sign of the residue a - (k + 1/2) D, which
+// a fused multiply-add gives exactly, decides between k and k + 1.  As far as possible in floating point, two values at a
+// time; codes are put together as digits of base 16 in a float32, which holds four of them exactly.
+__device__ __forceinline__ void q4_0_exact8(const float (&x)[8], float m, uint32_t &word) {
+    const float am = fabsf(m);
+    const float up = am < 0x1p-100f ? 0x1p100f : 1.f;   // 1 / D and the residues stay in the normal range
+    const float D = am * up * 0.125f, turn = m > 0.f ? -up : up;   // x turn has the sign of -8 x / m
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(D));
+    const uint64_t turn2 = ptx::f2_pack(turn, turn), mz = ptx::f2_pack(-0.f, -0.f), r2 = ptx::f2_pack(r, r),
+                   D2 = ptx::f2_pack(D, D), M2 = ptx::f2_pack(12582912.f, 12582912.f),
+                   nM2 = ptx::f2_pack(-12582912.f, -12582912.f), n1 = ptx::f2_pack(-1.f, -1.f),
+                   nh = ptx::f2_pack(-0.5f, -0.5f), base = ptx::f2_pack(16.f, 16.f);
+    uint64_t digits = 0;
+#pragma unroll
+    for (int i = 6; i >= 0; i -= 2) {
+        float y0, y1, c0, c1;
+        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), turn2, mz), y0, y1);
+        const uint64_t a = ptx::f2_pack(fabsf(y0), fabsf(y1));
+        const uint64_t t = ptx::f2_add(ptx::f2_fma(a, r2, nh), M2);             // k + M
+        const uint64_t nk = ptx::f2_fma(ptx::f2_add(t, nM2), n1, nh);           // -(k + 1/2)
+        ptx::f2_unpack(ptx::f2_fma(nk, D2, a), c0, c1);                         // a - (k + 1/2) D
+        const uint64_t half = ptx::f2_pack(copysignf(0.5f, c0), copysignf(0.5f, c1));
+        ptx::f2_unpack(ptx::f2_fma(nk, n1, half), c0, c1);                      // |code|
+        c0 = fminf(copysignf(c0, y0), 7.f);
+        c1 = fminf(copysignf(c1, y1), 7.f);
+        const uint64_t code = ptx::f2_pack(c0, c1);
+        digits = i == 6 ? code : ptx::f2_fma(digits, base, code);               // even values, odd values
+    }
+    float e, o;   // plus 8 in each digit; in the low bits of 2^23
+    ptx::f2_unpack(ptx::f2_add(digits, ptx::f2_pack(8388608.f + 34952.f, 8388608.f + 34952.f)), e, o);
+    word = __byte_perm(__float_as_uint(e), __float_as_uint(o), 0x5410);
+}
+
 // q4_0: a block spread over four neighbouring lanes, eight values each; all four lanes take part.  This lane's word of
 // codes and the block's scale.
 //
 //   m = the block's value of greatest magnitude (of +m and -m the negative one), d = fp16(-m / 8),
 //   code = min(round(-8 x / m), 7), ties away from zero; a block of zeros has d = +0 and codes of zero.
-// The quotient is meant exactly: with a = |x|, D = |m| / 8 and k <= a / D <= k + 1 but for an error that does not
-// matter, the sign of the residue a - (k + 1/2) D, which a fused multiply-add gives exactly, decides between k and k + 1.
-// No branch: bf16 and fp16 inputs, whose quotients have few bits, meet ties in most warps.
+// The quotient is meant exactly (q4_0_exact8).
+// bf16 and fp16 values (DT) have few bits, p = 8 or 11: a quotient y = -8 x / m that is not a tie is 2^-(p + 2) or more away
+// from one (x, near a tie no less than m / 17, and m are multiples of units that make 8 x - (k + 1/2) m one of
+// 2^-(p + 2) |m|).  Quotients made larger by 2^-18 of themselves, 2^-15 at most, therefore round to the nearest integer
+// as the exact ones round with ties away from zero, the error of 1/m (2^-23) notwithstanding.  Their integers are the
+// low bits of 1.5 2^23 + y.
 // A word holds eight codes, value i of them, as code + 8, in the four bits from bit 16 (i % 2) + 4 (i / 2): one AND
 // with 0x000F000F << 4 (i / 2) then gives the neighbours 2 j, 2 j + 1 as the halves of a register.
 // A non-finite block (outside the method's domain) has codes of zero under a scale of infinity or NaN.
+template <int DT>
 __device__ __forceinline__ uint16_t q4_0_quantize_quad(const float (&x)[8], uint32_t &word) {
-    uint32_t key = 0u;   // magnitude, then sign: the greatest is m, by integers, which also keeps a NaN
+    float hi = ptx::max3_nan(x[0], x[1], x[2]), lo = ptx::min3_nan(x[0], x[1], x[2]);
+    hi = ptx::max3_nan(hi, x[3], x[4]);
+    lo = ptx::min3_nan(lo, x[3], x[4]);
+    hi = ptx::max3_nan(ptx::max3_nan(hi, x[5], x[6]), x[7], x[7]);
+    lo = ptx::min3_nan(ptx::min3_nan(lo, x[5], x[6]), x[7], x[7]);
+    float m = hi > -lo ? hi : lo;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) key = max(key, __funnelshift_l(__float_as_uint(x[i]), __float_as_uint(x[i]), 1));
-    key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
-    key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
-    const uint32_t mbits = __funnelshift_r(key, key, 1);
-    const float m = __uint_as_float(mbits), am = fabsf(m);
+    for (int d = 1; d < 4; d <<= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, m, d);
+        hi = ptx::max3_nan(m, o, o);
+        lo = ptx::min3_nan(m, o, o);
+        m = hi > -lo ? hi : lo;
+    }
+    const float am = fabsf(m);
     word = 0x88888888u;
-    if (am > 0.f && am <= 3.402823466e38f) {
-        const float up = am < 0x1p-100f ? 0x1p100f : 1.f;   // 1 / D and the residues stay in the normal range
-        const float D = am * up * 0.125f;
+    if (DT != KVC_IN_F32 && am >= 0x1p-100f && am <= 3.402823466e38f) {
         float r;
-        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(D));
-        const uint64_t r2 = ptx::f2_pack(r, r), D2 = ptx::f2_pack(D, D), M2 = ptx::f2_pack(12582912.f, 12582912.f),
-                       nM2 = ptx::f2_pack(-12582912.f, -12582912.f), n1 = ptx::f2_pack(-1.f, -1.f),
-                       nh = ptx::f2_pack(-0.5f, -0.5f);
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(m * -0.125f));
+        r = fmaf(r, 0x1p-18f, r);
+        word = 0u;
+        uint32_t off = 0u;   // the eights, less the floats' own bits
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const uint64_t a = ptx::f2_pack(fabsf(x[i]) * up, fabsf(x[i + 1]) * up);
-            const uint64_t t = ptx::f2_add(ptx::f2_fma(a, r2, nh), M2);                          // k + M
-            const uint64_t c = ptx::f2_fma(ptx::f2_fma(ptx::f2_add(t, nM2), n1, nh), D2, a);     // a - (k + 1/2) D
-            float t0, t1, c0, c1;
-            ptx::f2_unpack(t, t0, t1);
-            ptx::f2_unpack(c, c0, c1);
-            // -8 x / m is negative where x and m have the same sign
-            const int s0 = (int)~(__float_as_uint(x[i]) ^ mbits) >> 31, s1 = (int)~(__float_as_uint(x[i + 1]) ^ mbits) >> 31;
-            const int q0 = __float_as_int(t0) - 0x4B400000 + 1 + (__float_as_int(c0) >> 31);
-            const int q1 = __float_as_int(t1) - 0x4B400000 + 1 + (__float_as_int(c1) >> 31);
-            // adding a signed code to the 8 of its four bits gives code + 8 there and carries nowhere
-            word += (uint32_t)min((q0 ^ s0) - s0, 7) << (2 * i);
-            word += (uint32_t)min((q1 ^ s1) - s1, 7) << (16 + 2 * i);
+        for (int i = 0; i < 8; ++i) {
+            const int at = 16 * (i & 1) + 4 * (i >> 1);
+            const float t = fminf(fmaf(x[i], r, 12582912.f), 12582912.f + 7.f);
+            word += __float_as_uint(t) * (1u << at);
+            off += (8u - 0x4B400000u) << at;
         }
+        word += off;
+    } else if (am > 0.f && am <= 3.402823466e38f) {
+        q4_0_exact8(x, m, word);
     }
     return am > 0.f || am != am ? __half_as_ushort(__float2half_rn(m * -0.125f)) : (uint16_t)0;
 }

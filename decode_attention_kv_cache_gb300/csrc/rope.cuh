@@ -1,0 +1,295 @@
+// Norms of queries and keys for each head and the rotation by position, in one pass; with the keys and values stored on
+// a pool's pages in the same pass where asked.
+//
+//   y_i = x_i w_i / sqrt(mean_j x_j^2 + eps),   (a, b) -> (a cos t - b sin t, a sin t + b cos t)  for each pair,
+// so that with A_i = w_i cos t, B_i = -+ w_p sin t (p the other of the pair) and r = 1 / sqrt(..)
+//   out_i = r (x_i A_i + x_p B_i):
+// A and B are the same for all heads of a row.  A warp takes a row, or some of its heads where there are few rows: it makes
+// the sines once, keeps A and B of its values in registers and goes through the heads, two or more at a time, eight values a
+// lane, several loads in flight.  The other of a pair lies in the same lane, or its eight in another one's registers.  Only bytes
+// move: what bounds it is HBM and the 90 instructions for eight values, and for a few rows the chain position -> angle -> store.
+//
+// Angles.  A pair's frequency is a 64-bit fixed-point fraction f of a turn for each position, so that position times f, modulo
+// 2^64, is the angle's fraction of a turn to 2^-33 whatever the position; its upper 32 bits go through sincospi.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "kvc_internal.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int WARPS = 4;
+constexpr int THREADS = 32 * WARPS;
+constexpr int MAX_PAIRS = 128;
+constexpr int NO_POOL = -1;
+// Warps for an SM that a row is cut for where there are few rows.
+template <int CT>
+constexpr int WARPS_PER_SM = CT == NO_POOL ? 16 : 4;
+
+struct Args {
+    RopeArgs a;
+    int lanes_log2;        // lanes of a head: eight values each, a power of two
+    int span;              // heads that a warp takes: a multiple of those that it takes at a time
+    int heads;             // of a row: queries, keys, values (if stored)
+    float inv_d;           // 1 / D
+    // the pool, of the layer
+    PagedView pg;
+    const int32_t *row_start;
+    uint8_t *kq, *vq;
+    uint16_t *ks, *vs;
+    int64_t c_tok, c_head, s_tok, s_head;
+};
+
+template <int DT>
+__device__ __forceinline__ float weight_at(const void *w, int i) {
+    if constexpr (DT == KVC_IN_F32) return __ldg(static_cast<const float *>(w) + i);
+    else if constexpr (DT == KVC_IN_BF16) return __bfloat162float(__ldg(static_cast<const __nv_bfloat16 *>(w) + i));
+    else return __half2float(__ldg(static_cast<const __half *>(w) + i));
+}
+
+// x rounded to the type, as it lies in memory.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> narrow8(const float (&x)[8]) {
+    Raw8<DT> r;
+    if constexpr (DT == KVC_IN_F32) {
+        r.u[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        r.u[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == KVC_IN_F16) {
+                w[i] = ptx::pack_half2(x[2 * i], x[2 * i + 1]);
+            } else {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+        r.u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void store_raw8(void *base, int64_t idx, const Raw8<DT> &r) {
+    uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(base) + idx * (DT == KVC_IN_F32 ? 4 : 2));
+    p[0] = r.u[0];
+    if constexpr (DT == KVC_IN_F32) p[1] = r.u[1];
+}
+__device__ __forceinline__ uint4 shfl4(const uint4 &u, int lane) {
+    return make_uint4(__shfl_sync(0xffffffffu, u.x, lane), __shfl_sync(0xffffffffu, u.y, lane),
+                      __shfl_sync(0xffffffffu, u.z, lane), __shfl_sync(0xffffffffu, u.w, lane));
+}
+
+// CT: the pool's type, or NO_POOL.  With a pool keys and values go there, to places that the pages give, and so do the
+// positions.  LANES: those of a head where they are known (16: heads of 96 to 128), or 0.
+template <int DT, int STYLE, int CT, int LANES>
+__global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const Args p) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    constexpr bool STORE = CT != NO_POOL;
+    __shared__ float2 turned[WARPS][MAX_PAIRS];   // (cosine, sine) of each pair
+    const RopeArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x * WARPS + warp;
+    if (row >= a.n_rows) return;
+    const int lanes = 1 << p.lanes_log2, together = 32 >> p.lanes_log2;   // heads at a time
+    const int chunks = a.D >> 3, chunk = lane & (lanes - 1), grp = lane >> p.lanes_log2;
+    const int h0 = blockIdx.y * p.span, h1 = min(h0 + p.span, p.heads);
+    const bool mine = chunk < chunks;
+    const int own_chunk = min(chunk, chunks - 1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- the row's position and place
+    int pos, slot = -1;   // slot: -1 a hole, -2 a row that belongs to no sequence
+    if constexpr (STORE) {
+        const int i = find_seq_warp(p.row_start, p.pg.n_seq, row);
+        const int s0 = __ldcg(p.row_start + i), s1 = __ldcg(p.row_start + i + 1), len = max(__ldcg(p.pg.len + i), 0);
+        if (row < s0 || row >= s1) return;
+        pos = len - (s1 - row);
+        slot = page_slot(p.pg, i, pos);
+    } else {
+        pos = __ldcg(a.pos + row);
+    }
+    // ---- sines
+    for (int pair = lane; pair < a.n_pairs; pair += 32) {
+        const long long t = (long long)(__ldg(a.turns + pair) * (unsigned long long)(long long)pos);
+        float s, c;
+        sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
+        turned[warp][pair] = make_float2(c, s);
+    }
+    __syncwarp();
+    float c[8], s[8];   // of this lane's values; s with the sign of out_i's other
+    const int n8 = a.n_pairs >> 3;   // chunks of half of a rotation in halves
+    const int other_chunk = STYLE == KVC_ROPE_PAIRS ? own_chunk
+                            : chunk < n8            ? chunk + n8
+                            : chunk < 2 * n8        ? chunk - n8
+                                                    : own_chunk;
+    const int partner = (lane & ~(lanes - 1)) | (chunk < 2 * n8 ? other_chunk : chunk);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int i = own_chunk * 8 + j, n = a.n_pairs;
+        c[j] = 1.f;
+        s[j] = 0.f;
+        if (i < 2 * n) {
+            const float2 cs = turned[warp][STYLE == KVC_ROPE_PAIRS ? i >> 1 : i < n ? i : i - n];
+            c[j] = cs.x;
+            s[j] = (STYLE == KVC_ROPE_PAIRS ? (j & 1) == 0 : i < n) ? -cs.y : cs.y;
+        }
+    }
+
+    // Heads [first, last) of one kind: queries (0), keys (1), values (2).
+    auto heads_of = [&](auto kind_tag, int first, int last) {
+        constexpr int KIND = decltype(kind_tag)::value;
+        constexpr int BATCH = KIND == 0 || !STORE ? (DT == KVC_IN_F32 ? 4 : 6) : 4;   // loads of a lane in flight
+        if (first >= last) return;
+        float A[8], B[8];
+        const void *w = KIND == 0 ? a.q_weight : a.k_weight;
+        const bool normed = KIND < 2 && w != nullptr;
+        const void *src = KIND == 0 ? a.q : KIND == 1 ? a.k : a.v;
+        const int64_t src0 = row * (KIND == 0 ? a.ld_q : KIND == 1 ? a.ld_k : a.ld_v) + 8 * own_chunk;
+        for (int base = first; base < last; base += BATCH * together) {
+            Raw8<DT> raw[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int h = base + i * together + grp;
+                raw[i] = Raw8<DT>{};
+                if (h < last && mine) raw[i] = load_raw8<DT>(src, src0 + h * a.D);
+            }
+            if (KIND < 2 && base == first) {
+                if (normed) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {   // weights may lie on any boundary of their type
+                        A[j] = weight_at<DT>(w, own_chunk * 8 + j) * c[j];
+                        B[j] = weight_at<DT>(w, other_chunk * 8 + (STYLE == KVC_ROPE_PAIRS ? j ^ 1 : j)) * s[j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) { A[j] = c[j]; B[j] = s[j]; }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                if (base + i * together >= last) break;
+                const int h = base + i * together + grp;
+                const bool some = h < last && mine;
+                float x[8];
+                widen8<DT>(raw[i], x);
+                Raw8<DT> out = raw[i];
+                if constexpr (KIND < 2) {
+                    float y[8];
+                    if constexpr (STYLE == KVC_ROPE_HALF) {
+                        Raw8<DT> other;
+                        other.u[0] = shfl4(raw[i].u[0], partner);
+                        if constexpr (DT == KVC_IN_F32) other.u[1] = shfl4(raw[i].u[1], partner);
+                        widen8<DT>(other, y);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+                    }
+                    float inv = 1.f;
+                    if (normed) {
+                        float ss = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+                        if constexpr (LANES == 0) {
+                            for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                        } else {
+#pragma unroll
+                            for (int o = LANES >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                        }
+                        inv = rsqrtf(fmaf(ss, p.inv_d, a.eps));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = inv * fmaf(x[j], A[j], y[j] * B[j]);
+                    out = narrow8<DT>(x);
+                }
+                if constexpr (KIND == 0) {
+                    if (some) store_raw8<DT>(a.q_out, row * a.ld_qo + h * a.D + 8 * chunk, out);
+                } else if constexpr (!STORE) {
+                    if (some) store_raw8<DT>(a.k_out, row * a.ld_ko + h * a.D + 8 * chunk, out);
+                } else {
+                    // as kv_paged_append stores a row of these
+                    if constexpr (KIND == 1) widen8<DT>(out, x);
+                    const int e = 8 * chunk;
+                    const int64_t at = slot * p.c_tok + h * p.c_head + e, sat = slot * p.s_tok + h * p.s_head + (e >> 5);
+                    uint8_t *codes = KIND == 2 ? p.vq : p.kq;
+                    uint16_t *scales = KIND == 2 ? p.vs : p.ks;
+                    if constexpr (CT == KVC_F16) {
+                        uint32_t w4[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w4[j] = ptx::pack_half2(x[2 * j], x[2 * j + 1]);
+                        if (some) *reinterpret_cast<uint4 *>(codes + 2 * at) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                    } else if constexpr (CT == KVC_Q8_0) {
+                        uint32_t w2[2];
+                        const uint16_t d = q8_0_quantize_quad(x, w2);
+                        if (some) {
+                            *reinterpret_cast<uint2 *>(codes + at) = make_uint2(w2[0], w2[1]);
+                            if ((e & 31) == 0) scales[sat] = d;
+                        }
+                    } else {
+                        uint32_t w1;
+                        const uint16_t d = q4_0_quantize_quad<DT>(x, w1);
+                        if (some) {
+                            *reinterpret_cast<uint32_t *>(codes + (at >> 1)) = w1;
+                            if ((e & 31) == 0) scales[sat] = d;
+                        }
+                    }
+                }
+            }
+        }
+    };
+    const int h_k = a.H_q, h_v = a.H_q + a.H_kv;
+    heads_of(std::integral_constant<int, 0>{}, h0, min(h1, h_k));
+    if (!STORE || slot >= 0) {
+        heads_of(std::integral_constant<int, 1>{}, max(h0, h_k) - h_k, min(h1, h_v) - h_k);
+        if constexpr (STORE) heads_of(std::integral_constant<int, 2>{}, max(h0, h_v) - h_v, h1 - h_v);
+    }
+}
+
+template <int DT, int STYLE, int CT>
+int launch_t(const Args &p, dim3 grid, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, p.lanes_log2 == 4 ? qk_norm_rope_kernel<DT, STYLE, CT, 16> : qk_norm_rope_kernel<DT, STYLE, CT, 0>, p) != cudaSuccess) return KVC_ECUDA;
+    return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ECUDA;
+}
+
+template <int CT>
+int launch_all(Args p, cudaStream_t s) {
+    const int chunks = p.a.D / 8;
+    p.inv_d = 1.f / p.a.D;
+    p.lanes_log2 = 2;
+    while ((1 << p.lanes_log2) < chunks) ++p.lanes_log2;
+    p.heads = p.a.H_q + p.a.H_kv * (CT != NO_POOL ? 2 : 1);
+    // Whole rows for a warp where there are enough of them to keep the SMs busy; else as many warps for a row as that takes.
+    const int together = 32 >> p.lanes_log2, times = (p.heads + together - 1) / together;
+    const int want = (WARPS_PER_SM<CT> * sm_count() + p.a.n_rows - 1) / p.a.n_rows, parts = want < times ? want : times;
+    p.span = (times + parts - 1) / parts * together;
+    const dim3 grid((p.a.n_rows + WARPS - 1) / WARPS, (p.heads + p.span - 1) / p.span);
+    switch (p.a.dtype * 2 + p.a.style) {
+        case KVC_IN_F32 * 2: return launch_t<KVC_IN_F32, KVC_ROPE_HALF, CT>(p, grid, s);
+        case KVC_IN_F32 * 2 + 1: return launch_t<KVC_IN_F32, KVC_ROPE_PAIRS, CT>(p, grid, s);
+        case KVC_IN_BF16 * 2: return launch_t<KVC_IN_BF16, KVC_ROPE_HALF, CT>(p, grid, s);
+        case KVC_IN_BF16 * 2 + 1: return launch_t<KVC_IN_BF16, KVC_ROPE_PAIRS, CT>(p, grid, s);
+        case KVC_IN_F16 * 2: return launch_t<KVC_IN_F16, KVC_ROPE_HALF, CT>(p, grid, s);
+        case KVC_IN_F16 * 2 + 1: return launch_t<KVC_IN_F16, KVC_ROPE_PAIRS, CT>(p, grid, s);
+        default: return KVC_EINVAL;
+    }
+}
+
+}  // namespace
+}  // namespace kvc
