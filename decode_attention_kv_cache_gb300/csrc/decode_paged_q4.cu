@@ -87,13 +87,31 @@ __device__ __forceinline__ __half inverse_above(__half d) {
     return __ushort_as_half((unsigned short)(e < 29 ? (29 - e) << 10 : 0x200 >> (e - 29)));
 }
 
-// Eight consecutive values of q, as float32.
+// A lane's values of the group's queries, eight of each block, as they lie in memory.
+template <int D, int DT, int NT>
+struct RawQueries {
+    uint4 u[NT][D / 32][DT == KVC_IN_F32 ? 2 : 1];
+};
+template <int D, int DT, int NT>
+__device__ __forceinline__ void read_queries(const uint8_t *q, int G, int lane, RawQueries<D, DT, NT> &raw) {
+    constexpr int ESZ = DT == KVC_IN_F32 ? 4 : 2;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int head = nt * 8 + (lane >> 2);
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+            const uint4 *at = reinterpret_cast<const uint4 *>(q + (head * D + 32 * b + 8 * (lane & 3)) * ESZ);
+#pragma unroll
+            for (int i = 0; i < (DT == KVC_IN_F32 ? 2 : 1); ++i) raw.u[nt][b][i] = head < G ? __ldcg(at + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
 template <int DT>
-__device__ __forceinline__ void load_q(const uint8_t *at, float (&v)[8]) {
-    const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(at));
+__device__ __forceinline__ void widen_q(const uint4 *u, float (&v)[8]) {
+    const uint4 x = u[0];
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     if constexpr (DT == KVC_IN_F32) {
-        const uint4 y = __ldcg(reinterpret_cast<const uint4 *>(at) + 1);
+        const uint4 y = u[1];
         const uint32_t z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) { v[i] = __uint_as_float(w[i]); v[4 + i] = __uint_as_float(z[i]); }
@@ -112,20 +130,15 @@ __device__ __forceinline__ void load_q(const uint8_t *at, float (&v)[8]) {
 // magnitude from 2^-100 to 2^100 keeps its 11 bits.  eights: the second operand of the product that the scores begin
 // with, worth: what this lane's two columns' products are worth in powers of two.
 template <int D, int DT, int NT>
-__device__ __forceinline__ void load_queries(const uint8_t *q, int G, float scale_log2, int lane, uint32_t (&qf)[D / 16][NT][2],
-                                             uint32_t (&eights)[NT], float (&worth)[NT][2]) {
-    const int g = lane >> 2, t4 = lane & 3;
-    constexpr int ESZ = DT == KVC_IN_F32 ? 4 : 2, NB = D / 32;
+__device__ __forceinline__ void make_queries(const RawQueries<D, DT, NT> &raw, float scale_log2, int lane,
+                                             uint32_t (&qf)[D / 16][NT][2], uint32_t (&eights)[NT], float (&worth)[NT][2]) {
+    const int t4 = lane & 3;
+    constexpr int NB = D / 32;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int head = nt * 8 + g;
         float v[NB][8], most = 0.f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[b][i] = 0.f;
-            if (head < G) load_q<DT>(q + (head * D + 32 * b + 8 * t4) * ESZ, v[b]);
-        }
+        for (int b = 0; b < NB; ++b) widen_q<DT>(raw.u[nt][b], v[b]);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -341,7 +354,8 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
 // Where the layer's codes and scales lie; distances in bytes.
 struct Codes {
     const uint8_t *k, *sk;
-    int64_t v_from_k, sv_from_sk, tok, rows, head, s_tok, s_head;   // rows: of the rows that a warp copies together
+    int64_t v_from_k, sv_from_sk, head, s_head;
+    uint32_t tok, rows, s_tok;   // rows: of the rows that a warp copies together
 };
 
 // A warp's way through its run of the list: groups of kv heads, in each the sequences, in each its units.  Kept in shared
@@ -353,16 +367,20 @@ struct Way {
     Piece piece;                 // h: the group
 };
 
-__device__ __forceinline__ void look(Way *w, const PagedView &pg, int seq, int lane) {
+// keys_of, from the CTA's copy of the lengths where it has them all.
+__device__ __forceinline__ int keys_at(const PagedView &pg, const int *all, int i) {
+    return pg.n_seq <= THREADS ? all[i] : keys_of(pg, i);
+}
+__device__ __forceinline__ void look(Way *w, const PagedView &pg, const int *all, int seq, int lane) {
     __syncwarp();
-    w->held[lane] = seq + lane < pg.n_seq ? keys_of(pg, seq + lane) : 0;
+    w->held[lane] = seq + lane < pg.n_seq ? keys_at(pg, all, seq + lane) : 0;
     if (lane == 0) w->base = seq;
     __syncwarp();
 }
 // Both of a warp's ways (one asks for tiles, one attends) from the start of its run.
-__device__ __forceinline__ void start(Way *w, Way *v, const PagedView &pg, int seq, int group, int x, unsigned long long left,
-                                      int lane) {
-    const int held = seq + lane < pg.n_seq ? keys_of(pg, seq + lane) : 0;
+__device__ __forceinline__ void start(Way *w, Way *v, const PagedView &pg, const int *all, int seq, int group, int x,
+                                      unsigned long long left, int lane) {
+    const int held = seq + lane < pg.n_seq ? keys_at(pg, all, seq + lane) : 0;
     if (lane < 2) {
         Way *t = lane == 0 ? w : v;
         t->left = left;
@@ -378,14 +396,14 @@ __device__ __forceinline__ unsigned long long div64(unsigned long long a, unsign
     return (a | b) >> 32 ? a / b : (unsigned)a / (unsigned)b;
 }
 // The next piece into w->piece; false: there is none.
-__device__ __noinline__ bool next(Way *w, const PagedView &pg, int groups, int lane) {
+__device__ __noinline__ bool next(Way *w, const PagedView &pg, const int *lengths, int groups, int lane) {
     unsigned long long left = w->left;
     int seq = w->seq, group = w->group, x = w->x, base = w->base;
     Piece p = {0, 0, 0, 0, 0, 0};
     bool found = false;
     while (!found && left > 0 && group < groups) {
         if (seq - base >= 32 || seq < base) {
-            look(w, pg, seq, lane);
+            look(w, pg, lengths, seq, lane);
             base = seq;
         }
         const int keys = w->held[seq - base], all = units_of<KT, PIECE_COST>(keys);
@@ -437,6 +455,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     __shared__ unsigned long long warp_units[WARPS];
     __shared__ int first_seq[WARPS], rest[WARPS];
     __shared__ Way ways[WARPS][2];
+    __shared__ int lengths[THREADS];   // of all sequences, where they are so few
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -451,7 +470,11 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
         const int per = (pg.n_seq + THREADS - 1) / THREADS;
         const int i0 = min((int)threadIdx.x * per, pg.n_seq), i1 = min(i0 + per, pg.n_seq);
         unsigned long long mine = 0;
-        for (int i = i0; i < i1; ++i) mine += units_of<KT, PIECE_COST>(keys_of(pg, i));
+        for (int i = i0; i < i1; ++i) {
+            const int keys = keys_of(pg, i);
+            mine += units_of<KT, PIECE_COST>(keys);
+            if (per == 1) lengths[i] = keys;
+        }
         unsigned long long sum = mine;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
@@ -497,7 +520,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     {
         const unsigned long long u0 = run_from(run), u1 = run_from(run + 1);
         const bool some = u1 > u0;
-        start(ahead, way, pg, some ? first_seq[warp] : 0, some ? (int)(div64(u0, total)) : 0, some ? rest[warp] : 0, u1 - u0, lane);
+        start(ahead, way, pg, lengths, some ? first_seq[warp] : 0, some ? (int)(div64(u0, total)) : 0, some ? rest[warp] : 0, u1 - u0, lane);
     }
     const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
     const int g = lane >> 2, t4 = lane & 3;
@@ -510,27 +533,29 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     const uint8_t *my_code = codes.k, *my_scale = codes.sk;              // row and chunk, key, from the pool's start on
     const int q_bytes = a.G * D * (DT == KVC_IN_F32 ? 4 : 2);            // a group's queries
     int ta = 0, ta_end = 0, keys = 0, chunk = 0;        // of the piece that tiles are asked for of
-    int slot = -1, slot_next = -1;                      // lane i's: of the i-th subtile from tile `chunk` on (-1: a hole)
+    int slot = -1, page_next = -1;                      // lane i's: of the i-th subtile from tile `chunk` on (-1: a hole); its
+                                                        // page 16 tiles later, which is not looked at before
     bool rest_of_run = true;
     int stage_in = 0, stage_out = 0;
     uint32_t exists = 0;                                // lane s: a bit for each key of the tile in stage s
-    auto look_up = [&](int tile, int seq) {
-        const int key = tile * KT + lane * 16;
-        const int lp = key / pg.page_size;
-        const int page = (unsigned)key < (unsigned)keys ? __ldcg(pg.table + (int64_t)seq * pg.max_pages + lp) : -1;
-        return (unsigned)page < (unsigned)pg.n_pages ? page * pg.page_size + (key - lp * pg.page_size) : -1;
+    auto page_of = [&](int tile, int seq) {
+        const unsigned key = (unsigned)tile * KT + lane * 16;
+        return key < (unsigned)keys ? __ldcg(pg.table + (int64_t)seq * pg.max_pages + key / (unsigned)pg.page_size) : -1;
+    };
+    auto slot_in = [&](int page, int tile) {
+        return (unsigned)page < (unsigned)pg.n_pages ? page * pg.page_size + (int)(((unsigned)tile * KT + lane * 16) % (unsigned)pg.page_size) : -1;
     };
     auto ask = [&]() {
         if (rest_of_run && ta >= ta_end) {
-            rest_of_run = next(ahead, pg, groups, lane);
+            rest_of_run = next(ahead, pg, lengths, groups, lane);
             if (rest_of_run) {
                 const Piece p = ahead->piece;
                 const int h = p.h * a.step + member;
                 ta = chunk = p.t0;
                 ta_end = p.t1;
                 keys = p.keys;
-                slot = look_up(chunk, p.seq);
-                slot_next = look_up(chunk + 16, p.seq);
+                slot = slot_in(page_of(chunk, p.seq), chunk);
+                page_next = page_of(chunk + 16, p.seq);
                 my_code = codes.k + my_row * codes.tok + h * codes.head + my_chunk * 16;
                 my_scale = codes.sk + (lane & 15) * codes.s_tok + h * codes.s_head;
             }
@@ -538,15 +563,15 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
         if (rest_of_run) {
             if (ta - chunk == 16) {
                 chunk = ta;
-                slot = slot_next;
-                slot_next = look_up(chunk + 16, ahead->piece.seq);
+                slot = slot_in(page_next, chunk);
+                page_next = page_of(chunk + 16, ahead->piece.seq);
             }
             const uint32_t kt = ring + stage_in * C::STAGE, place = kt + my_place;
             const int sl[2] = {__shfl_sync(0xffffffffu, slot, 2 * (ta - chunk)), __shfl_sync(0xffffffffu, slot, 2 * (ta - chunk) + 1)};
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 if (sl[u] < 0) continue;   // what the stage held stays: nothing of it counts
-                const uint8_t *k = my_code + sl[u] * codes.tok, *v = k + codes.v_from_k;
+                const uint8_t *k = my_code + (uint64_t)(uint32_t)sl[u] * codes.tok, *v = k + codes.v_from_k;
 #pragma unroll
                 for (int r = 0; r < 16; r += C::RPL) {
                     copy16(place + (16 * u + r) * C::ROW, k);
@@ -557,7 +582,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
             }
             const int mine = lane < 16 ? sl[0] : sl[1];   // a key for each lane: its scales
             const bool valid = mine >= 0 && lane < keys - ta * KT;
-            const uint8_t *k = my_scale + max(mine, 0) * codes.s_tok;
+            const uint8_t *k = my_scale + (uint64_t)(uint32_t)max(mine, 0) * codes.s_tok;
             const uint32_t sc = kt + 2 * C::TILE + lane * C::NB * 2;
             copy_scales<C::NB * 2>(sc, k, valid);
             copy_scales<C::NB * 2>(sc + C::SC, k + codes.sv_from_sk, valid);
@@ -568,6 +593,14 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
         }
         copies_end_group();   // one for each call, so that the oldest is always NS - 1 before the newest
     };
+    // the first piece's queries are on their way while its pages are looked up
+    RawQueries<D, DT, NT> raw;
+    auto read = [&]() {
+        read_queries<D, DT, NT>(a.q + way->piece.seq * a.ld_q + (way->piece.h * a.step + member) * (int64_t)q_bytes, a.G, lane, raw);
+    };
+    constexpr bool EARLY = NT == 1;   // else the registers are not there
+    bool some = next(way, pg, lengths, groups, lane);
+    if (EARLY && some) read();
     for (int i = 0; i < C::NS; ++i) ask();
 
     // sequences without keys have no unit in the list
@@ -580,10 +613,11 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
             for (int e = threadIdx.x; e < a.H_kv; e += THREADS) a.desc[e * pg.n_seq + i] = make_int4(0, 0, 0, 0);
     }
 
-    while (next(way, pg, groups, lane)) {
+    for (bool first = true; some; some = next(way, pg, lengths, groups, lane), first = false) {
+        if (!EARLY || !first) read();
         uint32_t qf[D / 16][NT][2], eights[NT];
         float worth[NT][2];
-        load_queries<D, DT, NT>(a.q + way->piece.seq * a.ld_q + (way->piece.h * a.step + member) * (int64_t)q_bytes, a.G, a.scale_log2, lane, qf, eights, worth);
+        make_queries<D, DT, NT>(raw, a.scale_log2, lane, qf, eights, worth);
         float o[C::MT][NT][4], ob[C::NB][NT][4], m[NT][2], l[NT][2];
         __half2 inv[C::NB / 2];
 #pragma unroll
@@ -720,7 +754,8 @@ int launch_decode_paged_q4(const kvc_cache &c, const kvc_pages &p, int layer, in
     const int64_t code = layer * g.c_layer / 2, scale = layer * g.s_layer * 2;
     const uint8_t *k = static_cast<const uint8_t *>(c.k_q), *v = static_cast<const uint8_t *>(c.v_q);
     const uint8_t *sk = static_cast<const uint8_t *>(c.k_s), *sv = static_cast<const uint8_t *>(c.v_s);
-    const Codes codes = {k + code, sk + scale, v - k, sv - sk, g.c_tok / 2, g.c_tok / 2 * (1024 / c.d.head_dim), g.c_head / 2, g.s_tok * 2, g.s_head * 2};
+    const Codes codes = {k + code, sk + scale, v - k, sv - sk, g.c_head / 2, g.s_head * 2, (uint32_t)(g.c_tok / 2),
+                         (uint32_t)(g.c_tok / 2 * (1024 / c.d.head_dim)), (uint32_t)(g.s_tok * 2)};
     const PagedView pg = paged_view(c, p);
     return c.d.head_dim == 128 ? launch_d<128>(dtype, pg, a, codes, s) : launch_d<64>(dtype, pg, a, codes, s);
 }
