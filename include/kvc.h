@@ -464,7 +464,13 @@ int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_
  * Computed as decode_attn (fp16 products of q and the values, float32
  * accumulation and softmax; |q| up to 65504), then rounded once to `dtype`.
  * Softmax numerators enter the second product as fp16 and count down to 2^-31
- * of the greatest.  out and lse overlap no
+ * of the greatest.  In a q4_0 pool the codes enter the products exactly; q is
+ * first scaled by a power of two for each head and keeps 11 bits of every value
+ * down to 2^-24 of the head's greatest, which may be 2^-100 to 2^100 in magnitude;
+ * numerators enter times V's scales, as fp16, and count down to 2^-31 of the
+ * greatest numerator times the greatest scale that the sequence has in that block of
+ * 32 dimensions; scaled scores below -6e29 count as none.
+ * out and lse overlap no
  * input.  head_dim 64 or 128, n_head_q / n_head_kv <= 16.  Errors as kv_paged_append, KVC_ENOSPC (scratch too small). */
 int decode_attn_paged(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const void *q, int64_t ld_q,
                       int32_t dtype, int32_t n_head_q, void *out, float *lse, void *scratch, size_t scratch_bytes,
@@ -596,7 +602,8 @@ int kvc_device_status(int32_t *status);
  * satisfy in the next launch of the chosen tensor-core kernel on any device:
  * which = KVC_TEST_PREFILL (the prefill attention pass, head_dim 64 or 128),
  * KVC_TEST_DECODE (the decode split pass for head_dim 128), KVC_TEST_PAGED
- * (decode_attn_paged) or KVC_TEST_PACKED (attn_packed).  In that launch the
+ * (decode_attn_paged; over a q4_0 pool it has no wait that could run out, and the
+ * arm stays for the next launch that does) or KVC_TEST_PACKED (attn_packed).  In that launch the
  * thread that issues the MMAs waits on a barrier nothing arrives at, in place
  * of its first wait for a softmax tile (decode_attn_paged: a consumer warp, in
  * front of its first tile); after limit_ns the wait gives up, as
