@@ -78,6 +78,45 @@ def test_matches_64_bits(kvc, dtype, rows, hq, hkv, d, rot, style, base, far):
             check(got, *expect(x, pos, rot, style, w, freqs(rot, base), 1e-5), "%s %s" % (dtype, w is not None))
 
 
+WHOLE = [  # heads that rotate whole, not at all, or in neighbours: dtype, rows, hq, hkv, d, rot, style
+    ("bf16", 300, 6, 2, 256, 256, "half"),
+    ("f16", 257, 11, 3, 64, 64, "half"),
+    ("f32", 100, 3, 1, 128, 0, "half"),
+    ("f16", 65, 1, 1, 128, 40, "pairs"),
+    ("bf16", 2500, 13, 5, 128, 128, "half"),
+    ("f32", 2500, 21, 1, 64, 64, "half"),
+]
+
+
+@pytest.mark.parametrize("dtype,rows,hq,hkv,d,rot,style", WHOLE)
+def test_heads_that_rotate_whole(kvc, dtype, rows, hq, hkv, d, rot, style):
+    test_matches_64_bits(kvc, dtype, rows, hq, hkv, d, rot, style, 2e4, 9000)
+
+
+@pytest.mark.parametrize("dtype,d,rot", [("bf16", 128, 128), ("f32", 64, 64), ("f16", 96, 48)])
+def test_weights_on_any_boundary_of_their_type(kvc, dtype, d, rot):
+    t = TYPES[dtype]
+    q, k = inputs((33, 5, d), t, 1), inputs((33, 2, d), t, 2)
+    w = (1 + inputs((2 * d,), torch.float32, 3, 0.3)).to(t)
+    pos, rope = torch.arange(33, device="cuda", dtype=torch.int32) * 7, kvc.RopeTable(rot)
+    for at in (1, 3, d - 1):
+        part = w[at:at + d]
+        got = kvc.qk_norm_rope(q, k, pos, rope, part, part)
+        want = kvc.qk_norm_rope(q, k, pos, rope, part.clone(), part.clone())
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), at
+
+
+def test_weights_that_the_kernel_before_wrote(kvc):
+    q, k = inputs((2000, 8, 128), torch.bfloat16, 1), inputs((2000, 2, 128), torch.bfloat16, 2)
+    w = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    pos, rope = torch.arange(2000, device="cuda", dtype=torch.int32), kvc.RopeTable(128)
+    one = kvc.qk_norm_rope(q, k, pos, rope, w, w)
+    for x in (2.0, 0.5, 4.0, 1.0):      # powers of two: the outputs scale exactly
+        w.fill_(x)
+        got = kvc.qk_norm_rope(q, k, pos, rope, w, w)
+        assert all(torch.equal(a, b * x) for a, b in zip(got, one)), x
+
+
 def test_far_and_negative_positions(kvc):
     # reference angles by exact integers: the fraction of a turn, from 300 bits of pi
     from fractions import Fraction
@@ -149,6 +188,10 @@ STORES = [  # cache, layout, dtype, hq, hkv, d, page, held, rows, rot, style
     ("q8_0", "head_major", "bf16", 40, 8, 128, 64, [2500, 700], [2500, 700], 128, "half"),
     ("f16", "layer_major", "f32", 3, 3, 256, 16, [500], [37], 128, "pairs"),
     ("q4_0", "head_major", "f16", 7, 2, 32, 16, [333, 1], [333, 1], 32, "half"),
+    ("q8_0", "layer_major", "f32", 5, 3, 64, 32, [700, 33], [700, 1], 64, "half"),
+    ("q4_0", "layer_major", "f32", 6, 2, 128, 16, [90, 2600], [3, 2600], 50, "pairs"),
+    ("q4_0", "head_major", "bf16", 11, 11, 256, 64, [130, 0, 64], [130, 0, 1], 256, "half"),
+    ("f16", "head_major", "f16", 1, 1, 64, 16, [1, 2, 3], [1, 2, 3], 0, "half"),
 ]
 
 
