@@ -377,19 +377,15 @@ __device__ __forceinline__ void look(Way *w, const PagedView &pg, const int *all
     if (lane == 0) w->base = seq;
     __syncwarp();
 }
-// Both of a warp's ways (one asks for tiles, one attends) from the start of its run.
-__device__ __forceinline__ void start(Way *w, Way *v, const PagedView &pg, const int *all, int seq, int group, int x,
-                                      unsigned long long left, int lane) {
-    const int held = seq + lane < pg.n_seq ? keys_at(pg, all, seq + lane) : 0;
-    if (lane < 2) {
-        Way *t = lane == 0 ? w : v;
-        t->left = left;
-        t->seq = t->base = seq;
-        t->group = group;
-        t->x = x;
+__device__ __forceinline__ void start(Way *w, const PagedView &pg, const int *all, int seq, int group, int x, unsigned long long left,
+                                      int lane) {
+    if (lane == 0) {
+        w->left = left;
+        w->seq = seq;
+        w->group = group;
+        w->x = x;
     }
-    w->held[lane] = v->held[lane] = held;
-    __syncwarp();
+    look(w, pg, all, seq, lane);
 }
 // In 32 bits where that is enough: 64-bit divisions take some hundred cycles each.
 __device__ __forceinline__ unsigned long long div64(unsigned long long a, unsigned long long b) {
@@ -452,22 +448,21 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     decode_paged_q4_kernel(const PagedView pg, const Args a, const Codes codes) {
     using C = Cfg<D, DT, NT>;
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ unsigned long long warp_units[WARPS];
-    __shared__ int first_seq[WARPS], rest[WARPS];
+    __shared__ unsigned long long warp_units[WARPS], units_before[THREADS];
     __shared__ Way ways[WARPS][2];
     __shared__ int lengths[THREADS];   // of all sequences, where they are so few
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
-    // ---- where the warps' runs of the list start: a.step warps take the heads of a group in one run
+    // ---- where the warp's run of the list starts: a.step warps take the heads of a group in one run
     const int groups = a.H_kv / a.step;
-    unsigned long long W = 0, each = 0;   // the list's units, of them the most that every run has
-    unsigned runs = 0, more = 0;          // runs that have units, units left: floor(W r / runs) = each r + floor(more r / runs)
-    auto run_from = [&](unsigned run) { return run >= runs ? W : each * run + more * run / runs; };
-    unsigned long long total = 0;
+    const int c = blockIdx.x * WARPS + warp, member = warp % a.step;   // my slot, my head of a group
+    const unsigned run = c / a.step;
+    Way *ahead = &ways[warp][0], *way = &ways[warp][1];
+    // each thread takes `per` sequences: the units before its own, in its warp
+    const int per = (pg.n_seq + THREADS - 1) / THREADS;
     {
-        const int per = (pg.n_seq + THREADS - 1) / THREADS;
         const int i0 = min((int)threadIdx.x * per, pg.n_seq), i1 = min(i0 + per, pg.n_seq);
         unsigned long long mine = 0;
         for (int i = i0; i < i1; ++i) {
@@ -482,45 +477,68 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
             if (lane >= x) sum += up;
         }
         if (lane == 31) warp_units[warp] = sum;
-        __syncthreads();
-        unsigned long long before = sum - mine;
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) before += warp_units[w];
-            total += warp_units[w];
-        }
-        W = total * groups;
-        runs = (unsigned)min((unsigned long long)(a.n_slots / a.step), W);
-        if (runs > 0) {
-            each = div64(W, runs);
-            more = (unsigned)(W - each * runs);
-        }
-        for (int w = 0; w < WARPS; w += a.step) {
-            const unsigned run = (blockIdx.x * WARPS + w) / a.step;
-            const unsigned long long u = run_from(run);
-            unsigned long long r = total ? u - div64(u, total) * total : 0;
-            if (r >= before && r < before + mine) {
-                r -= before;
-                int i = i0;
-                for (; i + 1 < i1; ++i) {
-                    const unsigned long long n = units_of<KT, PIECE_COST>(keys_of(pg, i));
-                    if (r < n) break;
-                    r -= n;
-                }
-                for (int e = 0; e < a.step; ++e) {
-                    first_seq[w + e] = i;
-                    rest[w + e] = (int)r;
-                }
-            }
-        }
-        __syncthreads();
+        units_before[threadIdx.x] = sum - mine;
     }
-    const int c = blockIdx.x * WARPS + warp, member = warp % a.step;   // my slot, my head of a group
-    const unsigned run = c / a.step;
-    Way *ahead = &ways[warp][0], *way = &ways[warp][1];
-    {
-        const unsigned long long u0 = run_from(run), u1 = run_from(run + 1);
-        const bool some = u1 > u0;
-        start(ahead, way, pg, lengths, some ? first_seq[warp] : 0, some ? (int)(div64(u0, total)) : 0, some ? rest[warp] : 0, u1 - u0, lane);
+    __syncthreads();
+    unsigned long long total = 0;   // a group's units
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) total += warp_units[w];
+    // The list's W units in runs: each of them has `each` units, the first `more` one more.
+    const unsigned long long W = total * groups;
+    const unsigned runs = (unsigned)min((unsigned long long)(a.n_slots / a.step), W);
+    const unsigned long long each = runs > 0 ? div64(W, runs) : 0;
+    const unsigned more = (unsigned)(W - each * runs);
+    auto run_from = [&](unsigned r) { return r >= runs ? W : each * r + min(r, more); };
+    auto run_of = [&](unsigned long long unit) {
+        const unsigned long long longer = (each + 1) * more;
+        return (unsigned)(unit < longer ? div64(unit, each + 1) : more + div64(unit - longer, each));
+    };
+    if (run < runs) {
+        unsigned long long u = run_from(run);
+        const unsigned long long left = run_from(run + 1) - u;
+        int group = 0;
+        if (groups > 8) {
+            group = (int)div64(u, total);
+            u -= group * total;
+        } else {
+            for (; u >= total; ++group) u -= total;
+        }
+        // the last thread that has no more units before it
+        int t = -1;
+        unsigned long long before = 0, at = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const int n = __popc(__ballot_sync(0xffffffffu, before + units_before[32 * w + lane] <= u));
+            if (n > 0) {
+                t = 32 * w + n - 1;
+                at = before + units_before[t];
+            }
+            before += warp_units[w];
+        }
+        u -= at;
+        int seq = t * per;
+        if (per > 1)   // and of its sequences
+            for (; seq < pg.n_seq; seq += 32) {
+                const unsigned own = seq + lane < pg.n_seq ? units_of<KT, PIECE_COST>(keys_of(pg, seq + lane)) : 0;
+                unsigned sum = own;
+#pragma unroll
+                for (int x = 1; x < 32; x <<= 1) {
+                    const unsigned up = __shfl_up_sync(0xffffffffu, sum, x);
+                    if (lane >= x) sum += up;
+                }
+                const unsigned all = __shfl_sync(0xffffffffu, sum, 31);
+                if (u >= all) {
+                    u -= all;
+                    continue;
+                }
+                const int n = __popc(__ballot_sync(0xffffffffu, sum <= u));   // of 32 that lie before
+                u -= __shfl_sync(0xffffffffu, sum - own, n);
+                seq += n;
+                break;
+            }
+        start(ahead, pg, lengths, min(seq, pg.n_seq - 1), group, (int)u, left, lane);
+    } else {
+        start(ahead, pg, lengths, 0, 0, 0, 0, lane);
     }
     const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
     const int g = lane >> 2, t4 = lane & 3;
@@ -535,7 +553,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     int ta = 0, ta_end = 0, keys = 0, chunk = 0;        // of the piece that tiles are asked for of
     int slot = -1, page_next = -1;                      // lane i's: of the i-th subtile from tile `chunk` on (-1: a hole); its
                                                         // page 16 tiles later, which is not looked at before
-    bool rest_of_run = true;
+    bool rest_of_run;
     int stage_in = 0, stage_out = 0;
     uint32_t exists = 0;                                // lane s: a bit for each key of the tile in stage s
     auto page_of = [&](int tile, int seq) {
@@ -545,20 +563,22 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     auto slot_in = [&](int page, int tile) {
         return (unsigned)page < (unsigned)pg.n_pages ? page * pg.page_size + (int)(((unsigned)tile * KT + lane * 16) % (unsigned)pg.page_size) : -1;
     };
+    auto begin_piece = [&]() {
+        const Piece p = ahead->piece;
+        const int h = p.h * a.step + member;
+        ta = chunk = p.t0;
+        ta_end = p.t1;
+        keys = p.keys;
+        const int page = page_of(chunk, p.seq);
+        page_next = page_of(chunk + 16, p.seq);
+        slot = slot_in(page, chunk);
+        my_code = codes.k + my_row * codes.tok + h * codes.head + my_chunk * 16;
+        my_scale = codes.sk + (lane & 15) * codes.s_tok + h * codes.s_head;
+    };
     auto ask = [&]() {
         if (rest_of_run && ta >= ta_end) {
             rest_of_run = next(ahead, pg, lengths, groups, lane);
-            if (rest_of_run) {
-                const Piece p = ahead->piece;
-                const int h = p.h * a.step + member;
-                ta = chunk = p.t0;
-                ta_end = p.t1;
-                keys = p.keys;
-                slot = slot_in(page_of(chunk, p.seq), chunk);
-                page_next = page_of(chunk + 16, p.seq);
-                my_code = codes.k + my_row * codes.tok + h * codes.head + my_chunk * 16;
-                my_scale = codes.sk + (lane & 15) * codes.s_tok + h * codes.s_head;
-            }
+            if (rest_of_run) begin_piece();
         }
         if (rest_of_run) {
             if (ta - chunk == 16) {
@@ -598,9 +618,12 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     auto read = [&]() {
         read_queries<D, DT, NT>(a.q + way->piece.seq * a.ld_q + (way->piece.h * a.step + member) * (int64_t)q_bytes, a.G, lane, raw);
     };
-    constexpr bool EARLY = NT == 1;   // else the registers are not there
-    bool some = next(way, pg, lengths, groups, lane);
+    constexpr bool EARLY = NT == 1 && DT != KVC_IN_F32;   // else the registers are not there
+    bool some = rest_of_run = next(ahead, pg, lengths, groups, lane);
+    for (int i = lane; i < (int)(sizeof(Way) / 4); i += 32) reinterpret_cast<int *>(way)[i] = reinterpret_cast<const int *>(ahead)[i];
+    __syncwarp();
     if (EARLY && some) read();
+    if (some) begin_piece();
     for (int i = 0; i < C::NS; ++i) ask();
 
     // sequences without keys have no unit in the list
@@ -694,8 +717,8 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
         if (p.t0 == 0 && (by_pair || !whole)) {
             owner = true;
             if (lane == 0) {
-                const unsigned long long end = run_from(run + 1) + (p.nt - p.t1);   // the pair's last unit, plus one
-                const int last = (int)div64(end * runs - 1, W);   // the run that holds it
+                // the run that holds the pair's last unit
+                const int last = whole ? 0 : (int)run_of(run_from(run + 1) + (p.nt - p.t1) - 1);
                 a.desc[by_pair ? h * pg.n_seq + p.seq : c] = make_int4(p.seq, h, whole ? 0 : last - (int)run + 1, c);
             }
         }
