@@ -14,7 +14,7 @@ namespace paged {
 
 using namespace ptx;
 
-constexpr int COMBINE_THREADS = 256;
+constexpr int COMBINE_THREADS = 256;   // of a join, unless said otherwise
 // A row's reference lies SHIFT_LOG2 below its greatest score, so that the numerators are 2^7 there (2^15 at most before the
 // reference is raised) and fp16 holds them down to 2^-31 of it.  With the reference at the score itself those below 2^-25
 // vanished from O, but not from the sum: long contexts lost them.
@@ -132,9 +132,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // each head, which is mostly the starting of CTAs.  The 96 sequences of 5 to 16,384 with a group for a head up to 0, 2, 8 and 32
 // partials: 82, 82, 79 and 79 us, in 16 heads to a group 136, 135, 125 and 125.
 constexpr int FEW_PARTS = 8;
-template <int D, int DT, bool MANY>
+template <int D, int DT, bool MANY, int THREADS, int B>   // B: partials that a group loads together
 __device__ __forceinline__ void join_pair(const Args &a, const int4 d) {
-    constexpr int LANES = D / 4, GROUPS = COMBINE_THREADS / LANES;
+    constexpr int LANES = D / 4, GROUPS = THREADS / LANES;
     const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
     // partials first, first + step, ... of a head
     auto join = [&](int head, int first, int step, float &m, float &l, float4 &acc) {
@@ -142,7 +142,6 @@ __device__ __forceinline__ void join_pair(const Args &a, const int4 d) {
         l = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
         // partial j lies with slot d.w + j step: its second place for the first (the pair begins there), else the first
-        constexpr int B = 4;
         for (int j0 = first; j0 < d.z; j0 += B * step) {
             float2 ml[B];
             float4 o[B];
@@ -218,15 +217,15 @@ __device__ __forceinline__ void join_pair(const Args &a, const int4 d) {
 
 
 // Joins blockIdx.x, blockIdx.x + gridDim.x, ... of n.
-template <int D, int DT, bool MANY>
-__global__ void __launch_bounds__(COMBINE_THREADS) combine_paged_kernel(const Args a, int n) {
+template <int D, int DT, bool MANY, int THREADS = COMBINE_THREADS, int B = 4>
+__global__ void __launch_bounds__(THREADS) combine_paged_kernel(const Args a, int n) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     for (int x = blockIdx.x; x < n; x += gridDim.x) {
         const int4 d = __ldcg(a.desc + x);
         if (d.z == 0) continue;
         if (x != (int)blockIdx.x) __syncthreads();   // the join before has been read
-        join_pair<D, DT, MANY>(a, d);
+        join_pair<D, DT, MANY, THREADS, B>(a, d);
     }
 }
 

@@ -741,14 +741,32 @@ int launch_t(const PagedView &pg, const Args &a, const Codes &codes, cudaStream_
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, decode_paged_q4_kernel<D, DT, NT>, pg, a, codes) != cudaSuccess) return KVC_ECUDA;
-    const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
-    const int joins = by_pair ? a.H_kv * pg.n_seq : a.n_slots;
-    cfg.gridDim = by_pair ? dim3(joins, a.G) : dim3(a.n_slots / WARPS);
+    // The join: warps' runs make four times as many partials as CTAs' would, and starting threads is most of what it costs.  A
+    // CTA gets as many threads as a pair will have partials for, if all CTAs then fit the GPU at once.  With 64, 128, 256
+    // and 512 threads, in us: the 96 sequences 53.5, 53.7, 55.7 and 61.9 (of 700 tokens 27.6, 28.5, 32.3 and 40.4), eight 15.7,
+    // 14.4, 13.8 and 14.2, one of 58,300 34.0, 28.4, 23.6 and 23.3 (22.4 with eight partials loaded together).  Joins by slot, 400
+    // sequences of 700: a CTA of 256 for each 82, for two 84, for four 95; of 128 for each 86.
+    const int joins = a.H_kv * pg.n_seq;
+    void (*join)(const Args, int) = combine_paged_kernel<D, DT, true>;
+    cfg.gridDim = dim3(a.n_slots);
     cfg.blockDim = dim3(COMBINE_THREADS);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, by_pair ? combine_paged_kernel<D, DT, false> : combine_paged_kernel<D, DT, true>, a, joins) !=
-        cudaSuccess)
-        return KVC_ECUDA;
+    const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
+    if (by_pair) {
+        const int parts = min(a.n_slots / joins, (pg.max_pages * pg.page_size - 1) / KT + 1) + 1;
+        auto fits = [&](int threads) {
+            return threads / (D / 4) <= parts && (int64_t)joins * a.G * threads <= 2048 * (int64_t)sm_count();
+        };
+        constexpr int MOST = 64;   // partials that 256 threads join as fast
+        const int threads = parts > MOST && fits(512) ? 512 : fits(256) ? 256 : fits(128) ? 128 : 64;
+        join = threads == 512   ? combine_paged_kernel<D, DT, false, 512, 8>
+               : threads == 256 ? combine_paged_kernel<D, DT, false, 256>
+               : threads == 128 ? combine_paged_kernel<D, DT, false, 128>
+                                : combine_paged_kernel<D, DT, false, 64>;
+        cfg.gridDim = dim3(joins, a.G);
+        cfg.blockDim = dim3(threads);
+    }
+    if (cudaLaunchKernelEx(&cfg, join, a, by_pair ? joins : a.n_slots) != cudaSuccess) return KVC_ECUDA;
     return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ECUDA;
 }
 
