@@ -23,11 +23,13 @@
 // instead of 67.  Copies are 16-byte asynchronous ones, waited for by the warp itself; no wait can fail to end.
 // TMA took 5 cycles for each row of 64 bytes, and 47 us where nothing was computed.
 //
-// Measured (40 query heads, 8 kv heads of 128, bf16; of the rate of a copy): 96 sequences of 5 to 16,384 tokens 58 us (3.6 TB/s,
-// 0.52; to fp16 59; the same from q8_0 79), in 16 heads to a group 90; 20 of 16,384 83 (0.67); one of 58,300 25 us (0.40); eight of about
-// 2,100 14.3; one of 64 8.6.  Without the copies the 96 take 52 us, without the products 47: the two hide each other in part.
-// A tile's products take a scheduler about 650 cycles: 42 matrix instructions, each 8 cycles of the tensor pipe and about four
-// in which nothing else issues, and 390 others.
+// Measured (40 query heads, 8 kv heads of 128, bf16, calls back to back in a graph; of the rate of a copy): 96 sequences of 5
+// to 16,384 tokens 53.6 us (3.8 TB/s, 0.56; to fp16 55.8; the same from q8_0 79), in 16 heads to a group 84; 20 of 16,384 78 (0.72);
+// one of 58,300 22.4 us (0.44); eight of about 2,100 13.8; one of 64 8.0.  Of the 53.6 the warps' runs take 43 on average and
+// 47.5 at most, the join and the launches 6; without the products all of it takes 45.  A tile takes a scheduler about 1,100
+// cycles, in which it issues 570 instructions: 42 matrix instructions, each 8 cycles of the tensor pipe and about four in which
+// nothing else issues, and 390 others for the products, 140 to ask for the next tile; three warps do not hide the rest of
+// the chain product - maximum - exponential - product.
 #include "decode_paged.cuh"
 
 namespace kvc {
@@ -38,8 +40,8 @@ using namespace paged;
 constexpr int KT = 32;              // keys per tile: two subtiles of 16, each within one page
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
-// What starting and ending a pair costs, in tiles.  With 2, 4 and 8, in us: the 96 sequences 59.5, 58 and 65 (an earlier
-// state), one of 58,300 24.7, 25.1 and 25.0.
+// What starting and ending a pair costs, in tiles.  With 1, 2, 3, 4 and 6, in us: the 96 sequences 62.4, 57.4, 53.7, 53.9 and 55.2,
+// 170 of up to 3,000 21.4, 21.1, 20.3, 20.0 and 20.5.
 constexpr int PIECE_COST = 4;
 // CTAs per SM: as many as the registers allow without spilling.  Two instead of three: the 96 sequences 57.5 us, in heads of
 // 64 48 instead of 39; four (128 registers) 64.
