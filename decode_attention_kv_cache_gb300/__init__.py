@@ -458,7 +458,16 @@ class PageTable:
         self.__dict__[name] = value
 
 
-class FreePages:
+class _Held:
+    """Attributes are set once: what a call reads holds their addresses, and one replaced would leave it freed memory."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError("%s of a %s cannot be replaced; its contents can" % (name, type(self).__name__))
+        self.__dict__[name] = value
+
+
+class FreePages(_Held):
     """The free pages of a pool of n_pages pages, for kv_pages_advance: ring (int32 [n_pages]), and state (int32 [3]: where
     the ring begins, how many pages it holds, how many were asked for and not there), on the device.  pages: those
     that are free at first (a sequence or int32 tensor of page numbers, each once); None: all of them, in order."""
@@ -672,7 +681,7 @@ def attn_packed(q, k, v, q_start, k_start=None, out=None, lse=None, scratch=None
 ROPE_STYLES = {"half": 0, "pairs": 1}
 
 
-class RopeTable:
+class RopeTable(_Held):
     """A rotation by position of the first `rot` values of each head: pairs (i, i + rot / 2) ("half") or (2 i, 2 i + 1)
     ("pairs"), pair i by position * base ** (-2 i / rot), or by position * inv_freq[i] where inv_freq (a sequence or
     tensor of rot / 2 frequencies in radians) is given.  The frequencies are kept as 64-bit fractions of a turn on

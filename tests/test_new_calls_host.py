@@ -172,3 +172,20 @@ def test_binding_refuses_tensors_it_cannot_pass(kvc):
         kvc.qk_norm_rope(x, x, torch.zeros(4, dtype=torch.int32), rope)      # not on a GPU
     with pytest.raises(ValueError):
         kvc.qk_norm_rope(x[0], x, torch.zeros(4, dtype=torch.int32), rope)
+
+
+def test_pools_of_4_bits_with_too_many_heads_for_decode(kvc):
+    b = ctypes.c_size_t()
+    for heads, want in ((65535, 0), (65536, kvc.KVC_EINVAL)):
+        d = kvc.make_desc(1, 16, heads, 64, "q4_0")
+        assert kvc.lib.kvc_paged_scratch_bytes(ctypes.byref(d), 1, heads, ctypes.byref(b)) == want
+
+
+def test_tensors_that_calls_hold_cannot_be_replaced(kvc):
+    free, rope = kvc.FreePages(4, device="cpu"), kvc.RopeTable(16, device="cpu")
+    for x, names in ((free, ("ring", "state", "n_pages", "c")), (rope, ("turns", "rot", "style"))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(x, name, getattr(x, name))
+    free.state[1] = 2
+    assert free.free() == (2, 0)
