@@ -373,6 +373,7 @@ int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_
     if (!pool_desc_ok(desc) || !bytes || n_seq < 0 || n_seq > 65535) return KVC_EINVAL;
     if (desc->head_dim != 64 && desc->head_dim != 128) return KVC_EINVAL;
     if (n_head_q <= 0 || n_head_q % desc->n_head_kv || n_head_q / desc->n_head_kv > 16) return KVC_EINVAL;
+    if (desc->type == KVC_Q4_0 && desc->n_head_kv > 65535) return KVC_EINVAL;   // distances between rows in 32 bits
     *bytes = paged_scratch_bytes(*desc, n_seq, n_head_q);
     return KVC_OK;
 }

@@ -436,9 +436,9 @@ int launch_all(Args p, cudaStream_t s) {
     p.heads = p.a.H_q + p.a.H_kv * (CT != NO_POOL ? 2 : 1);
     // Whole rows for a warp where there are enough of them to keep the SMs busy; else as many warps for a row as that takes.
     const int together = 32 >> p.lanes_log2, times = (p.heads + together - 1) / together;
-    const int want = (WARPS_PER_SM<CT> * sm_count() + p.a.n_rows - 1) / p.a.n_rows, parts = want < times ? want : times;
+    const int want = (int)(((int64_t)WARPS_PER_SM<CT> * sm_count() + p.a.n_rows - 1) / p.a.n_rows), parts = want < times ? want : times;
     p.span = (times + parts - 1) / parts * together;
-    const dim3 grid((p.a.n_rows + WARPS - 1) / WARPS, (p.heads + p.span - 1) / p.span);
+    const dim3 grid((unsigned)(((int64_t)p.a.n_rows + WARPS - 1) / WARPS), (p.heads + p.span - 1) / p.span);
     switch (p.a.dtype * 2 + p.a.style) {
         case KVC_IN_F32 * 2: return launch_t<KVC_IN_F32, KVC_ROPE_HALF, CT>(p, grid, s);
         case KVC_IN_F32 * 2 + 1: return launch_t<KVC_IN_F32, KVC_ROPE_PAIRS, CT>(p, grid, s);

@@ -471,7 +471,8 @@ int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_
  * greatest numerator times the greatest scale that the sequence has in that block of
  * 32 dimensions; scaled scores below -6e29 count as none.
  * out and lse overlap no
- * input.  head_dim 64 or 128, n_head_q / n_head_kv <= 16.  Errors as kv_paged_append, KVC_ENOSPC (scratch too small). */
+ * input.  head_dim 64 or 128, n_head_q / n_head_kv <= 16, in a q4_0 pool n_head_kv up
+ * to 65535.  Errors as kv_paged_append, KVC_ENOSPC (scratch too small). */
 int decode_attn_paged(const kvc_cache *pool, const kvc_pages *pages, int32_t layer, const void *q, int64_t ld_q,
                       int32_t dtype, int32_t n_head_q, void *out, float *lse, void *scratch, size_t scratch_bytes,
                       kvc_stream_t stream);
