@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from paged_util import TYPES, i32, inputs, starts
-from pool4_util import make_pool4, verify4
+from paged_util import check, check_lse
+from pool4_util import attend4, codes4, make_pool4, verify4
 
 pytestmark = pytest.mark.gpu
 
@@ -40,6 +41,33 @@ def test_ragged_batches(kvc, n_seq, hq):
     held[0] = 20000 if n_seq < 10 else 3000
     cache, pages, slots = make_pool4(kvc, held, 32, 2, 128, "layer_major", seed=n_seq, layers=1)
     verify4(kvc, cache, 0, pages, slots, inputs((n_seq, hq, 128), torch.bfloat16, 4))
+
+
+@pytest.mark.parametrize("n_seq,every,hkv,d", [(5000, 41, 2, 64), (65535, 997, 1, 128), (65535, 65534, 4, 64), (3000, 1, 1, 64)])
+def test_many_sequences_of_which_most_are_empty(kvc, n_seq, every, hkv, d):
+    cache, _, _ = make_pool4(kvc, [1024], 16, hkv, d, "layer_major", layers=1)
+    n_pages = cache.n_ctx // 16
+    g = torch.Generator(device="cuda").manual_seed(n_seq + every)
+    table = torch.randint(0, n_pages, (n_seq, 20), generator=g, device="cuda", dtype=torch.int32)   # shared, only read
+    lengths = torch.zeros(n_seq, dtype=torch.int32, device="cuda")
+    lengths[::every] = torch.randint(0, 40, lengths[::every].shape, generator=g, device="cuda", dtype=torch.int32)
+    lengths[n_seq - 1] = 320
+    lengths[n_seq // 2] = 319
+    pages = kvc.PageTable(table, lengths, 16)
+    q = inputs((n_seq, 3 * hkv, d), torch.float16, 5)
+    lse = torch.full((n_seq, 3 * hkv), 5.0, device="cuda")
+    out = kvc.decode_attn_paged(cache, 0, pages, q, lse=lse)
+    empty = lengths == 0
+    assert (out[empty] == 0).all() and (lse[empty] == -float("inf")).all()
+    some = torch.nonzero(~empty)[:, 0].tolist()
+    for i in some[:60] + some[-60:]:
+        n = int(lengths[i])
+        slots = (table[i].long()[:, None] * 16 + torch.arange(16, device="cuda")).flatten()[:n].tolist()
+        (k, dk), (v, dv) = (codes4(cache, 0, kv, slots) for kv in (0, 1))
+        o, l, b, lb = attend4(q[i], k * dk.repeat_interleave(32, -1), dk, v * dv.repeat_interleave(32, -1), dv)
+        check(out[i], o, b, "seq %d" % i)
+        check_lse(lse[i], l, lb, "seq %d" % i)
+    assert torch.equal(out, kvc.decode_attn_paged(cache, 0, pages, q))
 
 
 @pytest.mark.parametrize("d", [128, 64])
