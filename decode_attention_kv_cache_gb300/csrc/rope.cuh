@@ -7,8 +7,8 @@
 // A and B are the same for all heads of a row.  A warp takes a row, or some of its heads where there are few rows: it makes
 // the sines once, keeps A and B of its values in registers and goes through the heads with several loads in flight.  Only
 // bytes move: HBM bounds it, and for a few rows the chain position -> angle -> store.  What else costs is instructions: where
-// both of a pair lie in one lane, and two values share each multiplication (fma.f32x2), there are 40 for eight values, else
-// 90, a third of them to exchange and widen the other values.
+// both of a pair lie in one lane, and two values share each multiplication (fma.f32x2), a row of 48 heads takes a warp 2,300 (issue
+// slots 51% busy); elsewhere each lane exchanges and widens the other values as well.
 //
 // Measured (40 query and 8 kv heads of 128, bf16, of the rate of a copy): 10,041 rows 41.4 us (5.95 TB/s, 0.88; by exchange 52.8);
 // with keys and values stored, 12,711 rows on q8_0 pages 71.5 (0.70; by exchange 95.8), q4_0 64.0 (0.75; 82.4), f16 60.5 (0.89;
