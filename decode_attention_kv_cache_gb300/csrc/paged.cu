@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(THREADS)
                 }
             } else if constexpr (CT == KVC_Q8_0) {
                 uint32_t w[2];
-                const uint16_t scale = q8_0_quantize_quad(x, w);
+                const uint16_t scale = q8_0_quantize_quad<DT>(x, w);
                 if (slot >= 0) {
                     *reinterpret_cast<uint2 *>(static_cast<int8_t *>(kv ? p.vq : p.kq) + at) = make_uint2(w[0], w[1]);
                     if ((c & 31) == 0)

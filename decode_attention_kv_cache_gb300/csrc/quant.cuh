@@ -159,6 +159,13 @@ __device__ __forceinline__ void q8_0_exact2(float x0, float x1, uint64_t r2, uin
 // cheaper than one for each pair, and bf16 and fp16 inputs, whose quotients have few bits, meet ties in half of the
 // warps, so the exact codes come from q8_0_exact2 and not from divisions.  rcp.approx is within one unit
 // in the last place, so x * r is within 127 * (2^-23 + 2^-24) = 2.3e-5 of x / d.
+// bf16 and fp16 values (DT; p = 8 or 11 bits): 127 x / amax is a tie, or 2^-(p + 8) of itself or more away from one (127 x and
+// (k + 1/2) amax are multiples of a unit that large).  d is off by 2^-24 at most, 1 / d and its products by 2^-22, so quotients
+// made larger, or smaller, by 2^-20 round as they should where there is no tie.  At a tie (2 k + 1) amax = 254 x, and 127 is
+// prime: either it divides amax, d is exact, so is x / d, and it rounds away from zero: larger; or 2 k + 1 = 127, |x| = amax / 2,
+// and where the rounded quotient lies below 63.5 they have to be smaller: d is not exact then, so that the block has no other ties.
+// (All pairs of 8 and of 11 bits, at all distances of their exponents, agree with the division.)
+template <int DT>
 __device__ __forceinline__ uint16_t q8_0_quantize_quad(const float (&x)[8], uint32_t (&packed)[2]) {
     float m = ptx::fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2]));
     m = ptx::fmax3(m, fabsf(x[3]), fabsf(x[4]));
@@ -170,7 +177,14 @@ __device__ __forceinline__ uint16_t q8_0_quantize_quad(const float (&x)[8], uint
     packed[0] = packed[1] = 0u;
     if (d > 0.f && m <= 3.402823466e38f) {
         uint32_t q[8];   // the code is the low byte
-        if (d >= 1e-30f) {
+        if (DT != KVC_IN_F32 && d >= 1e-30f) {
+            float r;
+            asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+            // |x| = amax / 2: as in q8_0_exact2
+            r = fmaf(r, fmaf(-63.5f, d, 0.5f * m) >= d * -0x1p-19f ? 0x1p-20f : -0x1p-20f, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(fmaf(x[i], r, 12582912.f));
+        } else if (d >= 1e-30f) {
             float r;
             asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
             const uint64_t r2 = ptx::f2_pack(r, r), mz = ptx::f2_pack(-0.f, -0.f),

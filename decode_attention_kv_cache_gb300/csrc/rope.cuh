@@ -153,7 +153,7 @@ __device__ __forceinline__ void store_kv(const Args &p, bool value, bool some, i
         if (some) *reinterpret_cast<uint4 *>(codes + 2 * at) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
     } else if constexpr (CT == KVC_Q8_0) {
         uint32_t w2[2];
-        const uint16_t d = q8_0_quantize_quad(x, w2);
+        const uint16_t d = q8_0_quantize_quad<DT>(x, w2);
         if (some) {
             *reinterpret_cast<uint2 *>(codes + at) = make_uint2(w2[0], w2[1]);
             if ((e & 31) == 0) scales[sat] = d;
