@@ -5,11 +5,11 @@
 // x / d, d = fp16(-m/8), m the value of greatest magnitude), or rounded to
 // fp16.  read: x = d * q in float32 (exact: 11 and 8 significant bits), rounded once to the output type.
 // Both only move bytes: what bounds them is HBM, and for a few rows the latency of the dependent loads that
-// find a row's page (row_start, len, the table, then the data).  What bounds the q8_0 append of many rows is neither:
-// the quantiser's own arithmetic, about 200 instructions for eight values.
+// find a row's page (row_start, len, the table, then the data).  What bounds the q8_0 and q4_0 appends of many rows is neither:
+// instructions, 100 to 120 for eight 16-bit values with the look-ups, about 200 for float32 ones (quant.cuh).
 //
 // Measured (8 kv heads of 128, of the rate of a copy): 19,300 fp16 rows into an f16 cache 27.6 us (5.7 TB/s, 0.85);
-// 21,100 bf16 rows into a q8_0 cache 42.1 us (3.1 TB/s, 0.46; from float32 4.5 TB/s); 58,300 positions of a q8_0 cache
+// 20,465 bf16 rows into a q8_0 cache 34.8 us (3.7 TB/s, 0.54; from float32 50, 0.62); 58,300 positions of a q8_0 cache
 // read into bf16 56.7 us (6.5 TB/s, 0.95) and of an f16 cache 71.6 us (6.7 TB/s, 0.98); eight rows appended 2.0 us.
 // 20,465 bf16 rows into a q4_0 cache 32.5 us (3.4 TB/s, 0.50: 110 instructions for eight values, issue slots 65% busy), read back
 // into fp16 22.7 (4.9 TB/s, 0.72: loads of 8 bytes).  A warp for each row, all heads in turn, took 30.5 for the append, but 10.3
@@ -25,12 +25,12 @@
 namespace kvc {
 namespace {
 
-// Threads of a CTA, which waits for its look-ups as one: 256, 128 and 64 take 43.4, 42.1 and 42.6 us for the q8_0 append
-// above (54, 49 and 49 from float32), 56.6, 56.8 and 63.7 for the q8_0 read.
+// Threads of a CTA, which waits for its look-ups as one: 256, 128 and 64 take 37.6, 34.8 and 34.8 us for the q8_0 append
+// above (57, 50 and 50 from float32), 33.2, 32.2 and 32.6 for the q4_0 one, 56.6, 56.8 and 63.7 for the q8_0 read.
 constexpr int THREADS = 128;
 // Units that a thread takes where there are many.  Measured at the sizes above, with 1, 2 and 4 of them: a q8_0 append
-// 48.0, 42.1 and 42.6 us, an f16 append 27.7, 27.8 and 28.6; a read of a q8_0 cache, whose one load makes two stores'
-// worth of values, 56.7, 57.2 and 62.7; of an f16 cache 76.8, 71.6 and 71.8.  20,500 bf16 rows into a q4_0 cache 32.5, 32.1 and 33.4; read
+// 38.2, 34.8 and 36.0 us (20,465 rows of 4 heads of 64 20.3, 15.8 and 15.1), an f16 append 27.7, 27.8 and 28.6; a read of a q8_0 cache, whose one load makes two stores'
+// worth of values, 56.7, 57.2 and 62.7; of an f16 cache 76.8, 71.6 and 71.8.  A q4_0 append 32.6, 32.2 and 33.3, the read
 // back into fp16 26.1, 29.5 and 22.8.
 constexpr int APPEND_PASSES = 2;
 template <int CT>

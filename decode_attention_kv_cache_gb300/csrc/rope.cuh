@@ -11,9 +11,9 @@
 // slots 51% busy); elsewhere each lane exchanges and widens the other values as well.
 //
 // Measured (40 query and 8 kv heads of 128, bf16, of the rate of a copy): 10,041 rows 41.4 us (5.95 TB/s, 0.88; by exchange 52.8);
-// with keys and values stored, 12,711 rows on q8_0 pages 71.5 (0.70; by exchange 95.8), q4_0 64.0 (0.75; 82.4), f16 60.5 (0.89;
+// with keys and values stored, 12,711 rows on q8_0 pages 64.4 (0.78; by exchange 88), q4_0 64.0 (0.75; 82.4), f16 60.5 (0.89;
 // 75.0); 96 rows 3.6, 64 on f16 pages 4.3.  Five heads of a lane in flight (two of those that are stored) and 5 CTAs per SM; with
-// 2 heads and 6 CTAs 42.1, 79.0, 67.5 and 63.8; with 4 and 6 44.0, 77.1, 68.1 and 62.6.
+// 2 heads and 6 CTAs 42.1, 67.5 (q4_0) and 63.8 (f16); with 4 and 6 44.0, 68.1 and 62.6.
 //
 // Angles.  A pair's frequency is a 64-bit fixed-point fraction f of a turn for each position, so that position times f, modulo
 // 2^64, is the angle's fraction of a turn to 2^-33 whatever the position; its upper 32 bits go through sincospi.
