@@ -24,8 +24,8 @@
 // TMA took 5 cycles for each row of 64 bytes, and 47 us where nothing was computed.
 //
 // Measured (40 query heads, 8 kv heads of 128, bf16, calls back to back in a graph; of the rate of a copy): 96 sequences of 5
-// to 16,384 tokens 53.6 us (3.8 TB/s, 0.56; to fp16 55.8; the same from q8_0 79), in 16 heads to a group 84; 20 of 16,384 78 (0.72);
-// one of 58,300 22.4 us (0.44); eight of about 2,100 13.8; one of 64 8.0.  Of the 53.6 the warps' runs take 43 on average and
+// to 16,384 tokens 53.0 us (3.9 TB/s, 0.57; to fp16 54.7; the same from q8_0 79), in 16 heads to a group 82.6; 20 of 16,384 75
+// (0.74); one of 58,300 22.0 us (0.45); eight of about 2,100 13.7; one of 64 8.1.  Of the 53 the warps' runs take 43 on average and
 // 47.5 at most, the join and the launches 6; without the products all of it takes 45.  A tile takes a scheduler about 1,100
 // cycles, in which it issues 570 instructions: 42 matrix instructions, each 8 cycles of the tensor pipe and about four in which
 // nothing else issues, and 390 others for the products, 140 to ask for the next tile; three warps do not hide the rest of
@@ -72,8 +72,8 @@ struct Cfg {
 template <int D>
 __device__ __forceinline__ int swizzle(int row, int c) { return D == 128 ? c ^ ((row >> 1) & 3) : c ^ ((row >> 2) & 1); }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, int bytes) {   // 16, or 0: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void copy_scales(uint32_t dst, const uint8_t *src, bool valid) {
@@ -592,12 +592,12 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
             const int sl[2] = {__shfl_sync(0xffffffffu, slot, 2 * (ta - chunk)), __shfl_sync(0xffffffffu, slot, 2 * (ta - chunk) + 1)};
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                if (sl[u] < 0) continue;   // what the stage held stays: nothing of it counts
-                const uint8_t *k = my_code + (uint64_t)(uint32_t)sl[u] * codes.tok, *v = k + codes.v_from_k;
+                const int bytes = sl[u] < 0 ? 0 : 16;
+                const uint8_t *k = my_code + (uint64_t)(uint32_t)max(sl[u], 0) * codes.tok, *v = k + codes.v_from_k;
 #pragma unroll
                 for (int r = 0; r < 16; r += C::RPL) {
-                    copy16(place + (16 * u + r) * C::ROW, k);
-                    copy16(place + (16 * u + r) * C::ROW + C::TILE, v);
+                    copy16(place + (16 * u + r) * C::ROW, k, bytes);
+                    copy16(place + (16 * u + r) * C::ROW + C::TILE, v, bytes);
                     k += codes.rows;
                     v += codes.rows;
                 }

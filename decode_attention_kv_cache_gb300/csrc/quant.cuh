@@ -156,9 +156,8 @@ __device__ __forceinline__ void q8_0_exact2(float x0, float x1, uint64_t r2, uin
 
 // A block spread over four neighbouring lanes, eight values each: this lane's codes and the block's scale.  All four
 // lanes take part.  The same codes as above; with eight values to a thread one look at all of them for a near tie is
-// cheaper than one for each pair, and bf16 and fp16 inputs, whose quotients have few bits, meet ties in half of the
-// warps, so the exact codes come from q8_0_exact2 and not from divisions.  rcp.approx is within one unit
-// in the last place, so x * r is within 127 * (2^-23 + 2^-24) = 2.3e-5 of x / d.
+// cheaper than one for each pair, and the exact codes come from q8_0_exact2 and not from divisions.  rcp.approx is within one
+// unit in the last place, so x * r is within 127 * (2^-23 + 2^-24) = 2.3e-5 of x / d.
 // bf16 and fp16 values (DT; p = 8 or 11 bits): 127 x / amax is a tie, or 2^-(p + 8) of itself or more away from one (127 x and
 // (k + 1/2) amax are multiples of a unit that large).  d is off by 2^-24 at most, 1 / d and its products by 2^-22, so quotients
 // made larger, or smaller, by 2^-20 round as they should where there is no tie.  At a tie (2 k + 1) amax = 254 x, and 127 is
