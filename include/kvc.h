@@ -538,7 +538,8 @@ typedef struct {
  * A page belongs to one sequence: a table that shares pages between sequences is not
  * one for this call.  The call writes pages->table and pages->len.  max_pages limits a
  * sequence's table as for the other calls (positions behind it are holes).  n_rows == 0
- * still advances; n_seq == 0 is a no-op.  Results do not depend on timing.
+ * still advances; n_seq == 0 is a no-op.  Results do not depend on timing.  Calls that
+ * share a table, its lengths or a ring must not overlap on the GPU.
  * Errors: KVC_EINVAL (null or 4-byte-unaligned pointers, shapes). */
 int kv_pages_advance(const kvc_pages *pages, const kvc_free_pages *free_pages, const int32_t *rows, int32_t *row_start,
                      int32_t n_rows, int32_t *positions, int32_t *slots, kvc_stream_t stream);
