@@ -238,3 +238,29 @@ def test_a_query_of_nan_is_nan(kvc):
     want[0, 3] = want[1, 8] = float("nan")
     assert torch.equal(torch.isnan(out), torch.isnan(want))
     assert torch.equal(out.nan_to_num(0.0), want.nan_to_num(0.0))
+
+
+@pytest.mark.parametrize("layout", ["head_major", "layer_major"])
+def test_tokens_stored_just_before(kvc, layout):
+    # a step's scales lie in sectors that the step before read
+    held = [33, 700, 5, 16]
+    cache, pages, _ = make_pool4(kvc, held, 16, 4, 128, layout, extra_pages=12, max_pages=50)
+    used = {int(p) for i, h in enumerate(held) for p in pages.table[i, :-(-h // 16)].tolist()}
+    spare = [p for p in range(cache.n_ctx // 16) if p not in used]
+    for i, h in enumerate(held):          # pages for 40 more tokens of each
+        n = -(-h // 16)
+        pages.table[i, n:n + 3] = i32(spare[3 * i:3 * i + 3])
+    q = inputs((40, 4, 12, 128), torch.bfloat16, 1)
+    kv = inputs((40, 2, 4, 4, 128), torch.bfloat16, 2)
+    one, scratch, outs = starts([1] * 4), kvc.paged_scratch(cache, 4, 12), []
+    start = pages.lengths.clone()
+    for t in range(40):
+        pages.lengths.add_(1)
+        kvc.kv_paged_append(cache, 0, pages, one, kv[t, 0], kv[t, 1])
+        outs.append(kvc.decode_attn_paged(cache, 0, pages, q[t], scratch=scratch))
+    torch.cuda.synchronize()
+    for t in range(40):
+        pages.lengths.copy_(start + t + 1)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[t], kvc.decode_attn_paged(cache, 0, pages, q[t])), t
+        torch.cuda.synchronize()
