@@ -169,3 +169,35 @@ def test_truncate_clears_the_tail(kvc):
         t[:, :, 21:] = 0
     got = [cache.codes(0), cache.scales(0), cache.codes(1), cache.scales(1)]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype,bits", [("bf16", 8), ("f16", 11)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_every_pair_of_mantissas(kvc, dtype, bits, sign):
+    # a block's greatest and a value, at every distance of their exponents at which the code is not zero, in exact arithmetic
+    m = torch.arange(2 ** (bits - 1), 2 ** bits, device="cuda", dtype=torch.float64)
+    values = torch.cat([m / 2 ** s for s in range(6)])
+    values = torch.cat([values, values[:-values.numel() % 31]]).view(-1, 31)
+    for first in range(0, m.numel(), 128):
+        a = m[first:first + 128]
+        x = torch.minimum(values[None], a[:, None, None])
+        x = torch.cat([sign * a[:, None, None].expand(-1, x.shape[1], 1), x], -1)
+        x[..., 2::2] *= -1
+        x = x.reshape(-1, 32)
+        rows = -(-x.shape[0] // 8)
+        x = torch.cat([x, x[:rows * 8 - x.shape[0]]])
+        t = x.view(rows, 2, 128).to(TYPES[dtype])
+        assert torch.equal(t.double(), x.view(rows, 2, 128))
+        n_pages = -(-rows // 16)
+        cache = kvc.KVCache(1, n_pages * 16, 2, 128, "q4_0", "layer_major")
+        pages = kvc.PageTable(torch.arange(n_pages, dtype=torch.int32, device="cuda")[None], i32([rows]), 16)
+        kvc.kv_paged_append(cache, 0, pages, starts([rows]), t, t)
+        k, v = kvc.kv_paged_read(cache, 0, pages, starts([rows]), rows, dtype=torch.float32)
+        lo, hi = x.amin(-1, keepdim=True), x.amax(-1, keepdim=True)
+        g = torch.where(-lo >= hi, lo, hi)                     # of greatest magnitude, of +m and -m the negative one
+        num, den = 16 * x.abs() + g.abs(), 2 * g.abs()         # floor(num / den): the magnitude, ties away from zero
+        q = torch.floor(num / den)
+        q = q - (q * den > num).double() + ((q + 1) * den <= num).double()
+        q = torch.minimum(q * torch.sign(x) * -torch.sign(g), torch.full_like(q, 7.0))
+        want = (q * (g / -8).half().double()).float().view(rows, 2, 128)
+        assert torch.equal(k, want) and torch.equal(v, want)
