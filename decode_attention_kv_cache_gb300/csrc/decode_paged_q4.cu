@@ -5,11 +5,15 @@
 //   - An fp16 number is linear in its bits as long as the exponent's are zero, and matrix products take such numbers exactly:
 //     a nibble n (code + 8) in the low byte of a half is the subnormal n 2^-24 or n 2^-20 where it lies.  An AND with
 //     0x000F000F or 0x00F000F0 makes two operands, and no subtraction or conversion is left to do for each value.  In the first
-//     product the queries of the lower nibbles are 16 times as large.  The second takes the whole bytes, n + 16 n',
-//     beside the high nibbles (one operation less), and the two sums are told apart at the end.
+//     product the queries of the lower nibbles are 16 times as large, in the second the sums of the upper ones are.
 //   - The 8 in each nibble is taken care of outside of the loops over values: the scores begin at -8 times the product of
 //     the key's scales with the sums of the queries over each block (one small product, the sums in two fp16 parts), and a
-//     product with eights in place of the values is subtracted from O at the end.
+//     product with eights in place of the values is subtracted from O after every FOLD tiles.  Left in O, the eights would be most
+//     of it, and the truncations of float32 sums count against all of it: at 16,384 keys in a warp's run, V's scales of
+//     one sign, the error came to 2e-3 of the output with whole bytes n + 16 n' summed to the end; it is 5e-5 now (model:
+//     N / 16 2^-24 8 (32 FOLD / 2) against 4.6 sqrt(N)), where fp16 numerators cost 2e-4.
+//     (The 96 sequences below, bf16 and fp16, in us: summed to the end 52.9, 54.6; FOLD 1 55.3, 57.2; 4 54.2, 58.3; 8 54.0, 57.9;
+//     signed codes as operands, 1024 + n less 1032, 57.9 and 60.0.)
 // V's scales are multiplied into the numerators: in float32, before their one rounding, or where the output is bf16, whose
 // rounding is eight times as coarse, in fp16, after one.  So that numerators times scales stay in fp16's range, a warp divides
 // the scales of each block by a power of two above the greatest that it has met (inv: its inverse).
@@ -47,6 +51,7 @@ constexpr int PIECE_COST = 4;
 // 64 48 instead of 39; four (128 registers) 64.
 constexpr int ctas_per_sm(int NT) { return NT == 1 ? 3 : 2; }
 constexpr int MAX_NS = 6;
+constexpr int FOLD = 4;             // tiles between two subtractions of the eights from O: a power of two
 constexpr float NONE = -1e30f;      // the reference of a head that has met no key
 
 template <int D, int DT, int NT>
@@ -186,7 +191,7 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
                                        float (&ob)[C::NB][NT][4], float (&m)[NT][2], float (&l)[NT][2],
                                        __half2 (&inv)[C::NB / 2]) {
     constexpr int U = C::U, NB = C::NB;
-    constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, BYTES = 0x00FF00FFu;
+    constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     const uint32_t vt = kt + C::TILE, sc = vt + C::TILE;
     const int g = lane >> 2, t4 = lane & 3;
@@ -326,9 +331,8 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const uint32_t va = vw[u][b >> 1][2 * (b & 1)], vb = vw[u][b >> 1][2 * (b & 1) + 1];
-            const uint32_t va8 = __byte_perm(va, 0u, 0x4341), vb8 = __byte_perm(vb, 0u, 0x4341);
-            const uint32_t A[4] = {va & BYTES, va & HI, vb & BYTES, vb & HI}, B[4] = {va8, va8 & HI, vb8, vb8 & HI};
+            const uint32_t va = vw[u][b >> 1][2 * (b & 1)], vb = vw[u][b >> 1][2 * (b & 1) + 1], va8 = va >> 8, vb8 = vb >> 8;
+            const uint32_t A[4] = {va & LO, va & HI, vb & LO, vb & HI}, B[4] = {va8 & LO, va8 & HI, vb8 & LO, vb8 & HI};
             const uint32_t E[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
             const __half2 da = __hmul2(dv[u][0][b >> 1], inv[b >> 1]), db = __hmul2(dv[u][1][b >> 1], inv[b >> 1]);
 #pragma unroll
@@ -351,6 +355,24 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
             }
         }
     }
+}
+
+// The eights leave O: low nibbles' sums (rows 0 to 7 of a tile) have them once, upper ones' 16 times.
+template <int NT, class C>
+__device__ __forceinline__ void fold_eights(float (&o)[C::MT][NT][4], float (&ob)[C::NB][NT][4]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int b = 0; b < C::NB; ++b) {
+#pragma unroll
+            for (int i = 2 * b; i < 2 * b + 2; ++i) {
+                o[i][nt][0] -= ob[b][nt][0];
+                o[i][nt][1] -= ob[b][nt][1];
+                o[i][nt][2] = fmaf(ob[b][nt][0], -16.f, o[i][nt][2]);
+                o[i][nt][3] = fmaf(ob[b][nt][1], -16.f, o[i][nt][3]);
+            }
+            ob[b][nt][0] = ob[b][nt][1] = ob[b][nt][2] = ob[b][nt][3] = 0.f;
+        }
 }
 
 // Where the layer's codes and scales lie; distances in bytes.
@@ -665,12 +687,14 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
                 const uint32_t bits = C::U == 2 ? e : e >> (16 * u) & 0xFFFFu;
                 if (bits != 0) attend<D, NT, C>(kt, 16 * u, bits, lane, qf, eights, worth, o, ob, m, l, inv);
             }
+            if (left % FOLD == 0) fold_eights<NT, C>(o, ob);
             __syncwarp();   // before the stage is written again
             stage_out = stage_out + 1 == C::NS ? 0 : stage_out + 1;
             ask();
         }
 
         // ---- the piece is done
+        fold_eights<NT, C>(o, ob);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -696,10 +720,8 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
                 float x[8];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    // rows 0 to 7 of a tile have the bytes, rows 8 to 15 their high nibbles
                     const float (&r)[4] = o[2 * b + (n >> 1)][nt];
-                    const float e0 = (n & 1 ? r[2] * 0.0625f : r[0] - r[2]) - ob[b][nt][0];
-                    const float e1 = (n & 1 ? r[3] * 0.0625f : r[1] - r[3]) - ob[b][nt][1];
+                    const float e0 = n & 1 ? r[2] * 0.0625f : r[0], e1 = n & 1 ? r[3] * 0.0625f : r[1];
                     const float got = __shfl_xor_sync(0xffffffffu, g & 1 ? e0 : e1, 4);
                     x[2 * n] = (g & 1 ? got : e0) * w;
                     x[2 * n + 1] = (g & 1 ? e1 : got) * w;
