@@ -15,8 +15,12 @@
 //     (The 96 sequences below, bf16 and fp16, in us: summed to the end 52.9, 54.6; FOLD 1 55.3, 57.2; 4 54.2, 58.3; 8 54.0, 57.9;
 //     signed codes as operands, 1024 + n less 1032, 57.9 and 60.0.)
 // V's scales are multiplied into the numerators: in float32, before their one rounding, or where the output is bf16, whose
-// rounding is eight times as coarse, in fp16, after one.  So that numerators times scales stay in fp16's range, a warp divides
-// the scales of each block by a power of two above the greatest that it has met (inv: its inverse).
+// rounding is eight times as coarse, in fp16, after one.  All of these stay in fp16's range: a head's numerators are 2^7 to
+// 2^11 at its greatest score, and a warp takes the scales of each block times a power of two (factor) that brings the greatest that
+// it has met to 2^3 or more, below 2^4 (or any to 2^15 times itself).  So numerators count down to 2^-31 of the greatest, and scales to
+// 2^-28, with all of their bits to 2^-17.  (Scales of at most one beside numerators of up to 2^15 lost bits from 2^-14 on and
+// vanished at 2^-25, whatever their keys weighed.  Numerators of up to 2^8 beside scales of up to 2^7: one of eight heads passes its
+// limit so often that the 96 sequences below take 2 us more; products in float32 for bf16 outputs too: the same.)
 //
 // Work split.  The list of decode_attn_paged, in tiles of 32 keys, is cut into runs for single *warps*: a warp looks up its
 // pages, keeps its own ring of tiles in flight and attends over them with all heads of the group and all dimensions; warps
@@ -53,6 +57,7 @@ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 3 : 2; }
 constexpr int MAX_NS = 6;
 constexpr int FOLD = 4;             // tiles between two subtractions of the eights from O: a power of two
 constexpr float NONE = -1e30f;      // the reference of a head that has met no key
+constexpr float RAISE_LOG2 = SHIFT_LOG2 + 4.0f;   // a numerator above 2^this raises its head's reference
 
 template <int D, int DT, int NT>
 struct Cfg {
@@ -88,10 +93,10 @@ __device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.comm
 template <int N>
 __device__ __forceinline__ void wait_groups_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The inverse of the power of two above |d|, 2^14 at most.
-__device__ __forceinline__ __half inverse_above(__half d) {
-    const int e = min(__half_as_ushort(d) >> 10 & 31, 30);
-    return __ushort_as_half((unsigned short)(e < 29 ? (29 - e) << 10 : 0x200 >> (e - 29)));
+// The power of two that brings |d| to 2^3 or more, below 2^4; 2^15 at most.
+__device__ __forceinline__ __half factor_of(__half d) {
+    const int e = min(__half_as_ushort(d) >> 10 & 31, 30);   // |d| < 2^(e - 14)
+    return __ushort_as_half((unsigned short)(min(33 - e, 30) << 10));
 }
 
 // A lane's values of the group's queries, eight of each block, as they lie in memory.
@@ -189,7 +194,7 @@ template <int D, int NT, class C>
 __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, int lane, const uint32_t (&qf)[D / 16][NT][2],
                                        const uint32_t (&eights)[NT], const float (&worth)[NT][2], float (&o)[C::MT][NT][4],
                                        float (&ob)[C::NB][NT][4], float (&m)[NT][2], float (&l)[NT][2],
-                                       __half2 (&inv)[C::NB / 2]) {
+                                       __half2 (&factor)[C::NB / 2]) {
     constexpr int U = C::U, NB = C::NB;
     constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
@@ -262,13 +267,13 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
             }
     }
     bool above = false;
-    __half2 d_here[NB / 2];   // the greatest scales of V; is one above its block's power of two?
+    __half2 d_here[NB / 2];   // the greatest scales of V; is one too large for its block's factor?
 #pragma unroll
     for (int i = 0; i < NB / 2; ++i) {
         d_here[i] = __hmax2(__habs2(dv[0][0][i]), __habs2(dv[0][1][i]));
 #pragma unroll
         for (int u = 1; u < U; ++u) d_here[i] = __hmax2(d_here[i], __hmax2(__habs2(dv[u][0][i]), __habs2(dv[u][1][i])));
-        above |= !__hble2(__hmul2(d_here[i], inv[i]), __float2half2_rn(1.f));
+        above |= !__hble2(__hmul2(d_here[i], factor[i]), __float2half2_rn(16.f));
     }
     float top[NT][2];
 #pragma unroll
@@ -278,7 +283,7 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
             top[nt][e] = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
 #pragma unroll
             for (int u = 1; u < U; ++u) top[nt][e] = fmax3(top[nt][e], s[u][nt][e], s[u][nt][e + 2]);
-            above |= fmaf(top[nt][e], worth[nt][e], -m[nt][e]) > RESCALE_LOG2;
+            above |= fmaf(top[nt][e], worth[nt][e], -m[nt][e]) > RAISE_LOG2;
         }
     if (__any_sync(0xffffffffu, above)) {
         float fb[NB];
@@ -287,9 +292,9 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1)
                 d_here[i] = __hmax2(d_here[i], as_half2(__shfl_xor_sync(0xffffffffu, as_u32(d_here[i]), x)));
-            const float2 was = __half22float2(inv[i]);
-            inv[i] = __hmin2(inv[i], __halves2half2(inverse_above(__low2half(d_here[i])), inverse_above(__high2half(d_here[i]))));
-            const float2 is = __half22float2(inv[i]);
+            const float2 was = __half22float2(factor[i]);
+            factor[i] = __hmin2(factor[i], __halves2half2(factor_of(__low2half(d_here[i])), factor_of(__high2half(d_here[i]))));
+            const float2 is = __half22float2(factor[i]);
             fb[2 * i] = is.x / was.x;
             fb[2 * i + 1] = is.y / was.y;
         }
@@ -302,7 +307,8 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                const float m_new = fmaxf(m[nt][e], fmaf(x, worth[nt][e], -SHIFT_LOG2));
+                // only heads that are above it: what a head's numerators are does not depend on other heads
+                const float m_new = fmaf(x, worth[nt][e], -m[nt][e]) > RAISE_LOG2 ? fmaf(x, worth[nt][e], -SHIFT_LOG2) : m[nt][e];
                 f[e] = ex2(m[nt][e] - m_new);
                 m[nt][e] = m_new;
                 l[nt][e] *= f[e];
@@ -334,7 +340,7 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
             const uint32_t va = vw[u][b >> 1][2 * (b & 1)], vb = vw[u][b >> 1][2 * (b & 1) + 1], va8 = va >> 8, vb8 = vb >> 8;
             const uint32_t A[4] = {va & LO, va & HI, vb & LO, vb & HI}, B[4] = {va8 & LO, va8 & HI, vb8 & LO, vb8 & HI};
             const uint32_t E[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
-            const __half2 da = __hmul2(dv[u][0][b >> 1], inv[b >> 1]), db = __hmul2(dv[u][1][b >> 1], inv[b >> 1]);
+            const __half2 da = __hmul2(dv[u][0][b >> 1], factor[b >> 1]), db = __hmul2(dv[u][1][b >> 1], factor[b >> 1]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 uint32_t p0, p1;
@@ -666,9 +672,9 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
         float worth[NT][2];
         make_queries<D, DT, NT>(raw, a.scale_log2, lane, qf, eights, worth);
         float o[C::MT][NT][4], ob[C::NB][NT][4], m[NT][2], l[NT][2];
-        __half2 inv[C::NB / 2];
+        __half2 factor[C::NB / 2];
 #pragma unroll
-        for (int i = 0; i < C::NB / 2; ++i) inv[i] = __float2half2_rn(0x1p14f);
+        for (int i = 0; i < C::NB / 2; ++i) factor[i] = __float2half2_rn(0x1p15f);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = NONE;
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
 #pragma unroll 1
             for (int u = 0; u < 2; u += C::U) {
                 const uint32_t bits = C::U == 2 ? e : e >> (16 * u) & 0xFFFFu;
-                if (bits != 0) attend<D, NT, C>(kt, 16 * u, bits, lane, qf, eights, worth, o, ob, m, l, inv);
+                if (bits != 0) attend<D, NT, C>(kt, 16 * u, bits, lane, qf, eights, worth, o, ob, m, l, factor);
             }
             if (left % FOLD == 0) fold_eights<NT, C>(o, ob);
             __syncwarp();   // before the stage is written again
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
             const float by = whole ? (L > 0.f || L != L ? 1.f / L : 0.f) : 1.f;
 #pragma unroll
             for (int b = 0; b < C::NB; ++b) {
-                const float w = 0x1p24f / __half2float(b & 1 ? __high2half(inv[b >> 1]) : __low2half(inv[b >> 1])) * by;
+                const float w = 0x1p24f / __half2float(b & 1 ? __high2half(factor[b >> 1]) : __low2half(factor[b >> 1])) * by;
                 float x[8];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {

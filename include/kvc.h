@@ -467,9 +467,11 @@ int kvc_paged_scratch_bytes(const kvc_desc *desc, int32_t n_seq, int32_t n_head_
  * of the greatest.  In a q4_0 pool the codes enter the products exactly; q is
  * first scaled by a power of two for each head and keeps 11 bits of every value
  * down to 2^-24 of the head's greatest, which may be 2^-100 to 2^100 in magnitude;
- * numerators enter times V's scales, as fp16, and count down to 2^-31 of the
- * greatest numerator times the greatest scale that the sequence has in that block of
- * 32 dimensions; scaled scores below -6e29 count as none.
+ * numerators enter times V's scales, as fp16: numerators count down to 2^-31 of the
+ * greatest, V's scales down to 2^-28 of the greatest that the sequence has in that block
+ * of 32 dimensions, with all of their bits down to 2^-17.  Sums are taken over codes plus 8, the
+ * eights apart, 128 keys at a time, so that a key leaves a rounding of at most 2^-10 of
+ * its weight times its scale, whatever its code is; scaled scores below -6e29 count as none.
  * out and lse overlap no
  * input.  head_dim 64 or 128, n_head_q / n_head_kv <= 16, in a q4_0 pool n_head_kv up
  * to 65535.  Errors as kv_paged_append, KVC_ENOSPC (scratch too small). */
