@@ -250,11 +250,17 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
                 float acc[4];
                 mma_16816_to(acc, A, qf[2 * b][nt][0], qf[2 * b][nt][1], zero);
                 mma_16816_to(acc, B, qf[2 * b + 1][nt][0], qf[2 * b + 1][nt][1], acc);
-                s[u][nt][0] = fmaf(acc[0], ca, s[u][nt][0]);
-                s[u][nt][1] = fmaf(acc[1], ca, s[u][nt][1]);
-                s[u][nt][2] = fmaf(acc[2], cb, s[u][nt][2]);
-                s[u][nt][3] = fmaf(acc[3], cb, s[u][nt][3]);
+                f2_unpack(f2_fma(f2_pack(acc[0], acc[1]), f2_pack(ca, ca), f2_pack(s[u][nt][0], s[u][nt][1])), s[u][nt][0], s[u][nt][1]);
+                f2_unpack(f2_fma(f2_pack(acc[2], acc[3]), f2_pack(cb, cb), f2_pack(s[u][nt][2], s[u][nt][3])), s[u][nt][2], s[u][nt][3]);
             }
+        }
+        // In powers of two, and rounded before the reference is taken off, as the reference was: fused, the greatest score less its
+        // reference would be off by the reference's rounding, which passes any exponent where scores pass 2^27.
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint64_t w2 = f2_pack(worth[nt][0], worth[nt][1]);
+            f2_unpack(f2_mul(f2_pack(s[u][nt][0], s[u][nt][1]), w2), s[u][nt][0], s[u][nt][1]);
+            f2_unpack(f2_mul(f2_pack(s[u][nt][2], s[u][nt][3]), w2), s[u][nt][2], s[u][nt][3]);
         }
     }
     if (exists != C::ALL) {   // the last subtile of a sequence, or one of a hole
@@ -283,7 +289,7 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
             top[nt][e] = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
 #pragma unroll
             for (int u = 1; u < U; ++u) top[nt][e] = fmax3(top[nt][e], s[u][nt][e], s[u][nt][e + 2]);
-            above |= fmaf(top[nt][e], worth[nt][e], -m[nt][e]) > RAISE_LOG2;
+            above |= top[nt][e] - m[nt][e] > RAISE_LOG2;
         }
     if (__any_sync(0xffffffffu, above)) {
         float fb[NB];
@@ -308,7 +314,7 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                 // only heads that are above it: what a head's numerators are does not depend on other heads
-                const float m_new = fmaf(x, worth[nt][e], -m[nt][e]) > RAISE_LOG2 ? fmaf(x, worth[nt][e], -SHIFT_LOG2) : m[nt][e];
+                const float m_new = x - m[nt][e] > RAISE_LOG2 ? x - SHIFT_LOG2 : m[nt][e];
                 f[e] = ex2(m[nt][e] - m_new);
                 m[nt][e] = m_new;
                 l[nt][e] *= f[e];
@@ -327,7 +333,12 @@ __device__ __forceinline__ void attend(uint32_t kt, int row0, uint32_t exists, i
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[u][nt][i] = ex2(fmaf(s[u][nt][i], worth[nt][i & 1], -m[nt][i & 1]));
+            for (int i = 0; i < 4; i += 2) {
+                float x0, x1;
+                f2_unpack(f2_add(f2_pack(s[u][nt][i], s[u][nt][i + 1]), f2_pack(-m[nt][0], -m[nt][1])), x0, x1);
+                s[u][nt][i] = ex2(x0);
+                s[u][nt][i + 1] = ex2(x1);
+            }
             l[nt][0] += s[u][nt][0] + s[u][nt][2];
             l[nt][1] += s[u][nt][1] + s[u][nt][3];
             if constexpr (!C::FINE) {
