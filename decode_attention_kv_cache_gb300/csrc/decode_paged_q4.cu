@@ -787,13 +787,13 @@ int launch_t(const PagedView &pg, const Args &a, const Codes &codes, cudaStream_
     // and 512 threads, in us: the 96 sequences 53.5, 53.7, 55.7 and 61.9 (of 700 tokens 27.6, 28.5, 32.3 and 40.4), eight 15.7,
     // 14.4, 13.8 and 14.2, one of 58,300 34.0, 28.4, 23.6 and 23.3 (22.4 with eight partials loaded together).  Joins by slot, 400
     // sequences of 700: a CTA of 256 for each 82, for two 84, for four 95; of 128 for each 86.
-    const int joins = a.H_kv * pg.n_seq;
     void (*join)(const Args, int) = combine_paged_kernel<D, DT, true>;
     cfg.gridDim = dim3(a.n_slots);
     cfg.blockDim = dim3(COMBINE_THREADS);
     cfg.dynamicSmemBytes = 0;
-    const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
-    if (by_pair) {
+    int joins = a.n_slots;
+    if (join_by_pair(a.H_kv, pg.n_seq, a.n_slots)) {
+        joins = a.H_kv * pg.n_seq;   // n_slots at most
         const int parts = min(a.n_slots / joins, (pg.max_pages * pg.page_size - 1) / KT + 1) + 1;
         auto fits = [&](int threads) {
             return threads / (D / 4) <= parts && (int64_t)joins * a.G * threads <= 2048 * (int64_t)sm_count();
@@ -807,7 +807,7 @@ int launch_t(const PagedView &pg, const Args &a, const Codes &codes, cudaStream_
         cfg.gridDim = dim3(joins, a.G);
         cfg.blockDim = dim3(threads);
     }
-    if (cudaLaunchKernelEx(&cfg, join, a, by_pair ? joins : a.n_slots) != cudaSuccess) return KVC_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, join, a, joins) != cudaSuccess) return KVC_ECUDA;
     return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ECUDA;
 }
 
