@@ -51,13 +51,30 @@ constexpr int THREADS = 32 * WARPS;
 // What starting and ending a pair costs, in tiles.  With 1, 2, 3, 4 and 6, in us: the 96 sequences 62.4, 57.4, 53.7, 53.9 and 55.2,
 // 170 of up to 3,000 21.4, 21.1, 20.3, 20.0 and 20.5.
 constexpr int PIECE_COST = 4;
-// CTAs per SM: as many as the registers allow without spilling.  Two instead of three: the 96 sequences 57.5 us, in heads of
-// 64 48 instead of 39; four (128 registers) 64.
+// CTAs per SM: as many as the registers allow (three 168, of which those for heads of 128 and 16-bit queries take all; nothing
+// spills).  Two instead of three: the 96 sequences 57.5 us, in heads of 64 48 instead of 39; four (128 registers) 64.
 constexpr int ctas_per_sm(int NT) { return NT == 1 ? 3 : 2; }
 constexpr int MAX_NS = 6;
 constexpr int FOLD = 4;             // tiles between two subtractions of the eights from O: a power of two
 constexpr float NONE = -1e30f;      // the reference of a head that has met no key
 constexpr float RAISE_LOG2 = SHIFT_LOG2 + 4.0f;   // a numerator above 2^this raises its head's reference
+
+// A warp's way through its run of the list: groups of kv heads, in each the sequences, in each its units.  Kept in shared
+// memory, where the loop over tiles leaves it alone: registers decide how many warps there are.
+struct Way {
+    unsigned long long left;
+    int seq, group, x, base;     // x: units of the current pair that lie before this run
+    int held[32];                // lengths from sequence `base` on
+    Piece piece;                 // h: the group
+};
+
+// A CTA's shared memory besides its warps' tiles.
+struct Small {
+    unsigned long long warp_units[WARPS], units_before[THREADS];
+    Way ways[WARPS][2];
+    int lengths[THREADS];        // of all sequences, where they are so few
+};
+constexpr int SMALL = (sizeof(Small) + 127) / 128 * 128;
 
 template <int D, int DT, int NT>
 struct Cfg {
@@ -70,10 +87,11 @@ struct Cfg {
     static constexpr int SC = KT * NB * 2;                  // a tile's scales
     static constexpr int STAGE = 2 * TILE + 2 * SC;         // keeps the tiles on the swizzle's boundaries
     static constexpr int MT = D / 16;                       // 16-row tiles of O^T
-    // of 228 KB, 1 KB for each CTA besides what it asks for, and 2 KB for what is small
-    static constexpr int FIT = (228 * 1024 / ctas_per_sm(NT) - 1024 - 2048) / (WARPS * STAGE);
+    // of 228 KB, 1 KB for each CTA besides what it asks for; for heads of 128 three CTAs leave nothing over
+    static constexpr int FIT = (228 * 1024 / ctas_per_sm(NT) - 1024 - SMALL) / (WARPS * STAGE);
     static constexpr int NS = FIT < MAX_NS ? FIT : MAX_NS;
     static constexpr int SMEM = WARPS * NS * STAGE;
+    static_assert(ctas_per_sm(NT) * (SMEM + SMALL + 1024) <= 228 * 1024, "the CTAs that slots are counted by have to fit an SM");
     static constexpr int CHUNKS = ROW / 16, RPL = 32 / CHUNKS;   // 16-byte chunks of a row; rows that a warp's copy takes
     static_assert(NS >= 2, "shared memory plan");
 };
@@ -399,15 +417,6 @@ struct Codes {
     uint32_t tok, rows, s_tok;   // rows: of the rows that a warp copies together
 };
 
-// A warp's way through its run of the list: groups of kv heads, in each the sequences, in each its units.  Kept in shared
-// memory, where the loop over tiles leaves it alone: registers decide how many warps there are.
-struct Way {
-    unsigned long long left;
-    int seq, group, x, base;     // x: units of the current pair that lie before this run
-    int held[32];                // lengths from sequence `base` on
-    Piece piece;                 // h: the group
-};
-
 // keys_of, from the CTA's copy of the lengths where it has them all.
 __device__ __forceinline__ int keys_at(const PagedView &pg, const int *all, int i) {
     return pg.n_seq <= THREADS ? all[i] : keys_of(pg, i);
@@ -489,9 +498,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     decode_paged_q4_kernel(const PagedView pg, const Args a, const Codes codes) {
     using C = Cfg<D, DT, NT>;
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ unsigned long long warp_units[WARPS], units_before[THREADS];
-    __shared__ Way ways[WARPS][2];
-    __shared__ int lengths[THREADS];   // of all sequences, where they are so few
+    __shared__ Small small;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     const int groups = a.H_kv / a.step;
     const int c = blockIdx.x * WARPS + warp, member = warp % a.step;   // my slot, my head of a group
     const unsigned run = c / a.step;
-    Way *ahead = &ways[warp][0], *way = &ways[warp][1];
+    Way *ahead = &small.ways[warp][0], *way = &small.ways[warp][1];
     // each thread takes `per` sequences: the units before its own, in its warp
     const int per = (pg.n_seq + THREADS - 1) / THREADS;
     {
@@ -509,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
         for (int i = i0; i < i1; ++i) {
             const int keys = keys_of(pg, i);
             mine += units_of<KT, PIECE_COST>(keys);
-            if (per == 1) lengths[i] = keys;
+            if (per == 1) small.lengths[i] = keys;
         }
         unsigned long long sum = mine;
 #pragma unroll
@@ -517,13 +524,13 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
             const unsigned long long up = __shfl_up_sync(0xffffffffu, sum, x);
             if (lane >= x) sum += up;
         }
-        if (lane == 31) warp_units[warp] = sum;
-        units_before[threadIdx.x] = sum - mine;
+        if (lane == 31) small.warp_units[warp] = sum;
+        small.units_before[threadIdx.x] = sum - mine;
     }
     __syncthreads();
     unsigned long long total = 0;   // a group's units
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) total += warp_units[w];
+    for (int w = 0; w < WARPS; ++w) total += small.warp_units[w];
     // The list's W units in runs: each of them has `each` units, the first `more` one more.
     const unsigned long long W = total * groups;
     const unsigned runs = (unsigned)min((unsigned long long)(a.n_slots / a.step), W);
@@ -549,12 +556,12 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
         unsigned long long before = 0, at = 0;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            const int n = __popc(__ballot_sync(0xffffffffu, before + units_before[32 * w + lane] <= u));
+            const int n = __popc(__ballot_sync(0xffffffffu, before + small.units_before[32 * w + lane] <= u));
             if (n > 0) {
                 t = 32 * w + n - 1;
-                at = before + units_before[t];
+                at = before + small.units_before[t];
             }
-            before += warp_units[w];
+            before += small.warp_units[w];
         }
         u -= at;
         int seq = t * per;
@@ -577,9 +584,9 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
                 seq += n;
                 break;
             }
-        start(ahead, pg, lengths, min(seq, pg.n_seq - 1), group, (int)u, left, lane);
+        start(ahead, pg, small.lengths, min(seq, pg.n_seq - 1), group, (int)u, left, lane);
     } else {
-        start(ahead, pg, lengths, 0, 0, 0, 0, lane);
+        start(ahead, pg, small.lengths, 0, 0, 0, 0, lane);
     }
     const bool by_pair = join_by_pair(a.H_kv, pg.n_seq, a.n_slots);
     const int g = lane >> 2, t4 = lane & 3;
@@ -618,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
     };
     auto ask = [&]() {
         if (rest_of_run && ta >= ta_end) {
-            rest_of_run = next(ahead, pg, lengths, groups, lane);
+            rest_of_run = next(ahead, pg, small.lengths, groups, lane);
             if (rest_of_run) begin_piece();
         }
         if (rest_of_run) {
@@ -660,7 +667,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
         read_queries<D, DT, NT>(a.q + way->piece.seq * a.ld_q + (way->piece.h * a.step + member) * (int64_t)q_bytes, a.G, lane, raw);
     };
     constexpr bool EARLY = NT == 1 && DT != KVC_IN_F32;   // else the registers are not there
-    bool some = rest_of_run = next(ahead, pg, lengths, groups, lane);
+    bool some = rest_of_run = next(ahead, pg, small.lengths, groups, lane);
     for (int i = lane; i < (int)(sizeof(Way) / 4); i += 32) reinterpret_cast<int *>(way)[i] = reinterpret_cast<const int *>(ahead)[i];
     __syncwarp();
     if (EARLY && some) read();
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
             for (int e = threadIdx.x; e < a.H_kv; e += THREADS) a.desc[e * pg.n_seq + i] = make_int4(0, 0, 0, 0);
     }
 
-    for (bool first = true; some; some = next(way, pg, lengths, groups, lane), first = false) {
+    for (bool first = true; some; some = next(way, pg, small.lengths, groups, lane), first = false) {
         if (!EARLY || !first) read();
         uint32_t qf[D / 16][NT][2], eights[NT];
         float worth[NT][2];
