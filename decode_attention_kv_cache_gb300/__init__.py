@@ -684,8 +684,9 @@ ROPE_STYLES = {"half": 0, "pairs": 1}
 class RopeTable(_Held):
     """A rotation by position of the first `rot` values of each head: pairs (i, i + rot / 2) ("half") or (2 i, 2 i + 1)
     ("pairs"), pair i by position * base ** (-2 i / rot), or by position * inv_freq[i] where inv_freq (a sequence or
-    tensor of rot / 2 frequencies in radians) is given.  The frequencies are kept as 64-bit fractions of a turn on
-    `device`: angles are exact to about 2^-32 of a turn at any position.  rot = 0: no rotation."""
+    tensor of rot / 2 frequencies in radians) is given.  The frequencies, as float64, are kept as 64-bit fractions of a
+    turn on `device`: angles are exact to 2^-32 of a turn at any position, and rounded to float32 beside the nearest
+    quarter of a turn (2^-28 of a turn at most).  rot = 0: no rotation."""
 
     def __init__(self, rot, base=10000.0, style="half", inv_freq=None, device="cuda"):
         if rot < 0 or rot % 2 or style not in ROPE_STYLES:

@@ -16,7 +16,9 @@
 // 2 heads and 6 CTAs 42.1, 67.5 (q4_0) and 63.8 (f16); with 4 and 6 44.0, 68.1 and 62.6.
 //
 // Angles.  A pair's frequency is a 64-bit fixed-point fraction f of a turn for each position, so that position times f, modulo
-// 2^64, is the angle's fraction of a turn to 2^-33 whatever the position; its upper 32 bits go through sincospi.
+// 2^64, is the angle's fraction of a turn whatever the position; its upper 32 bits are used.  The nearest quarter of a turn is taken
+// off them as integers, and what is left, an eighth of a turn at most, is rounded to float32 (2^-28 of a turn) for sincospi.  (The
+// whole fraction as a float32 was off by up to 2^-26 of a turn, and sines near half a turn by as much.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -131,8 +133,14 @@ __device__ __forceinline__ void turn(const RopeArgs &a, int pos, int lane, float
     for (int pair = lane; pair < a.D >> 1; pair += 32) {
         float s = 0.f, c = 1.f;
         if (pair < a.n_pairs) {
-            const long long t = (long long)(a.turns[pair] * (unsigned long long)(long long)pos);
-            sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
+            const unsigned t = (unsigned)((a.turns[pair] * (unsigned long long)(long long)pos) >> 32);
+            const unsigned quarter = (t + 0x20000000u) >> 30;
+            float y, x;
+            sincospif((float)(int)(t - (quarter << 30)) * 0x1p-31f, &y, &x);
+            c = quarter & 1 ? y : x;
+            s = quarter & 1 ? x : y;
+            if (quarter == 1 || quarter == 2) c = -c;
+            if (quarter >= 2) s = -s;
         }
         turned[pair] = make_float2(c, s);
     }

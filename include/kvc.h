@@ -551,8 +551,9 @@ int kv_pages_advance(const kvc_pages *pages, const kvc_free_pages *free_pages, c
  * Pair i is values (i, i + n_pairs) (KVC_ROPE_HALF; n_pairs a multiple of 8) or
  * (2 i, 2 i + 1) (KVC_ROPE_PAIRS).  turns (device): each pair's frequency in turns,
  * frequency / (2 pi) modulo 1, as a fraction of 2^64 rounded to an integer, so that
- * angles are exact to about 2^-32 of a turn at any position.  n_pairs 0: no
- * rotation (turns may be null). */
+ * angles are exact to 2^-32 of a turn, and half of 2^-64 for each position, at any
+ * position; beside the nearest quarter of a turn they are then rounded to float32
+ * (2^-28 of a turn at most).  n_pairs 0: no rotation (turns may be null). */
 typedef struct {
     const uint64_t *turns; /* device [n_pairs], 8-byte aligned */
     int32_t n_pairs;       /* 0 .. head_dim / 2 */
