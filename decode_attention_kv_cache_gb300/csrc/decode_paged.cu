@@ -401,12 +401,17 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
                             if (kp + 8 >= count) s[nt][2] = s[nt][3] = -INFINITY;
                         }
                     }
+                    // In powers of two, and rounded before the reference is taken off, as the reference was: fused, the greatest score
+                    // less its reference would be off by the reference's rounding, which passes any exponent where scores pass 2^27.
+                    const uint64_t scale2 = f2_pack(a.scale_log2, a.scale_log2);
                     bool above = false;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        f2_unpack(f2_mul(f2_pack(s[nt][0], s[nt][1]), scale2), s[nt][0], s[nt][1]);
+                        f2_unpack(f2_mul(f2_pack(s[nt][2], s[nt][3]), scale2), s[nt][2], s[nt][3]);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            above |= fmaxf(s[nt][e], s[nt][e + 2]) * a.scale_log2 > m[nt][e] + RESCALE_LOG2;
+                        for (int e = 0; e < 2; ++e) above |= fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + RESCALE_LOG2;
+                    }
                     if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                                const float m_new = fmaxf(m[nt][e], x * a.scale_log2 - SHIFT_LOG2);
+                                const float m_new = fmaxf(m[nt][e], x - SHIFT_LOG2);
                                 f[e] = m[nt][e] == m_new ? 1.f : ex2(m[nt][e] - m_new);
                                 m[nt][e] = m_new;
                                 l[nt][e] *= f[e];
@@ -435,7 +440,11 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm(Q8, NT))
                         // a reference of -infinity (no score above it yet): the numerators are zero, or NaN where a score is
                         const float ref[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0], m[nt][1] == -INFINITY ? 0.f : m[nt][1]};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) e[i] = ex2(fmaf(s[nt][i], a.scale_log2, -ref[i & 1]));
+                        for (int i = 0; i < 4; i += 2) {
+                            f2_unpack(f2_add(f2_pack(s[nt][i], s[nt][i + 1]), f2_pack(-ref[0], -ref[1])), e[i], e[i + 1]);
+                            e[i] = ex2(e[i]);
+                            e[i + 1] = ex2(e[i + 1]);
+                        }
                         l[nt][0] += e[0] + e[2];
                         l[nt][1] += e[1] + e[3];
                         const uint32_t p0 = pack_half2(e[0], e[1]), p1 = pack_half2(e[2], e[3]);
