@@ -67,20 +67,20 @@ def prefill_flops(w, chunks=None):
 # Entries: kernel -> {"sources": {file: sha16}, workload: (bytes per call, what was captured)}.
 TRAFFIC = {
     # the step's 29 prefill_step calls (the front kernel, the attention, the split merge), mean per call
-    "prefill": {"sources": {"prefill.cu": "76d9e5f11862e4bd", "quant.cuh": "c3633f9beb4a3793"},
-                "q8_0_58k": (415272713, "mean per call over the 29 prefill_step calls of one step (all three kernels)")},
-    "append_chunk": {"sources": {"append.cu": "2302d1cd16863358", "quant.cuh": "c3633f9beb4a3793"},
-                     "q8_0_58k": (8413773, "one 2048-token chunk append (writes still in L2 at the launch end)")},
-    "append_prompt": {"sources": {"append.cu": "2302d1cd16863358", "quant.cuh": "c3633f9beb4a3793"},
-                      "q8_0_58k": (330950528, "the 58,300-token prompt in one append")},
+    "prefill": {"sources": {"prefill.cu": "76d9e5f11862e4bd", "quant.cuh": "305575756d2d97bc"},
+                "q8_0_58k": (416026147, "mean per call over the 29 prefill_step calls of one step (all three kernels)")},
+    "append_chunk": {"sources": {"append.cu": "2302d1cd16863358", "quant.cuh": "305575756d2d97bc"},
+                     "q8_0_58k": (8414413, "one 2048-token chunk append (writes still in L2 at the launch end)")},
+    "append_prompt": {"sources": {"append.cu": "2302d1cd16863358", "quant.cuh": "305575756d2d97bc"},
+                      "q8_0_58k": (330893312, "the 58,300-token prompt in one append")},
     "decode_attn": {"sources": {"decode.cu": "d280bfd9f3fbd2ec"},
-                    "q8_0_58k": (128019610, "split pass + combine at position 58,555")},
-    "decode_step": {"sources": {"decode.cu": "d280bfd9f3fbd2ec", "quant.cuh": "c3633f9beb4a3793"},
-                    "q8_0_58k": (128064487, "split pass storing the token + combine at position 58,555")},
+                    "q8_0_58k": (128076928, "split pass + combine at position 58,555")},
+    "decode_step": {"sources": {"decode.cu": "d280bfd9f3fbd2ec", "quant.cuh": "305575756d2d97bc"},
+                    "q8_0_58k": (128033510, "split pass storing the token + combine at position 58,555")},
     "state_pack": {"sources": {"state.cu": "0b844f534c53c1b8"},
-                   "q8_0_58k": (201835392, "pack of 58,556 tokens (the kernel writes the header)")},
+                   "q8_0_58k": (201824230, "pack of 58,556 tokens (the kernel writes the header)")},
     "state_unpack": {"sources": {"state.cu": "0b844f534c53c1b8"},
-                     "q8_0_58k": (202343910, "unpack of 58,556 tokens")},
+                     "q8_0_58k": (202373965, "unpack of 58,556 tokens")},
 }
 
 
