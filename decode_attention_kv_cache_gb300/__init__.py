@@ -691,6 +691,8 @@ class RopeTable(_Held):
     def __init__(self, rot, base=10000.0, style="half", inv_freq=None, device="cuda"):
         if rot < 0 or rot % 2 or style not in ROPE_STYLES:
             raise ValueError('rot must be even and style "half" or "pairs"')
+        if inv_freq is None and not 0 < base < math.inf:
+            raise ValueError("base must be positive and finite")
         n = rot // 2
         if inv_freq is None:
             freq = [float(base) ** (-2.0 * i / rot) for i in range(n)]
