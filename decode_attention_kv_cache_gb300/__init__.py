@@ -686,7 +686,8 @@ class RopeTable(_Held):
     ("pairs"), pair i by position * base ** (-2 i / rot), or by position * inv_freq[i] where inv_freq (a sequence or
     tensor of rot / 2 frequencies in radians) is given.  The frequencies, as float64, are kept as 64-bit fractions of a
     turn on `device`: angles are exact to 2^-32 of a turn at any position, and rounded to float32 beside the nearest
-    quarter of a turn (2^-28 of a turn at most).  rot = 0: no rotation."""
+    quarter of a turn (2^-28 of a turn at most).  rot = 0: no rotation.  The calls take "half" with rot a multiple of 16.
+    Make it once for a model and keep it: making one works the frequencies out on the host and copies them."""
 
     def __init__(self, rot, base=10000.0, style="half", inv_freq=None, device="cuda"):
         if rot < 0 or rot % 2 or style not in ROPE_STYLES:

@@ -9,11 +9,11 @@
 //   - The 8 in each nibble is taken care of outside of the loops over values: the scores begin at -8 times the product of
 //     the key's scales with the sums of the queries over each block (one small product, the sums in two fp16 parts), and a
 //     product with eights in place of the values is subtracted from O after every FOLD tiles.  Left in O, the eights would be most
-//     of it, and the truncations of float32 sums count against all of it: at 16,384 keys in a warp's run, V's scales of
-//     one sign, the error came to 2e-3 of the output with whole bytes n + 16 n' summed to the end; it is 5e-5 now (model:
-//     N / 16 2^-24 8 (32 FOLD / 2) against 4.6 sqrt(N)), where fp16 numerators cost 2e-4.
-//     (The 96 sequences below, bf16 and fp16, in us: summed to the end 52.9, 54.6; FOLD 1 55.3, 57.2; 4 54.2, 58.3; 8 54.0, 57.9;
-//     signed codes as operands, 1024 + n less 1032, 57.9 and 60.0.)
+//     of it, and float32 sums of matrix products, which cut toward zero, count against all of it: with whole bytes n + 16 n' summed to
+//     the end of a run of 16,384 keys, V's scales of one sign, float32 outputs were off by 2.1e-3 of their rms (65,536 keys
+//     4.4e-3; scales of either sign 3.4e-4 and 6.5e-4).  They are off by 1.7e-5 and 6.6e-5, and by 2.0e-4 and 2.1e-4, which is
+//     fp16 numerators'.  It takes 1.2 us of the 96 sequences below in bf16 (FOLD 1, 4 and 8: 55.3, 54.2 and 54.0 us; signed codes as
+//     operands, 1024 + n less 1032: 57.9), 4 of the 82 in 16 heads to a group.
 // V's scales are multiplied into the numerators: in float32, before their one rounding, or where the output is bf16, whose
 // rounding is eight times as coarse, in fp16, after one.  All of these stay in fp16's range: a head's numerators are 2^7 to
 // 2^11 at its greatest score, and a warp takes the scales of each block times a power of two (factor) that brings the greatest that
@@ -32,12 +32,12 @@
 // TMA took 5 cycles for each row of 64 bytes, and 47 us where nothing was computed.
 //
 // Measured (40 query heads, 8 kv heads of 128, bf16, calls back to back in a graph; of the rate of a copy): 96 sequences of 5
-// to 16,384 tokens 53.0 us (3.9 TB/s, 0.57; to fp16 54.7; the same from q8_0 79), in 16 heads to a group 82.6; 20 of 16,384 75
-// (0.74); one of 58,300 22.0 us (0.45); eight of about 2,100 13.7; one of 64 8.1.  Of the 53 the warps' runs take 43 on average and
-// 47.5 at most, the join and the launches 6; without the products all of it takes 45.  A tile takes a scheduler about 1,100
-// cycles, in which it issues 570 instructions: 42 matrix instructions, each 8 cycles of the tensor pipe and about four in which
-// nothing else issues, and 390 others for the products, 140 to ask for the next tile; three warps do not hide the rest of
-// the chain product - maximum - exponential - product.
+// to 16,384 tokens 54.3 us (3.8 TB/s, 0.56; to fp16 56.3, float32 56.9; the same from q8_0 82), in 16 heads to a group 87.4; 20 of
+// 16,384 78 (0.71), 96 of them 345 (0.77); one of 58,300 22.7 us (0.44); eight of about 2,100 14.0; one of 64 8.0.  Where the 96 took
+// 53, before the eights were folded, the warps' runs took 43 on average and 47.5 at most, the join and the launches 6; without
+// the products all of it took 45.  A tile took a scheduler about 1,100 cycles, in which it issued 570 instructions: 42 matrix
+// instructions, each 8 cycles of the tensor pipe and about four in which nothing else issues, and 390 others for the products,
+// 140 to ask for the next tile; three warps do not hide the rest of the chain product - maximum - exponential - product.
 #include "decode_paged.cuh"
 
 namespace kvc {

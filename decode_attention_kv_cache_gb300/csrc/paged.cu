@@ -11,9 +11,10 @@
 // Measured (8 kv heads of 128, of the rate of a copy): 19,300 fp16 rows into an f16 cache 27.6 us (5.7 TB/s, 0.85);
 // 20,465 bf16 rows into a q8_0 cache 34.8 us (3.7 TB/s, 0.54; from float32 50, 0.62); 58,300 positions of a q8_0 cache
 // read into bf16 56.7 us (6.5 TB/s, 0.95) and of an f16 cache 71.6 us (6.7 TB/s, 0.98); eight rows appended 2.0 us.
-// 20,465 bf16 rows into a q4_0 cache 32.5 us (3.4 TB/s, 0.50: 110 instructions for eight values, issue slots 65% busy), read back
-// into fp16 22.7 (4.9 TB/s, 0.72: loads of 8 bytes).  A warp for each row, all heads in turn, took 30.5 for the append, but 10.3
-// instead of 9.9 for 5,000 rows and 19.5 instead of 15.6 for 4 heads of 64; fp16 arithmetic for fp16 outputs left the read at 22.6.
+// 20,465 bf16 rows into a q4_0 cache 32.5 us (3.4 TB/s, 0.50: 110 instructions for eight values, issue slots 65% busy; from float32
+// 49, 0.57), read back into fp16 22.7 to 24.1 (4.6 TB/s, 0.66 to 0.70: loads of 8 bytes; into float32 36, 0.78).  A warp for each
+// row, all heads in turn, took 30.5 for the append, but 10.3 instead of 9.9 for 5,000 rows and 19.5 instead of 15.6 for 4 heads of
+// 64; fp16 arithmetic for fp16 outputs left the read at 22.6.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

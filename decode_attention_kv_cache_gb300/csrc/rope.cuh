@@ -8,12 +8,13 @@
 // the sines once, keeps A and B of its values in registers and goes through the heads with several loads in flight.  Only
 // bytes move: HBM bounds it, and for a few rows the chain position -> angle -> store.  What else costs is instructions: where
 // both of a pair lie in one lane, and two values share each multiplication (fma.f32x2), a row of 48 heads takes a warp 2,300 (issue
-// slots 51% busy); elsewhere each lane exchanges and widens the other values as well.
+// slots 51% busy); heads that rotate in part, in halves, and heads of 32, 96 and the like have a kernel in which each lane
+// exchanges and widens the other values as well.
 //
-// Measured (40 query and 8 kv heads of 128, bf16, of the rate of a copy): 10,041 rows 41.4 us (5.95 TB/s, 0.88; by exchange 52.8);
-// with keys and values stored, 12,711 rows on q8_0 pages 64.4 (0.78; by exchange 88), q4_0 64.0 (0.75; 82.4), f16 60.5 (0.89;
-// 75.0); 96 rows 3.6, 64 on f16 pages 4.3.  Five heads of a lane in flight (two of those that are stored) and 5 CTAs per SM; with
-// 2 heads and 6 CTAs 42.1, 67.5 (q4_0) and 63.8 (f16); with 4 and 6 44.0, 68.1 and 62.6.
+// Measured (40 query and 8 kv heads of 128, bf16, of the rate of a copy): 10,041 rows 41.8 us (5.9 TB/s, 0.87); with keys and
+// values stored, 12,711 rows on q8_0 pages 64.6 (0.77), q4_0 64.3 (0.75), f16 60.6 (0.88); 96 rows 3.6, 64 on f16 pages 4.3.  With 64
+// of the 128 rotated in halves, by exchange, 52.0 (0.70), 80.6, 81.1 and 74.0.  Five heads of a lane in flight (two of those that are
+// stored) and 5 CTAs per SM; with 2 heads and 6 CTAs 42.1, 67.5 (q4_0) and 63.8 (f16); with 4 and 6 44.0, 68.1 and 62.6.
 //
 // Angles.  A pair's frequency is a 64-bit fixed-point fraction f of a turn for each position, so that position times f, modulo
 // 2^64, is the angle's fraction of a turn whatever the position; its upper 32 bits are used.  The nearest quarter of a turn is taken

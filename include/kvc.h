@@ -59,7 +59,9 @@
  *             from zero), all codes and d zero for an all-zero block.  The stored
  *             value is d * q.  A block's 16 bytes are four little-endian 32-bit
  *             words; value i of a word's eight lies, as q + 8, in the four bits from
- *             bit 16 (i % 2) + 4 (i / 2).  The calls on pages take this type
+ *             bit 16 (i % 2) + 4 (i / 2).  (llama.cpp's type of this name is another format:
+ *             it rounds halves up, takes the first of +m and -m and packs otherwise.)
+ *             The calls on pages take this type
  *             (kv_paged_*, decode_attn_paged, qk_norm_rope_append), and
  *             kvc_cache_bytes, kvc_cache_init and kv_cache_truncate; every other
  *             call refuses it (KVC_EINVAL).
